@@ -15,6 +15,7 @@
 #include <string>
 
 #include "fa8.h"
+#include "fa8_host.h"
 #include "fa8_launch.h"
 
 // Device status word of the library (timeouts, out-of-range block-table entries),
@@ -85,6 +86,14 @@ std::atomic<unsigned long long> g_timeout_ns{2000000000ull};
 std::atomic<unsigned long long *> g_trace{nullptr};  // pipeline trace buffer (FA8_TRACE builds)
 std::atomic<bool> g_decode_kernel{true};             // few-rows shapes go to decode_kernel
 
+std::mutex g_mu;
+fa8::host::DeviceState g_dev[64];
+
+}  // namespace
+
+namespace fa8 {
+namespace host {
+
 fa8_status fail(fa8_status s, const char *fmt, ...) {
     char buf[512];
     va_list ap;
@@ -99,15 +108,9 @@ fa8_status cuda_fail(cudaError_t e, const char *what) {
     return fail(FA8_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-// ---------------------------------------------------------------- per-device state
-struct DeviceState {
-    bool ready = false;
-    int sm_count = 0;
-    unsigned int *status = nullptr;
-};
-std::mutex g_mu;
-DeviceState g_dev[64];
+void clear_error() { g_last_error.clear(); }
 
+// ---------------------------------------------------------------- per-device state
 fa8_status device_state(DeviceState **out) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -127,6 +130,136 @@ fa8_status device_state(DeviceState **out) {
     *out = &d;
     return FA8_SUCCESS;
 }
+
+// ---------------------------------------------------------------- argument checks
+bool supported_dims(int d, int dv) {
+    return (d == 64 && dv == 64) || (d == 96 && dv == 96) || (d == 128 && dv == 128) || (d == 192 && dv == 128) ||
+           (d == 192 && dv == 192) || (d == 256 && dv == 256);
+}
+
+fa8_status check_int_vec(const fa8_tensor *t, const char *name, long long n) {
+    if (t->dtype != FA8_DTYPE_I32) return fail(FA8_ERR_INVALID_ARG, "%s must be int32", name);
+    if (t->ndim != 1 || t->shape[0] != n || (n > 1 && t->stride[0] != 1))
+        return fail(FA8_ERR_INVALID_ARG, "%s must be a contiguous 1-D tensor of %lld entries", name, n);
+    if (!t->data) return fail(FA8_ERR_INVALID_ARG, "%s has a null data pointer", name);
+    return FA8_SUCCESS;
+}
+
+// Q/K/V payload: last dim contiguous, other strides multiples of 16 bytes, 16-byte base.
+fa8_status check_payload(const fa8_tensor *t, const char *name) {
+    if (t->ndim < 3 || t->ndim > 4) return fail(FA8_ERR_INVALID_ARG, "%s must have 3 or 4 dims", name);
+    if (t->stride[t->ndim - 1] != 1) return fail(FA8_ERR_INVALID_ARG, "%s: last dim must be contiguous", name);
+    for (int i = 0; i < t->ndim - 1; ++i) {
+        if (t->shape[i] < 0) return fail(FA8_ERR_INVALID_ARG, "%s: negative extent", name);
+        if (t->stride[i] <= 0 || t->stride[i] % 16 != 0)
+            return fail(FA8_ERR_INVALID_ARG, "%s: stride[%d]=%lld must be a positive multiple of 16 bytes", name, i,
+                        (long long)t->stride[i]);
+    }
+    if (t->shape[t->ndim - 1] < 0) return fail(FA8_ERR_INVALID_ARG, "%s: negative extent", name);
+    if (!aligned16(t->data)) return fail(FA8_ERR_INVALID_ARG, "%s: data must be 16-byte aligned", name);
+    return FA8_SUCCESS;
+}
+
+fa8_status check_descale(const fa8_tensor *t, const char *name, int B, int Hkv, const float **ptr, long long *sb,
+                         long long *sh) {
+    *ptr = nullptr;
+    *sb = *sh = 0;
+    if (!t) return FA8_SUCCESS;
+    if (t->dtype != FA8_DTYPE_F32) return fail(FA8_ERR_INVALID_ARG, "%s must be fp32", name);
+    if (!t->data) return fail(FA8_ERR_INVALID_ARG, "%s has a null data pointer", name);
+    if (t->ndim == 0) {
+    } else if (t->ndim == 2 && t->shape[0] == B && t->shape[1] == Hkv) {
+        *sb = t->stride[0];
+        *sh = t->stride[1];
+    } else {
+        return fail(FA8_ERR_INVALID_ARG, "%s must be 0-d or (batch=%d, kv_heads=%d)", name, B, Hkv);
+    }
+    *ptr = static_cast<const float *>(t->data);
+    return FA8_SUCCESS;
+}
+
+fa8_status check_table(const fa8_tensor *cu_k, const fa8_tensor *bt, int page_size, int B, Table *out) {
+    if (!cu_k) return fail(FA8_ERR_INVALID_ARG, "paged K/V needs cu_seqlens_k for the per-request key counts");
+    if (!bt) return fail(FA8_ERR_INVALID_ARG, "paged K/V needs a block_table");
+    if (bt->dtype != FA8_DTYPE_I32 || bt->ndim != 2) return fail(FA8_ERR_INVALID_ARG, "block_table must be a 2-D int32 tensor");
+    if (bt->shape[0] != B) return fail(FA8_ERR_INVALID_ARG, "block_table rows (%lld) != batch (%d)", (long long)bt->shape[0], B);
+    if (bt->shape[1] < 1 || bt->shape[1] > 0x7fffffffLL || (bt->shape[1] > 1 && bt->stride[1] != 1) || bt->stride[0] < 0)
+        return fail(FA8_ERR_INVALID_ARG, "block_table rows must be contiguous (stride(1) == 1)");
+    if (!bt->data) return fail(FA8_ERR_INVALID_ARG, "block_table has a null data pointer");
+    if (page_size <= 0 || page_size % 8 != 0) return fail(FA8_ERR_UNSUPPORTED, "page_size must be a positive multiple of 8");
+    const fa8_status st = check_int_vec(cu_k, "cu_seqlens_k", (long long)B + 1);
+    if (st) return st;
+    out->cu_k = static_cast<const int *>(cu_k->data);
+    out->bt = static_cast<const int *>(bt->data);
+    out->bt_stride = bt->stride[0];
+    out->B = B;
+    out->max_pages = (int)bt->shape[1];
+    out->page_size = page_size;
+    return FA8_SUCCESS;
+}
+
+fa8_status check_queries(const fa8_tensor *q, const fa8_tensor *cu_q, Queries *out) {
+    long long B, T;
+    if (q->ndim == 4) {
+        if (cu_q) return fail(FA8_ERR_INVALID_ARG, "cu_seqlens_q is only valid with a 3-D (varlen) q");
+        B = q->shape[0];
+        if (B > 0x7fffffffLL - 1 || q->shape[1] > 0x7fffffffLL) return fail(FA8_ERR_UNSUPPORTED, "too many tokens");
+        T = B * q->shape[1];
+        out->Sq = (int)q->shape[1];
+        for (int i = 0; i < 3; ++i) out->stride[i] = q->stride[i];
+    } else {
+        if (!cu_q) return fail(FA8_ERR_INVALID_ARG, "a 3-D (varlen) q needs cu_seqlens_q");
+        if (cu_q->ndim != 1 || cu_q->shape[0] < 2 || cu_q->shape[0] > 0x7fffffffLL)
+            return fail(FA8_ERR_INVALID_ARG, "cu_seqlens_q must have B+1 >= 2 entries");
+        B = cu_q->shape[0] - 1;
+        T = q->shape[0];
+        const fa8_status st = check_int_vec(cu_q, "cu_seqlens_q", B + 1);
+        if (st) return st;
+        out->cu_q = static_cast<const int *>(cu_q->data);
+        for (int i = 1; i < 3; ++i) out->stride[i] = q->stride[i - 1];
+    }
+    if (B <= 0) return fail(FA8_ERR_INVALID_ARG, "batch must be >= 1");
+    if (T > 0x7fffffffLL) return fail(FA8_ERR_UNSUPPORTED, "too many tokens");
+    const long long Hq = q->shape[q->ndim - 2], D = q->shape[q->ndim - 1];
+    if (Hq > 65536 || D > 65536) return fail(FA8_ERR_UNSUPPORTED, "q is (.., %lld, %lld): too large", Hq, D);
+    out->B = (int)B;
+    out->T = (int)T;
+    out->Hq = (int)Hq;
+    out->D = (int)D;
+    return FA8_SUCCESS;
+}
+
+fa8_status check_groups(long long Hq, long long Hkv, int *G) {
+    if (Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0)
+        return fail(FA8_ERR_INVALID_ARG, "q heads (%lld) must be a positive multiple of kv heads (%lld)", Hq, Hkv);
+    if (Hq / Hkv > 128) return fail(FA8_ERR_UNSUPPORTED, "more than 128 q-heads per kv-head (%lld)", Hq / Hkv);
+    *G = (int)(Hq / Hkv);
+    return FA8_SUCCESS;
+}
+
+fa8_status check_page_lists(const fa8_tensor *t, const Queries &q, int Hkv, long long stride[3], int *K) {
+    if (t->dtype != FA8_DTYPE_I32) return fail(FA8_ERR_INVALID_ARG, "pages must be int32");
+    const int nd = q.cu_q ? 3 : 4;
+    if (t->ndim != nd) return fail(FA8_ERR_INVALID_ARG, "pages must have q's rank");
+    const bool same = q.cu_q ? t->shape[0] == q.T : (t->shape[0] == q.B && t->shape[1] == q.Sq);
+    if (!same || t->shape[nd - 2] != Hkv) return fail(FA8_ERR_INVALID_ARG, "pages must be (q's tokens, Hkv=%d, K)", Hkv);
+    const long long k = t->shape[nd - 1];
+    if (k < 0) return fail(FA8_ERR_INVALID_ARG, "pages: negative extent");
+    if (k > kMaxPageList) return fail(FA8_ERR_UNSUPPORTED, "%lld pages per list, at most %d are supported", k, kMaxPageList);
+    if (k > 1 && t->stride[nd - 1] != 1) return fail(FA8_ERR_INVALID_ARG, "pages: last dim must be contiguous");
+    stride[0] = q.cu_q ? 0 : t->stride[0];
+    stride[1] = t->stride[nd - 3];
+    stride[2] = t->stride[nd - 2];
+    *K = (int)k;
+    return FA8_SUCCESS;
+}
+
+}  // namespace host
+}  // namespace fa8
+
+namespace {
+
+using namespace fa8::host;
 
 // Device address of g_fa8_static_scratch on the current device, looked up on the first
 // request for each device.
@@ -196,11 +329,6 @@ fa8_status encode4(CUtensorMap *m, void *base, const uint64_t dims[4], const uin
 
 int chunk_of(int d) { return (d % 128 == 0) ? 128 : ((d % 64 == 0) ? 64 : 32); }
 
-bool supported_dims(int d, int dv) {
-    return (d == 64 && dv == 64) || (d == 96 && dv == 96) || (d == 128 && dv == 128) || (d == 192 && dv == 128) ||
-           (d == 192 && dv == 192) || (d == 256 && dv == 256);
-}
-
 // ---------------------------------------------------------------- planner
 struct Plan {
     int D = 0, DV = 0, B = 0, Hq = 0, Hkv = 0, G = 0, P = 0, rows_per_tile = 0;
@@ -218,8 +346,6 @@ struct Plan {
     long long units = 0;       // (slot, kv-head, split) work units
     int cap = 0;  // split cap chosen on the host (dense K/V, batched q); 0: as the launch decides
 };
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // The split cap for dense K/V with batched q: every request has the same key and query
 // counts, so the host knows all that split_plan_kernel would read.  The same model as
@@ -257,29 +383,6 @@ int uniform_split_cap(int B, int Hkv, int Sk, int Sq, int P, int n, int slots) {
         if (cost(T) < best) best_cap = (int)T;
     }
     return best_cap;
-}
-
-fa8_status check_int_vec(const fa8_tensor *t, const char *name, long long n) {
-    if (t->dtype != FA8_DTYPE_I32) return fail(FA8_ERR_INVALID_ARG, "%s must be int32", name);
-    if (t->ndim != 1 || t->shape[0] != n || (n > 1 && t->stride[0] != 1))
-        return fail(FA8_ERR_INVALID_ARG, "%s must be a contiguous 1-D tensor of %lld entries", name, n);
-    if (!t->data) return fail(FA8_ERR_INVALID_ARG, "%s has a null data pointer", name);
-    return FA8_SUCCESS;
-}
-
-// Q/K/V payload: last dim contiguous, other strides multiples of 16 bytes, 16-byte base.
-fa8_status check_payload(const fa8_tensor *t, const char *name) {
-    if (t->ndim < 3 || t->ndim > 4) return fail(FA8_ERR_INVALID_ARG, "%s must have 3 or 4 dims", name);
-    if (t->stride[t->ndim - 1] != 1) return fail(FA8_ERR_INVALID_ARG, "%s: last dim must be contiguous", name);
-    for (int i = 0; i < t->ndim - 1; ++i) {
-        if (t->shape[i] < 0) return fail(FA8_ERR_INVALID_ARG, "%s: negative extent", name);
-        if (t->stride[i] <= 0 || t->stride[i] % 16 != 0)
-            return fail(FA8_ERR_INVALID_ARG, "%s: stride[%d]=%lld must be a positive multiple of 16 bytes", name, i,
-                        (long long)t->stride[i]);
-    }
-    if (t->shape[t->ndim - 1] < 0) return fail(FA8_ERR_INVALID_ARG, "%s: negative extent", name);
-    if (!aligned16(t->data)) return fail(FA8_ERR_INVALID_ARG, "%s: data must be 16-byte aligned", name);
-    return FA8_SUCCESS;
 }
 
 fa8_status make_plan(const fa8_tensor *q, const fa8_tensor *k, const fa8_tensor *v, const fa8_tensor *cu_q,
@@ -439,24 +542,6 @@ fa8_status make_plan(const fa8_tensor *q, const fa8_tensor *k, const fa8_tensor 
         p.ws_bytes = o_bytes + ((rows * sizeof(float) + 255) & ~(size_t)255) + 256;
     }
     *pl = p;
-    return FA8_SUCCESS;
-}
-
-fa8_status check_descale(const fa8_tensor *t, const char *name, const Plan &p, const float **ptr, long long *sb,
-                         long long *sh) {
-    *ptr = nullptr;
-    *sb = *sh = 0;
-    if (!t) return FA8_SUCCESS;
-    if (t->dtype != FA8_DTYPE_F32) return fail(FA8_ERR_INVALID_ARG, "%s must be fp32", name);
-    if (!t->data) return fail(FA8_ERR_INVALID_ARG, "%s has a null data pointer", name);
-    if (t->ndim == 0) {
-    } else if (t->ndim == 2 && t->shape[0] == p.B && t->shape[1] == p.Hkv) {
-        *sb = t->stride[0];
-        *sh = t->stride[1];
-    } else {
-        return fail(FA8_ERR_INVALID_ARG, "%s must be 0-d or (batch=%d, kv_heads=%d)", name, p.B, p.Hkv);
-    }
-    *ptr = static_cast<const float *>(t->data);
     return FA8_SUCCESS;
 }
 
@@ -638,9 +723,9 @@ fa8_status fa8_fwd(const fa8_tensor *q, const fa8_tensor *k, const fa8_tensor *v
     // ---- descales, sink, flags
     fa8::FwdParams p;
     memset(&p, 0, sizeof(p));
-    if ((st = check_descale(descale_q, "descale_q", pl, &p.dq, &p.dq_sb, &p.dq_sh)) ||
-        (st = check_descale(descale_k, "descale_k", pl, &p.dk, &p.dk_sb, &p.dk_sh)) ||
-        (st = check_descale(descale_v, "descale_v", pl, &p.dv, &p.dv_sb, &p.dv_sh)))
+    if ((st = check_descale(descale_q, "descale_q", pl.B, pl.Hkv, &p.dq, &p.dq_sb, &p.dq_sh)) ||
+        (st = check_descale(descale_k, "descale_k", pl.B, pl.Hkv, &p.dk, &p.dk_sb, &p.dk_sh)) ||
+        (st = check_descale(descale_v, "descale_v", pl.B, pl.Hkv, &p.dv, &p.dv_sb, &p.dv_sh)))
         return st;
     if (sink) {
         if (sink->dtype != FA8_DTYPE_F32 || sink->ndim != 1 || sink->shape[0] != pl.Hq ||

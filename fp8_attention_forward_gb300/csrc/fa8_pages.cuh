@@ -1,0 +1,120 @@
+// fa8_pages.cuh -- device pieces shared by the paged-cache operators: the token's request, the
+// warp-level f16 MMA on E4M3 operands, and cluster addressing.
+//
+// Why warp MMAs here and not tcgen05: these kernels stream a cache past at most 16 query rows, so
+// HBM or L2 is the bound and an MMA tile is mostly padding.  With the keys (or pages) on M and the
+// query rows on N = 8, operands go from global memory straight to registers: a thread reads 8 or 16
+// contiguous bytes of a row, and because the order of a contraction is free, those bytes serve as
+// its k elements of consecutive MMAs.  No shared memory, barrier or TMEM round trip per tile.
+// E4M3 is exact in f16 and products of two are exact in fp32.
+#pragma once
+
+#include <stdint.h>
+
+#include "fa8_ptx.cuh"
+
+namespace fa8 {
+
+// Request b, index i within its Lq new tokens, of flat token `tok`; false for rows outside the
+// packed sequences.  cu_q null: batched, Sq tokens each.
+__device__ __forceinline__ bool locate_token(const int *cu_q, int B, int Sq, int tok, int *b, int *i, int *Lq) {
+    if (!cu_q) {
+        *b = tok / Sq;
+        *i = tok - *b * Sq;
+        *Lq = Sq;
+        return true;
+    }
+    int lo = 0, hi = B - 1;  // last request whose first token is <= tok
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cu_q[mid] <= tok) lo = mid;
+        else hi = mid - 1;
+    }
+    const int start = cu_q[lo], end = cu_q[lo + 1];
+    *b = lo;
+    *i = tok - start;
+    *Lq = end - start;
+    return tok >= start && tok < end;
+}
+
+// D (16x8 fp32) += A (16x16 f16, row) B (16x8 f16, col)
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// transpose of an 8x8 matrix of 16-bit elements held in MMA fragment layout
+__device__ __forceinline__ uint32_t trans8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+// four E4M3 bytes -> two f16 pairs (bytes 0, 1 and 2, 3)
+__device__ __forceinline__ void e4m3x4_to_h2(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    lo = ptx::e4m3x2_to_h2(w);
+    hi = ptx::e4m3x2_to_h2(w >> 16);
+}
+// byte pairs of two words: (x0, y0, x1, y1) and (x2, y2, x3, y3)
+__device__ __forceinline__ uint32_t zip_lo(uint32_t x, uint32_t y) {
+    uint32_t d;
+    asm("prmt.b32 %0, %1, %2, 0x5140;" : "=r"(d) : "r"(x), "r"(y));
+    return d;
+}
+__device__ __forceinline__ uint32_t zip_hi(uint32_t x, uint32_t y) {
+    uint32_t d;
+    asm("prmt.b32 %0, %1, %2, 0x7362;" : "=r"(d) : "r"(x), "r"(y));
+    return d;
+}
+
+// read-once global loads of N = 4, 8 or 16 bytes (no L1 allocation)
+template <int N>
+struct Bytes {
+    uint32_t w[N / 4];
+};
+template <int N>
+__device__ __forceinline__ Bytes<N> ld_stream(const uint8_t *p) {
+    Bytes<N> r;
+    if constexpr (N == 16)
+        asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3])
+                     : "l"(p));
+    else if constexpr (N == 8)
+        asm volatile("ld.global.nc.L1::no_allocate.v2.b32 {%0, %1}, [%2];" : "=r"(r.w[0]), "=r"(r.w[1]) : "l"(p));
+    else
+        asm volatile("ld.global.nc.L1::no_allocate.b32 %0, [%1];" : "=r"(r.w[0]) : "l"(p));
+    return r;
+}
+
+// ---------------------------------------------------------------- clusters
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// every thread of every CTA of the cluster: writes before are visible after
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// address of a shared-memory word in CTA `rank` of the cluster
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+}  // namespace fa8

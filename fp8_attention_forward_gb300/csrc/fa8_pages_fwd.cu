@@ -1,0 +1,559 @@
+// fa8_pages_fwd.cu -- attention over listed pages of an FP8 paged cache (fa8_fwd_pages).
+//
+// Each (token, kv-head) has its own list of pages, so a tile has at most the G q-heads of one
+// kv-head as rows and no two tiles share keys by construction: the work is a gather of K and V
+// rows, bound by HBM (decode) or by L2 (many tokens of one request).
+//
+//   S^T (16 keys x 8 rows)  = K (M = keys, k = d) . Q^T        f16 MMAs on exactly widened E4M3
+//   O^T (16 dv x 8 rows)   += V^T (M = dv, k = keys) . P^T
+//
+// A warp works alone: it takes every (4 x cluster)-th chunk of 16 or 32 keys of the list, keeps its
+// own running maximum, sum and O^T in registers, and loads K and V fragments straight from global
+// memory (see fa8_pages.cuh); V's fragments pair the bytes of two keys with one byte permute.  P is
+// rounded to f16 (2^-11 relative; p <= 1 and the running maximum is exact, so nothing saturates),
+// not to E4M3 as in fa8_fwd: V widens to f16 anyway.  The four warps, then the CTAs of the cluster
+// through distributed shared memory, merge by their maxima, so no workspace and no second kernel.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <string.h>
+
+#include <algorithm>
+
+#include "fa8.h"
+#include "fa8_host.h"
+#include "fa8_kernel.cuh"
+#include "fa8_pages.cuh"
+
+namespace fa8 {
+
+struct PagesParams {
+    const uint8_t *q, *k, *v;
+    long long q_s[3];            // request, token, head
+    long long k_s[3], v_s[3];    // page, row, head
+    const int *list;
+    long long l_s[3];            // request, token, head
+    const int *cu_q;
+    const float *dq, *dk, *dv;
+    long long dq_s[2], dk_s[2], dv_s[2];
+    const float *sink;
+    float scale_log2;
+    void *o;
+    long long o_s[3];
+    int out_fp16;
+    float *lse;
+    long long lse_s[3];          // request, token, head
+    int T, B, Sq, Hkv, G, K, causal, num_pages, cluster, row_blocks;
+    unsigned int group_magic;    // ceil(2^32 / (page_size / 8)): 8-key group -> list entry
+    host::Table tab;
+    unsigned int *status;
+};
+
+constexpr int kPgWarps = 4, kPgThreads = kPgWarps * 32;
+constexpr int kPgMaxCluster = 8;
+
+template <int D, int DV, int NT>
+struct PgCfg {
+    static constexpr int ROWS = 8 * NT;
+    static constexpr int MT = D + DV <= 256 ? 2 : 1;  // 16-key tiles per chunk
+    static constexpr int KC = 16 * MT;                // keys per chunk
+    static constexpr int NG = 2 * MT;                 // 8-key groups per chunk
+    static constexpr int VK = D % 64 == 0 ? 16 : 8;   // bytes of one K vector load
+    static constexpr int NKV = D / (4 * VK);          // K vector loads per key and lane
+    static constexpr int STEPS = D / 16;
+    static constexpr int DT = DV / 16;                // 16-row tiles of O^T
+    // a lane's DV / 8 bytes of a V row: runs of 16, 8 and 4 bytes at 128-, 64- and 32-byte blocks
+    static constexpr int NV16 = DV / 128, NV8 = (DV % 128) / 64, NV4 = (DV % 64) / 32;
+    static constexpr int OPITCH = DV + 4;             // floats per row of a merge buffer
+    static constexpr int Q_BYTES = NT * STEPS * 32 * 8;
+    static constexpr int MERGE_BYTES = kPgWarps * ROWS * (OPITCH + 2) * 4;
+    static int smem(int K) { return std::max(Q_BYTES + ((K * 8 + 15) & ~15), MERGE_BYTES); }
+};
+
+// dv index of slot s (0 .. DV / 8 - 1) of the lane with row r
+template <int DV>
+__device__ __forceinline__ int slot_dv(int s, int r) {
+    constexpr int n16 = DV / 128 * 16, n8 = (DV % 128) / 64 * 8;
+    if (s < n16) return (s >> 4) * 128 + 16 * r + (s & 15);
+    if (s < n16 + n8) return DV / 128 * 128 + 8 * r + (s - n16);
+    return DV / 128 * 128 + (DV % 128) / 64 * 64 + 4 * r + (s - n16 - n8);
+}
+
+template <int D, int DV, int NT>
+__global__ void __launch_bounds__(kPgThreads) fwd_pages_kernel(const __grid_constant__ PagesParams p) {
+    using C = PgCfg<D, DV, NT>;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ int s_used;
+    __shared__ float s_m[C::ROWS], s_l[C::ROWS];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int r = lane >> 2, c = lane & 3;
+    const int CS = p.cluster;
+    const int rank = CS > 1 ? (int)cluster_rank() : 0;
+    int row = blockIdx.x / CS;
+    const int rb = row % p.row_blocks;
+    row /= p.row_blocks;
+    const int kvh = row % p.Hkv, tok = row / p.Hkv;
+    const int ps = p.tab.page_size;
+    int b, ti, Lq;
+    if (!locate_token(p.cu_q, p.B, p.Sq, tok, &b, &ti, &Lq)) return;
+    const int Lk = p.tab.cu_k[b + 1] - p.tab.cu_k[b];
+    int vis = p.causal ? min(Lk, Lk - Lq + ti + 1) : Lk;
+    if (Lk < 0 || (long long)Lk > (long long)p.tab.max_pages * ps) {
+        if (tid == 0) atomicOr(p.status, kStatusBounds);
+        vis = 0;
+    }
+    const long long bb = p.cu_q ? 0 : b, tt = p.cu_q ? tok : ti;
+    const int h0 = kvh * p.G + rb * C::ROWS;            // first q-head of the tile
+    const int rows = min(C::ROWS, p.G - rb * C::ROWS);  // real rows
+
+    // ---- the list: page and first key of every entry (page -1: nothing visible in it)
+    uint2 *qf = reinterpret_cast<uint2 *>(smem);
+    int2 *ent = reinterpret_cast<int2 *>(smem + C::Q_BYTES);
+    if (tid == 0) s_used = 0;
+    __syncthreads();
+    {
+        const int *list = p.list + bb * p.l_s[0] + tt * p.l_s[1] + kvh * p.l_s[2];
+        const int *bt = p.tab.bt + (long long)b * p.tab.bt_stride;
+        int used = 0;
+        for (int e = tid; e < p.K; e += kPgThreads) {
+            const int lp = list[e];
+            int page = -1, key0 = 0;
+            if (lp >= p.tab.max_pages) {
+                atomicOr(p.status, kStatusBounds);
+            } else if (lp >= 0 && (long long)lp * ps < vis) {
+                page = bt[lp];
+                if (page < 0 || page >= p.num_pages) {
+                    page = -1;
+                    atomicOr(p.status, kStatusBounds);
+                } else {
+                    used = e + 1;
+                    key0 = lp * ps;
+                }
+            }
+            ent[e] = make_int2(page, key0);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) used = max(used, __shfl_xor_sync(0xffffffffu, used, o));
+        if (lane == 0 && used) atomicMax(&s_used, used);
+        const uint8_t *q = p.q + bb * p.q_s[0] + tt * p.q_s[1] + (long long)h0 * p.q_s[2];
+        for (int x = tid; x < NT * C::STEPS * 32; x += kPgThreads) {
+            const int ln = x & 31, st = (x >> 5) % C::STEPS, nt = x / (32 * C::STEPS);
+            const int qr = nt * 8 + (ln >> 2);
+            constexpr int SPV = C::VK / 4;  // k-steps fed by one vector load
+            const int pos = (st / SPV) * 4 * C::VK + (ln & 3) * C::VK + 4 * (st % SPV);
+            uint32_t lo = 0, hi = 0;
+            if (qr < rows) e4m3x4_to_h2(*reinterpret_cast<const uint32_t *>(q + qr * p.q_s[2] + pos), lo, hi);
+            qf[x] = make_uint2(lo, hi);
+        }
+    }
+    __syncthreads();
+    const int gpp = ps >> 3;                   // 8-key groups per page
+    const int groups = s_used * gpp;           // groups of the list
+    const float dqv = p.dq ? p.dq[b * p.dq_s[0] + kvh * p.dq_s[1]] : 1.f;
+    const float dkv = p.dk ? p.dk[b * p.dk_s[0] + kvh * p.dk_s[1]] : 1.f;
+    const float cs = p.scale_log2 * dqv * dkv;
+    const uint8_t *kb = p.k + (long long)kvh * p.k_s[2] + (long long)r * p.k_s[1] + c * C::VK;
+    const uint8_t *vb = p.v + (long long)kvh * p.v_s[2] + (long long)(2 * c) * p.v_s[1];
+
+    float m[NT][2], l[NT][2];  // running maximum (log2 units) and this lane's share of the sum, rows 2c, 2c + 1
+    float o[C::DT][NT][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            m[t][e] = -INFINITY;
+            l[t][e] = 0.f;
+        }
+#pragma unroll
+    for (int d = 0; d < C::DT; ++d)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[d][t][e] = 0.f;
+
+    for (int g0 = (warp * CS + rank) * C::NG; g0 < groups; g0 += C::NG * CS * kPgWarps) {
+        // the chunk's groups: row offsets and how many of the 8 keys are visible
+        long long ko[C::NG], vo[C::NG];
+        int lim[C::NG];
+#pragma unroll
+        for (int i = 0; i < C::NG; ++i) {
+            const int g = g0 + i;
+            lim[i] = 0;
+            ko[i] = vo[i] = 0;
+            if (g < groups) {
+                const int e = gpp == 1 ? g : (int)__umulhi((unsigned)g, p.group_magic);
+                const int off = (g - e * gpp) * 8;
+                const int2 en = ent[e];
+                if (en.x >= 0) {
+                    lim[i] = vis - en.y - off;
+                    ko[i] = en.x * p.k_s[0] + off * p.k_s[1];
+                    vo[i] = en.x * p.v_s[0] + off * p.v_s[1];
+                }
+            }
+        }
+        Bytes<C::VK> kr[C::NG][C::NKV];
+#pragma unroll
+        for (int i = 0; i < C::NG; ++i)
+#pragma unroll
+            for (int j = 0; j < C::NKV; ++j) {
+                if (r < lim[i]) kr[i][j] = ld_stream<C::VK>(kb + ko[i] + j * 4 * C::VK);
+                else kr[i][j] = Bytes<C::VK>{};
+            }
+        uint32_t vr[C::NG][2][DV / 32];
+#pragma unroll
+        for (int i = 0; i < C::NG; ++i)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const uint8_t *src = vb + vo[i] + y * p.v_s[1];
+                if (2 * c + y < lim[i]) {
+#pragma unroll
+                    for (int j = 0; j < C::NV16; ++j) {
+                        const Bytes<16> x = ld_stream<16>(src + 128 * j + 16 * r);
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) vr[i][y][4 * j + w] = x.w[w];
+                    }
+                    if constexpr (C::NV8 > 0) {
+                        const Bytes<8> x = ld_stream<8>(src + 128 * C::NV16 + 8 * r);
+                        vr[i][y][4 * C::NV16] = x.w[0];
+                        vr[i][y][4 * C::NV16 + 1] = x.w[1];
+                    }
+                    if constexpr (C::NV4 > 0) {
+                        const Bytes<4> x = ld_stream<4>(src + 128 * C::NV16 + 64 * C::NV8 + 4 * r);
+                        vr[i][y][4 * C::NV16 + 2 * C::NV8] = x.w[0];
+                    }
+                } else {
+#pragma unroll
+                    for (int w = 0; w < DV / 32; ++w) vr[i][y][w] = 0u;
+                }
+            }
+        // ---- S^T
+        float s[C::MT][NT][4];
+#pragma unroll
+        for (int x = 0; x < C::MT; ++x)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[x][t][e] = 0.f;
+#pragma unroll
+        for (int j = 0; j < C::NKV; ++j)
+#pragma unroll
+            for (int w = 0; w < C::VK / 4; ++w) {
+                uint2 bf[NT];
+#pragma unroll
+                for (int t = 0; t < NT; ++t) bf[t] = qf[(t * C::STEPS + j * (C::VK / 4) + w) * 32 + lane];
+#pragma unroll
+                for (int x = 0; x < C::MT; ++x) {
+                    uint32_t a0, a1, a2, a3;
+                    e4m3x4_to_h2(kr[2 * x][j].w[w], a0, a2);
+                    e4m3x4_to_h2(kr[2 * x + 1][j].w[w], a1, a3);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) mma_f16(s[x][t], a0, a1, a2, a3, bf[t].x, bf[t].y);
+                }
+            }
+        // ---- softmax: scale, mask, running maximum per row (over the lanes of equal c)
+        uint32_t pb[C::MT][NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int x = 0; x < C::MT; ++x)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float &y = s[x][t][2 * h + e];
+                        y = r < lim[2 * x + h] ? y * cs : -INFINITY;
+                        mx[e] = fmaxf(mx[e], y);
+                    }
+            float ref[2], alpha[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int sh = 4; sh < 32; sh <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], sh));
+                const float mn = fmaxf(m[t][e], mx[e]);
+                ref[e] = mn == -INFINITY ? 0.f : mn;
+                alpha[e] = ptx::ex2(m[t][e] - ref[e]);  // 0 while nothing has been seen
+                m[t][e] = mn;
+                l[t][e] *= alpha[e];
+            }
+#pragma unroll
+            for (int d = 0; d < C::DT; ++d)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[d][t][e] *= alpha[e & 1];
+#pragma unroll
+            for (int x = 0; x < C::MT; ++x)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float p0 = ptx::ex2(s[x][t][2 * h] - ref[0]), p1 = ptx::ex2(s[x][t][2 * h + 1] - ref[1]);
+                    l[t][0] += p0;
+                    l[t][1] += p1;
+                    pb[x][t][h] = trans8x8(ptx::cvt_f16x2(p1, p0));
+                }
+        }
+        // ---- O^T
+#pragma unroll
+        for (int x = 0; x < C::MT; ++x)
+#pragma unroll
+            for (int w = 0; w < DV / 32; ++w) {
+                const uint32_t *k0 = vr[2 * x][0], *k1 = vr[2 * x][1], *k2 = vr[2 * x + 1][0], *k3 = vr[2 * x + 1][1];
+                uint32_t a[8];
+                e4m3x4_to_h2(zip_lo(k0[w], k1[w]), a[0], a[1]);
+                e4m3x4_to_h2(zip_hi(k0[w], k1[w]), a[2], a[3]);
+                e4m3x4_to_h2(zip_lo(k2[w], k3[w]), a[4], a[5]);
+                e4m3x4_to_h2(zip_hi(k2[w], k3[w]), a[6], a[7]);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    mma_f16(o[2 * w][t], a[0], a[1], a[4], a[5], pb[x][t][0], pb[x][t][1]);
+                    mma_f16(o[2 * w + 1][t], a[2], a[3], a[6], a[7], pb[x][t][0], pb[x][t][1]);
+                }
+            }
+    }
+
+    // ---- merge: warps through shared memory, CTAs through distributed shared memory
+    __syncthreads();  // the list and Q are done with
+    float *wo = reinterpret_cast<float *>(smem);                       // [warp][row][OPITCH]
+    float *wm = wo + kPgWarps * C::ROWS * C::OPITCH, *wl = wm + kPgWarps * C::ROWS;  // [warp][row]
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float x = l[t][e];
+#pragma unroll
+            for (int sh = 4; sh < 32; sh <<= 1) x += __shfl_xor_sync(0xffffffffu, x, sh);
+            const int rw = 8 * t + 2 * c + e;
+            if (r == 0) {
+                wm[warp * C::ROWS + rw] = m[t][e];
+                wl[warp * C::ROWS + rw] = x;
+            }
+#pragma unroll
+            for (int d = 0; d < C::DT; ++d)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    wo[(warp * C::ROWS + rw) * C::OPITCH + slot_dv<DV>(2 * d + h, r)] = o[d][t][2 * h + e];
+        }
+    __syncthreads();
+    // warp buffers -> buffer of warp 0 (relative to the CTA's maximum), and the CTA's m and l
+    for (int x = tid; x < rows * (DV / 2); x += kPgThreads) {
+        const int rw = x / (DV / 2), d = 2 * (x - rw * (DV / 2));
+        float M = wm[rw];
+#pragma unroll
+        for (int w = 1; w < kPgWarps; ++w) M = fmaxf(M, wm[w * C::ROWS + rw]);
+        const float ref = M == -INFINITY ? 0.f : M;
+        float a0 = 0.f, a1 = 0.f, L = 0.f;
+#pragma unroll
+        for (int w = 0; w < kPgWarps; ++w) {
+            const float f = ptx::ex2(wm[w * C::ROWS + rw] - ref);
+            const float2 y = *reinterpret_cast<const float2 *>(wo + (w * C::ROWS + rw) * C::OPITCH + d);
+            a0 = fmaf(f, y.x, a0);
+            a1 = fmaf(f, y.y, a1);
+            L = fmaf(f, wl[w * C::ROWS + rw], L);
+        }
+        *reinterpret_cast<float2 *>(wo + rw * C::OPITCH + d) = make_float2(a0, a1);
+        if (d == 0) {
+            s_m[rw] = M;
+            s_l[rw] = L;
+        }
+    }
+    if (CS > 1) cluster_sync();
+    else __syncthreads();
+    const float dvv = p.dv ? p.dv[b * p.dv_s[0] + kvh * p.dv_s[1]] : 1.f;
+    const uint32_t a_m = ptx::smem_u32(s_m), a_l = ptx::smem_u32(s_l), a_o = ptx::smem_u32(wo);
+    // the cluster's CTAs share the tile's output: pair x of columns belongs to rank x mod CS's stretch
+    const int total = rows * (DV / 2), share = (total + CS - 1) / CS;
+    for (int x = rank * share + tid; x < min(total, (rank + 1) * share); x += kPgThreads) {
+        const int rw = x / (DV / 2), d = 2 * (x - rw * (DV / 2));
+        float M, L, a0, a1;
+        if (CS > 1) {
+            float mr[kPgMaxCluster];
+            M = -INFINITY;
+            for (int k = 0; k < CS; ++k) M = fmaxf(M, mr[k] = ld_cluster_f32(map_rank(a_m + 4u * rw, k)));
+            const float ref = M == -INFINITY ? 0.f : M;
+            L = a0 = a1 = 0.f;
+            for (int k = 0; k < CS; ++k) {
+                const float f = ptx::ex2(mr[k] - ref);
+                const float2 y = ld_cluster_f2(map_rank(a_o + 4u * (uint32_t)(rw * C::OPITCH + d), k));
+                a0 = fmaf(f, y.x, a0);
+                a1 = fmaf(f, y.y, a1);
+                L = fmaf(f, ld_cluster_f32(map_rank(a_l + 4u * rw, k)), L);
+            }
+        } else {
+            M = s_m[rw];
+            L = s_l[rw];
+            a0 = wo[rw * C::OPITCH + d];
+            a1 = wo[rw * C::OPITCH + d + 1];
+        }
+        const int hq = h0 + rw;
+        float lse, f;
+        if (M == -INFINITY && L == 0.f) {  // no visible key
+            f = 0.f;
+            lse = p.sink ? p.sink[hq] : -INFINITY;
+        } else {
+            const float ref = M == -INFINITY ? 0.f : M;
+            float top = ref, sum = L, sc = 1.f;
+            if (p.sink) {
+                const float sl = p.sink[hq] * kLog2e;
+                top = fmaxf(ref, sl);
+                sc = ptx::ex2(ref - top);
+                sum = L * sc + ptx::ex2(sl - top);
+            }
+            f = sc * dvv / sum;
+            lse = (log2f(sum) + top) * kLn2;
+        }
+        uint8_t *dst = reinterpret_cast<uint8_t *>(p.o) + 2 * (bb * p.o_s[0] + tt * p.o_s[1] + (long long)hq * p.o_s[2] + d);
+        if (p.out_fp16) *reinterpret_cast<__half2 *>(dst) = __floats2half2_rn(a0 * f, a1 * f);
+        else *reinterpret_cast<__nv_bfloat162 *>(dst) = __floats2bfloat162_rn(a0 * f, a1 * f);
+        if (d == 0 && p.lse) p.lse[bb * p.lse_s[0] + tt * p.lse_s[1] + (long long)hq * p.lse_s[2]] = lse;
+    }
+    if (CS > 1) cluster_sync();  // no CTA leaves while its shared memory is still read
+}
+
+template <int D, int DV, int NT>
+cudaError_t launch_pages(const PagesParams &p, unsigned int tiles, cudaStream_t s) {
+    const int smem = PgCfg<D, DV, NT>::smem(p.K);
+    cudaError_t e = cudaFuncSetAttribute(fwd_pages_kernel<D, DV, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(tiles * p.cluster);
+    cfg.blockDim = dim3(kPgThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = p.cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fwd_pages_kernel<D, DV, NT>, p);
+}
+
+}  // namespace fa8
+
+using namespace fa8::host;
+
+extern "C" fa8_status fa8_fwd_pages(const fa8_tensor *q, const fa8_tensor *k, const fa8_tensor *v, const fa8_tensor *pages,
+                                    const fa8_tensor *descale_q, const fa8_tensor *descale_k, const fa8_tensor *descale_v,
+                                    fa8_tensor *out, fa8_tensor *lse, const fa8_tensor *cu_seqlens_q,
+                                    const fa8_tensor *cu_seqlens_k, const fa8_tensor *block_table, int page_size, int causal,
+                                    const fa8_tensor *sink, float softmax_scale, void *stream) {
+    clear_error();
+    if (!q || !k || !v || !pages || !out) return fail(FA8_ERR_INVALID_ARG, "q, k, v, pages and out are required");
+    for (const fa8_tensor *t : {q, k, v})
+        if (t->dtype != FA8_DTYPE_E4M3) return fail(FA8_ERR_UNSUPPORTED, "q/k/v must be E4M3");
+    fa8::PagesParams p;
+    memset(&p, 0, sizeof(p));
+    fa8_status st;
+    if ((st = check_payload(q, "q")) || (st = check_payload(k, "k")) || (st = check_payload(v, "v"))) return st;
+    Queries qs;
+    if ((st = check_queries(q, cu_seqlens_q, &qs))) return st;
+    if (k->ndim != 4 || v->ndim != 4) return fail(FA8_ERR_INVALID_ARG, "k and v must be paged (num_pages, page_size, Hkv, d)");
+    for (int i = 0; i < 3; ++i)
+        if (k->shape[i] != v->shape[i]) return fail(FA8_ERR_INVALID_ARG, "k and v leading shapes differ at dim %d", i);
+    if (k->shape[3] != qs.D) return fail(FA8_ERR_INVALID_ARG, "k head dim %lld != q head dim %d", (long long)k->shape[3], qs.D);
+    if (v->shape[3] > 1024 || !supported_dims(qs.D, (int)v->shape[3]))
+        return fail(FA8_ERR_UNSUPPORTED, "(d, dv) = (%d, %lld) is not supported", qs.D, (long long)v->shape[3]);
+    const int DV = (int)v->shape[3];
+    const long long Hkv = k->shape[2];
+    if ((st = check_groups(qs.Hq, Hkv, &p.G))) return st;
+    if ((st = check_table(cu_seqlens_k, block_table, page_size, qs.B, &p.tab))) return st;
+    if (page_size != k->shape[1]) return fail(FA8_ERR_INVALID_ARG, "page_size (%d) != k.shape[1] (%lld)", page_size, (long long)k->shape[1]);
+    if (page_size > 4096) return fail(FA8_ERR_UNSUPPORTED, "page_size %d is above 4096", page_size);
+    if (k->shape[0] > 0x7fffffffLL) return fail(FA8_ERR_UNSUPPORTED, "too many pages");
+    if (k->shape[0] > 0 && (!k->data || !v->data)) return fail(FA8_ERR_INVALID_ARG, "k and v need data");
+    if ((st = check_page_lists(pages, qs, (int)Hkv, p.l_s, &p.K))) return st;
+    // ---- outputs
+    const int nd = q->ndim;
+    if (out->dtype != FA8_DTYPE_BF16 && out->dtype != FA8_DTYPE_F16) return fail(FA8_ERR_INVALID_ARG, "out must be bf16 or fp16");
+    if (out->ndim != nd) return fail(FA8_ERR_INVALID_ARG, "out must have q's rank");
+    for (int i = 0; i < nd - 1; ++i) {
+        if (out->shape[i] != q->shape[i]) return fail(FA8_ERR_INVALID_ARG, "out shape differs from q at dim %d", i);
+        if (out->stride[i] % 8 != 0) return fail(FA8_ERR_INVALID_ARG, "out strides must be multiples of 8 elements");
+    }
+    if (out->shape[nd - 1] != DV) return fail(FA8_ERR_INVALID_ARG, "out last dim must be dv=%d", DV);
+    if (out->stride[nd - 1] != 1) return fail(FA8_ERR_INVALID_ARG, "out: last dim must be contiguous");
+    if (!aligned16(out->data)) return fail(FA8_ERR_INVALID_ARG, "out must be 16-byte aligned");
+    if (lse) {
+        if (lse->dtype != FA8_DTYPE_F32) return fail(FA8_ERR_INVALID_ARG, "lse must be fp32");
+        if (qs.cu_q) {
+            if (lse->ndim != 2 || lse->shape[0] != qs.Hq || lse->shape[1] != qs.T)
+                return fail(FA8_ERR_INVALID_ARG, "varlen lse must be (Hq, total_q)");
+            p.lse_s[1] = lse->stride[1];
+            p.lse_s[2] = lse->stride[0];
+        } else {
+            if (lse->ndim != 3 || lse->shape[0] != qs.B || lse->shape[1] != qs.Hq || lse->shape[2] != qs.Sq)
+                return fail(FA8_ERR_INVALID_ARG, "lse must be (B, Hq, Sq)");
+            p.lse_s[0] = lse->stride[0];
+            p.lse_s[1] = lse->stride[2];
+            p.lse_s[2] = lse->stride[1];
+        }
+    }
+    if ((st = check_descale(descale_q, "descale_q", qs.B, (int)Hkv, &p.dq, &p.dq_s[0], &p.dq_s[1])) ||
+        (st = check_descale(descale_k, "descale_k", qs.B, (int)Hkv, &p.dk, &p.dk_s[0], &p.dk_s[1])) ||
+        (st = check_descale(descale_v, "descale_v", qs.B, (int)Hkv, &p.dv, &p.dv_s[0], &p.dv_s[1])))
+        return st;
+    if (sink) {
+        if (sink->dtype != FA8_DTYPE_F32 || sink->ndim != 1 || sink->shape[0] != qs.Hq || (qs.Hq > 1 && sink->stride[0] != 1) || !sink->data)
+            return fail(FA8_ERR_INVALID_ARG, "sink must be a contiguous fp32 (Hq,) tensor");
+        p.sink = static_cast<const float *>(sink->data);
+    }
+    if (causal != 0 && causal != 1) return fail(FA8_ERR_INVALID_ARG, "causal must be 0 or 1");
+    if (!std::isfinite(softmax_scale)) return fail(FA8_ERR_INVALID_ARG, "softmax_scale must be finite");
+    if (softmax_scale <= 0.f) softmax_scale = 1.0f / std::sqrt((float)qs.D);
+    const int nt = p.G <= 8 ? 1 : 2;
+    p.row_blocks = (p.G + 8 * nt - 1) / (8 * nt);
+    const long long tiles = (long long)qs.T * Hkv * p.row_blocks;
+    if (tiles * fa8::kPgMaxCluster > 0x7fffffffLL) return fail(FA8_ERR_UNSUPPORTED, "problem too large for the grid");
+    if (tiles == 0) return FA8_SUCCESS;
+    if (!q->data || !out->data || (lse && !lse->data) || (p.K > 0 && !pages->data))
+        return fail(FA8_ERR_INVALID_ARG, "q, pages, out and lse need data");
+    DeviceState *ds = nullptr;
+    if ((st = device_state(&ds))) return st;
+    p.q = static_cast<const uint8_t *>(q->data);
+    p.k = static_cast<const uint8_t *>(k->data);
+    p.v = static_cast<const uint8_t *>(v->data);
+    for (int i = 0; i < 3; ++i) {
+        p.q_s[i] = qs.stride[i];
+        p.k_s[i] = k->stride[i];
+        p.v_s[i] = v->stride[i];
+        p.o_s[i] = nd == 4 ? out->stride[i] : (i ? out->stride[i - 1] : 0);
+    }
+    p.list = static_cast<const int *>(pages->data);
+    p.cu_q = qs.cu_q;
+    p.scale_log2 = softmax_scale * 1.4426950408889634f;
+    p.o = out->data;
+    p.out_fp16 = out->dtype == FA8_DTYPE_F16;
+    p.lse = lse ? static_cast<float *>(lse->data) : nullptr;
+    p.T = qs.T;
+    p.B = qs.B;
+    p.Sq = qs.Sq;
+    p.Hkv = (int)Hkv;
+    p.causal = causal;
+    p.num_pages = (int)k->shape[0];
+    p.status = ds->status;
+    const unsigned gpp = (unsigned)page_size / 8;
+    p.group_magic = gpp > 1 ? (unsigned)((0x100000000ull + gpp - 1) / gpp) : 0u;
+    // Clusters split a list over CTAs while the grid is below four CTAs per SM and every warp keeps
+    // at least two chunks.
+    const long long keys = (long long)p.K * page_size;
+    p.cluster = 1;
+    while (p.cluster < fa8::kPgMaxCluster && tiles * p.cluster * 2 <= 4LL * ds->sm_count &&
+           keys >= 2LL * 32 * fa8::kPgWarps * p.cluster * 2)
+        p.cluster *= 2;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaErrorInvalidValue;
+#define FA8_PAGES(D_, DV_)                                                                             \
+    case D_ * 1000 + DV_:                                                                              \
+        e = nt == 1 ? fa8::launch_pages<D_, DV_, 1>(p, (unsigned)tiles, s) : fa8::launch_pages<D_, DV_, 2>(p, (unsigned)tiles, s); \
+        break;
+    switch (qs.D * 1000 + DV) {
+        FA8_PAGES(64, 64)
+        FA8_PAGES(96, 96)
+        FA8_PAGES(128, 128)
+        FA8_PAGES(192, 128)
+        FA8_PAGES(192, 192)
+        FA8_PAGES(256, 256)
+    }
+#undef FA8_PAGES
+    if (e != cudaSuccess) return cuda_fail(e, "page attention kernel launch");
+    return FA8_SUCCESS;
+}

@@ -33,6 +33,7 @@ _DTYPES = {
     torch.float16: 4,
     torch.float32: 5,
     torch.int32: 6,
+    torch.float64: 7,
 }
 
 # name -> (restype, argtypes); every function declared in include/fa8.h
@@ -58,6 +59,16 @@ SIGNATURES = {
     "fa8_fwd_static_scratch": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_int,
                                               ctypes.c_int, ctypes.c_int, _P, ctypes.c_float, ctypes.c_int,
                                               ctypes.c_void_p]),
+    "fa8_rope_inv_freq": (ctypes.c_int, [ctypes.c_int, ctypes.c_double, ctypes.c_int, ctypes.c_double,
+                                         ctypes.c_double, ctypes.c_double, ctypes.c_double,
+                                         ctypes.POINTER(ctypes.c_double)]),
+    "fa8_rope_append": (ctypes.c_int, [_P, _P, _P, _P, _P, ctypes.c_int, ctypes.c_int, ctypes.c_float, _P, _P, _P,
+                                       _P, _P, _P, _P, _P, _P, ctypes.c_int, ctypes.c_void_p]),
+    "fa8_page_bounds": (ctypes.c_int, [_P, _P, _P, _P, _P, ctypes.c_int, ctypes.c_int, ctypes.c_void_p]),
+    "fa8_select_pages": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                        ctypes.c_int, ctypes.c_void_p]),
+    "fa8_fwd_pages": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_int, ctypes.c_int, _P,
+                                     ctypes.c_float, ctypes.c_void_p]),
     "fa8_check": (ctypes.c_int, [ctypes.c_void_p]),
     "fa8_set_wait_timeout_ns": (ctypes.c_int, [ctypes.c_uint64]),
     "fa8_set_decode_kernel": (ctypes.c_int, [ctypes.c_int]),
@@ -206,6 +217,88 @@ def fwd_static_scratch(q, k, v, *, out, lse=None, descale_q=None, descale_k=None
                                           int(window_left), _ref(views["sink"]), float(softmax_scale),
                                           int(num_splits), _stream_handle(stream, q.device))
     _raise(st)
+    return out, lse
+
+
+# ------------------------------------------------------------------ around the paged cache
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}  # fa8_rope_scaling
+
+
+def rope_inv_freq(rotary_dim, base=10000.0, *, scaling="none", factor=1.0, original_len=0.0, low=1.0,
+                  high=None, device="cpu"):
+    """The rotary_dim / 2 frequencies (fp64) that ``rope_append`` takes, stretched for long
+    contexts as ``fa8_rope_scaling`` in include/fa8.h says."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}")
+    if high is None:
+        high = 4.0 if scaling == "bands" else 32.0
+    out = torch.empty(max(int(rotary_dim), 0) // 2, dtype=torch.float64)
+    _raise(lib().fa8_rope_inv_freq(int(rotary_dim), float(base), ROPE_SCALINGS[scaling], float(factor),
+                                   float(original_len), float(low), float(high),
+                                   ctypes.cast(out.data_ptr(), ctypes.POINTER(ctypes.c_double))))
+    return out.to(device)
+
+
+def _call(name, dev, stream, args):
+    """One library call with tensors as views; the stream goes last."""
+    views = [_view(a) if isinstance(a, torch.Tensor) else a for a in args]
+    views = [ctypes.byref(a) if isinstance(a, Fa8Tensor) else a for a in views]
+    with _on_device(dev):
+        _raise(getattr(lib(), name)(*views, _stream_handle(stream, dev) if dev.type == "cuda" else None))
+
+
+def rope_append(q, k, v, inv_freq, *, k_out, v_out, q_out=None, positions=None, interleaved=False,
+                rotary_offset=0, rot_scale=1.0, descale_q=None, descale_k=None, descale_v=None,
+                cu_seqlens_q=None, cu_seqlens_k=None, block_table=None, page_size=0, stream=None):
+    """Rotates Q and K, rounds Q, K and V to E4M3, appends K and V to k_out / v_out (dense,
+    varlen or paged, as in ``fwd``) and returns E4M3 Q."""
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=torch.float8_e4m3fn, device=q.device)
+    _call("fa8_rope_append", q.device, stream,
+          (q, k, v, inv_freq, positions, int(bool(interleaved)), int(rotary_offset), float(rot_scale), descale_q,
+           descale_k, descale_v, q_out, k_out, v_out, cu_seqlens_q, cu_seqlens_k, block_table, int(page_size)))
+    return q_out
+
+
+def page_bounds(k, bounds=None, *, cu_seqlens_k, block_table, page_size, cu_seqlens_q=None, new_tokens=-1,
+                stream=None):
+    """Updates the per-channel key bounds of the pages that hold the last new_tokens keys of each
+    request (cu_seqlens_q: its new tokens; neither: all pages).  Without ``bounds`` a zeroed
+    (num_pages, Hkv, 2, D) tensor is made."""
+    if bounds is None:
+        bounds = torch.zeros((k.shape[0], k.shape[2], 2, k.shape[3]), dtype=torch.uint8,
+                             device=k.device).view(torch.float8_e4m3fn)
+    _call("fa8_page_bounds", k.device, stream,
+          (k, bounds, cu_seqlens_q, cu_seqlens_k, block_table, int(page_size), int(new_tokens)))
+    return bounds
+
+
+def select_pages(q, bounds, top_k, *, cu_seqlens_k, block_table, page_size, cu_seqlens_q=None, causal=True,
+                 keep_first=1, keep_last=1, pages=None, stream=None):
+    """For every token and kv-head the top_k pages by bounded score: int32 (.., Hkv, top_k),
+    ascending, -1 behind the last."""
+    if pages is None:
+        pages = torch.empty((*q.shape[:-2], bounds.shape[1], int(top_k)), dtype=torch.int32, device=q.device)
+    elif pages.shape[-1] != top_k:
+        raise ValueError("pages must hold top_k entries")
+    _call("fa8_select_pages", q.device, stream,
+          (q, bounds, pages, cu_seqlens_q, cu_seqlens_k, block_table, int(page_size), int(bool(causal)),
+           int(keep_first), int(keep_last)))
+    return pages
+
+
+def fwd_pages(q, k, v, pages, *, cu_seqlens_k, block_table, page_size, descale_q=None, descale_k=None,
+              descale_v=None, out=None, lse=None, cu_seqlens_q=None, causal=True, sink=None, softmax_scale=0.0,
+              out_dtype=torch.bfloat16, return_lse=True, stream=None):
+    """Attention over the listed pages of a paged cache; returns (out, lse) as ``fwd`` does."""
+    if out is None:
+        out = torch.empty((*q.shape[:-1], v.shape[-1]), dtype=out_dtype, device=q.device)
+    if lse is None and return_lse:
+        shape = (q.shape[0], q.shape[2], q.shape[1]) if q.dim() == 4 else (q.shape[1], q.shape[0])
+        lse = torch.empty(shape, dtype=torch.float32, device=q.device)
+    _call("fa8_fwd_pages", q.device, stream,
+          (q, k, v, pages, descale_q, descale_k, descale_v, out, lse, cu_seqlens_q, cu_seqlens_k, block_table,
+           int(page_size), int(bool(causal)), sink, float(softmax_scale)))
     return out, lse
 
 

@@ -58,7 +58,8 @@ typedef enum {
     FA8_DTYPE_BF16 = 3,
     FA8_DTYPE_F16 = 4,
     FA8_DTYPE_F32 = 5,
-    FA8_DTYPE_I32 = 6
+    FA8_DTYPE_I32 = 6,
+    FA8_DTYPE_F64 = 7
 } fa8_dtype;
 
 /*
@@ -187,6 +188,128 @@ FA8_API fa8_status fa8_fwd_static_scratch(const fa8_tensor *q, const fa8_tensor 
                                           const fa8_tensor *block_table, int page_size,
                                           int causal, int window_left, const fa8_tensor *sink,
                                           float softmax_scale, int num_splits, void *stream);
+
+/* ------------------------------------------------------------------------------------
+ * Around the paged cache: filling it, summarising its pages, choosing pages for each query,
+ * and attention over the chosen pages.
+ *
+ * Shared conventions.  "New tokens" are the last Lq keys of each request: batched
+ * (B, Sq, ...) or packed (total_q, ...) with cu_seqlens_q, as q in fa8_fwd; token i of a
+ * request with Lk keys is its key Lk - Lq + i.  Rows of a packed tensor behind the last
+ * sequence are neither read nor written.  A cu_seqlens_k or block_table entry out of range
+ * raises FA8_ERR_DEVICE_BOUNDS in fa8_check and is never followed.  Every call enqueues one
+ * kernel on `stream`, needs no workspace, allocates nothing, and its launch depends on
+ * shapes and the SM count only, so it can be graph-captured.  Results do not depend on
+ * timing: equal inputs give equal bits.
+ * ------------------------------------------------------------------------------------ */
+
+/* How fa8_rope_inv_freq stretches the frequencies w_i = base^(-2 i / rotary_dim). */
+typedef enum {
+    FA8_ROPE_PLAIN = 0,  /* w_i                                                            */
+    FA8_ROPE_LINEAR = 1, /* w_i / factor (position interpolation)                          */
+    FA8_ROPE_NTK = 2,    /* base * factor^(rotary_dim / (rotary_dim - 2)) in place of base */
+    FA8_ROPE_YARN = 3,   /* w_i / factor where w_i makes fewer than `low` turns over
+                            original_len, w_i above `high` turns, a ramp over the index i
+                            between (YaRN; customary low = 1, high = 32)                   */
+    FA8_ROPE_BANDS = 4   /* as YARN, with the ramp over the number of turns itself
+                            (customary low = 1, high = 4)                                  */
+} fa8_rope_scaling;
+
+/*
+ * fa8_rope_inv_freq -- host only: writes the rotary_dim / 2 frequencies (radians per
+ * position) to inv_freq in host memory.  factor >= 1 is read by every scaling but PLAIN;
+ * original_len, low and high by YARN and BANDS.
+ */
+FA8_API fa8_status fa8_rope_inv_freq(int rotary_dim, double base, int scaling, double factor,
+                                     double original_len, double low, double high,
+                                     double *inv_freq);
+
+/*
+ * fa8_rope_append -- rotates Q and K, rounds Q, K and V to E4M3 and stores them: Q in
+ * q_out, K and V as the new tokens' keys in k_out / v_out.
+ *   q (B, Sq, Hq, D) or (total_q, Hq, D); k (.., Hkv, D) and v (.., Hkv, DV) with the same
+ *     leading dims; all bf16 or all fp16; last dim contiguous, strides multiples of 8
+ *     elements (views of one projection output will do), 16-byte aligned.  (D, DV) as in
+ *     fa8_fwd.
+ *   q_out: E4M3, q's shape.  k_out / v_out: E4M3, in any of fa8_fwd's K/V layouts; with
+ *     batched k_out (B, Sk, ..) the new tokens are the last Sq of Sk.
+ *   inv_freq: fp64 or fp32, (rotary_dim / 2) on the device; rotary_dim a multiple of 16.
+ *     Dims [rotary_offset, rotary_offset + rotary_dim) of every head are rotated, the rest
+ *     pass through; rotary_offset is a multiple of 8.  Pair i is dims (i, i + rotary_dim/2)
+ *     of that range, or (2 i, 2 i + 1) when interleaved = 1.
+ *   positions: int32, one per token, any strides; NULL = the token's key index.  The angle
+ *     of pair i is position * inv_freq[i], reduced exactly at every position.
+ *   rot_scale multiplies the rotated dims (YaRN's attention factor; 1 otherwise).
+ *   descale_q/k/v: as in fa8_fwd; out = e4m3(x / descale), round to nearest even,
+ *     saturating at +-448 (infinities too); NaN stays NaN.
+ * The outputs must not overlap the inputs, and no two tokens may share a cache slot.
+ */
+FA8_API fa8_status fa8_rope_append(const fa8_tensor *q, const fa8_tensor *k, const fa8_tensor *v,
+                                   const fa8_tensor *inv_freq, const fa8_tensor *positions,
+                                   int interleaved, int rotary_offset, float rot_scale,
+                                   const fa8_tensor *descale_q, const fa8_tensor *descale_k,
+                                   const fa8_tensor *descale_v, fa8_tensor *q_out,
+                                   fa8_tensor *k_out, fa8_tensor *v_out,
+                                   const fa8_tensor *cu_seqlens_q, const fa8_tensor *cu_seqlens_k,
+                                   const fa8_tensor *block_table, int page_size, void *stream);
+
+/*
+ * fa8_page_bounds -- per page, kv-head and channel, the smallest and the largest key:
+ * bounds[page, h, 0, c] = min and bounds[page, h, 1, c] = max over the page's keys of the
+ * request (rows past its Lk are ignored).  Exact: E4M3 values in, E4M3 values out.  A
+ * channel with a NaN key has NaN bounds.
+ *   k: paged (num_pages, page_size, Hkv, D); D a multiple of 16 up to 256.
+ *   bounds: E4M3 (num_pages, Hkv, 2, D), last two dims contiguous, 16-byte strides.
+ *   Updated are the pages that hold a new key: of each request's last Lq keys when
+ *   cu_seqlens_q is given, else of its last `new_tokens` keys, or all its pages when
+ *   new_tokens < 0.  A page is recomputed whole.  Other pages keep what they hold.
+ * Requests that share a page (a common prefix) must both fill it.
+ */
+FA8_API fa8_status fa8_page_bounds(const fa8_tensor *k, fa8_tensor *bounds,
+                                   const fa8_tensor *cu_seqlens_q, const fa8_tensor *cu_seqlens_k,
+                                   const fa8_tensor *block_table, int page_size, int new_tokens,
+                                   void *stream);
+
+/*
+ * fa8_select_pages -- for every new token and kv-head, the top_k pages that can hold the
+ * largest scores: score(page) = max over the kv-head's q-heads of
+ * sum_c max(q_c * lo_c, q_c * hi_c), an upper bound of q . key over the page.
+ *   q: E4M3 (B, Sq, Hq, D) or (total_q, Hq, D); D in {64, 96, 128, 192, 256}.
+ *   bounds: as fa8_page_bounds writes them.
+ *   pages: int32 (B, Sq, Hkv, top_k) or (total_q, Hkv, top_k), last dim contiguous: page
+ *     indices of the request (positions in its block_table row), ascending, -1 behind the
+ *     last.
+ * Candidates are the n pages with a key the token sees (all of the request's when
+ * causal = 0, keys up to its own when causal = 1); n <= top_k lists them all.  The first
+ * keep_first and the last keep_last of them are always listed (their sum is at most
+ * top_k); the rest goes by score.  Scores are compared exactly, as the real numbers that
+ * the formula gives, and ties go to the lower page; a NaN score ranks above all others.
+ * At most 16384 block_table columns; top_k 1 to 4096.
+ */
+FA8_API fa8_status fa8_select_pages(const fa8_tensor *q, const fa8_tensor *bounds,
+                                    fa8_tensor *pages, const fa8_tensor *cu_seqlens_q,
+                                    const fa8_tensor *cu_seqlens_k, const fa8_tensor *block_table,
+                                    int page_size, int causal, int keep_first, int keep_last,
+                                    void *stream);
+
+/*
+ * fa8_fwd_pages -- fa8_fwd over the keys of listed pages only: token t's q-heads of kv-head
+ * h attend to the keys of pages[t, h, :] that the token sees (causal or all, below Lk).
+ *   q, k, v (paged), descales, out, lse, sink, softmax_scale, causal: as in fa8_fwd.
+ *   pages: int32, as fa8_select_pages writes them.  Any order will do; entries below 0 are
+ *     skipped, a page listed twice counts twice, and a page with no visible key adds
+ *     nothing.  At most 4096 per token and kv-head.
+ *   page_size: a multiple of 8 up to 4096.
+ * Tokens with no visible listed key get O = 0 and LSE = -inf (the sink's logit with a
+ * sink).  Keys that are not visible are not read.
+ */
+FA8_API fa8_status fa8_fwd_pages(const fa8_tensor *q, const fa8_tensor *k, const fa8_tensor *v,
+                                 const fa8_tensor *pages, const fa8_tensor *descale_q,
+                                 const fa8_tensor *descale_k, const fa8_tensor *descale_v,
+                                 fa8_tensor *out, fa8_tensor *lse, const fa8_tensor *cu_seqlens_q,
+                                 const fa8_tensor *cu_seqlens_k, const fa8_tensor *block_table,
+                                 int page_size, int causal, const fa8_tensor *sink,
+                                 float softmax_scale, void *stream);
 
 /*
  * fa8_check -- reads the library's device status word of the current device on `stream`
