@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -239,12 +240,49 @@ def rope_inv_freq(rotary_dim, base=10000.0, *, scaling="none", factor=1.0, origi
     return out.to(device)
 
 
-def _call(name, dev, stream, args):
-    """One library call with tensors as views; the stream goes last."""
-    views = [_view(a) if isinstance(a, torch.Tensor) else a for a in args]
-    views = [ctypes.byref(a) if isinstance(a, Fa8Tensor) else a for a in views]
-    with _on_device(dev):
-        _raise(getattr(lib(), name)(*views, _stream_handle(stream, dev) if dev.type == "cuda" else None))
+_ARG = [struct.Struct("Qii%dq%dx%dq%dx" % (n, 32 - 8 * n, n, 32 - 8 * n)) for n in range(5)]  # fa8_tensor of n dims
+_ARGS = ctypes.c_char * (ctypes.sizeof(Fa8Tensor) * 16)
+_SCALARS = (type(None), int, float)
+_direct = {}
+
+
+def _call(name, device, stream, *args):
+    """One library call on ``device``; tensors are passed as views, the stream goes last.  The
+    views are packed into one buffer: a decode step's calls are short, and building a ctypes
+    structure per tensor took longer than the kernels."""
+    fn = _direct.get(name)
+    if fn is None:
+        res, types = SIGNATURES[name]
+        fn = lib()[name]
+        fn.restype, fn.argtypes = res, [ctypes.c_void_p if t is _P else t for t in types]
+        _direct[name] = fn
+    buf = _ARGS()
+    at = start = ctypes.addressof(buf)
+    passed = []
+    for a in args:
+        if type(a) in _SCALARS:
+            passed.append(a)
+            continue
+        shape = a.shape
+        n = len(shape)
+        if a.dtype not in _DTYPES:
+            raise TypeError(f"unsupported dtype {a.dtype}")
+        if n > 4:
+            raise ValueError("at most 4 dims")
+        _ARG[n].pack_into(buf, at - start, a.data_ptr(), _DTYPES[a.dtype], n, *shape, *a.stride())
+        passed.append(at)
+        at += 80
+    if device.type != "cuda":
+        status = fn(*passed, None)
+    else:
+        handle = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+        if torch.cuda.current_device() == device.index:
+            status = fn(*passed, handle)
+        else:
+            with torch.cuda.device(device):
+                status = fn(*passed, handle)
+    if status:
+        _raise(status)
 
 
 def rope_append(q, k, v, inv_freq, *, k_out, v_out, q_out=None, positions=None, interleaved=False,
@@ -254,9 +292,9 @@ def rope_append(q, k, v, inv_freq, *, k_out, v_out, q_out=None, positions=None, 
     varlen or paged, as in ``fwd``) and returns E4M3 Q."""
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=torch.float8_e4m3fn, device=q.device)
-    _call("fa8_rope_append", q.device, stream,
-          (q, k, v, inv_freq, positions, int(bool(interleaved)), int(rotary_offset), float(rot_scale), descale_q,
-           descale_k, descale_v, q_out, k_out, v_out, cu_seqlens_q, cu_seqlens_k, block_table, int(page_size)))
+    _call("fa8_rope_append", q.device, stream, q, k, v, inv_freq, positions, int(bool(interleaved)),
+          int(rotary_offset), float(rot_scale), descale_q, descale_k, descale_v, q_out, k_out, v_out, cu_seqlens_q,
+          cu_seqlens_k, block_table, int(page_size))
     return q_out
 
 
@@ -268,8 +306,8 @@ def page_bounds(k, bounds=None, *, cu_seqlens_k, block_table, page_size, cu_seql
     if bounds is None:
         bounds = torch.zeros((k.shape[0], k.shape[2], 2, k.shape[3]), dtype=torch.uint8,
                              device=k.device).view(torch.float8_e4m3fn)
-    _call("fa8_page_bounds", k.device, stream,
-          (k, bounds, cu_seqlens_q, cu_seqlens_k, block_table, int(page_size), int(new_tokens)))
+    _call("fa8_page_bounds", k.device, stream, k, bounds, cu_seqlens_q, cu_seqlens_k, block_table, int(page_size),
+          int(new_tokens))
     return bounds
 
 
@@ -281,9 +319,8 @@ def select_pages(q, bounds, top_k, *, cu_seqlens_k, block_table, page_size, cu_s
         pages = torch.empty((*q.shape[:-2], bounds.shape[1], int(top_k)), dtype=torch.int32, device=q.device)
     elif pages.shape[-1] != top_k:
         raise ValueError("pages must hold top_k entries")
-    _call("fa8_select_pages", q.device, stream,
-          (q, bounds, pages, cu_seqlens_q, cu_seqlens_k, block_table, int(page_size), int(bool(causal)),
-           int(keep_first), int(keep_last)))
+    _call("fa8_select_pages", q.device, stream, q, bounds, pages, cu_seqlens_q, cu_seqlens_k, block_table,
+          int(page_size), int(bool(causal)), int(keep_first), int(keep_last))
     return pages
 
 
@@ -296,9 +333,8 @@ def fwd_pages(q, k, v, pages, *, cu_seqlens_k, block_table, page_size, descale_q
     if lse is None and return_lse:
         shape = (q.shape[0], q.shape[2], q.shape[1]) if q.dim() == 4 else (q.shape[1], q.shape[0])
         lse = torch.empty(shape, dtype=torch.float32, device=q.device)
-    _call("fa8_fwd_pages", q.device, stream,
-          (q, k, v, pages, descale_q, descale_k, descale_v, out, lse, cu_seqlens_q, cu_seqlens_k, block_table,
-           int(page_size), int(bool(causal)), sink, float(softmax_scale)))
+    _call("fa8_fwd_pages", q.device, stream, q, k, v, pages, descale_q, descale_k, descale_v, out, lse, cu_seqlens_q,
+          cu_seqlens_k, block_table, int(page_size), int(bool(causal)), sink, float(softmax_scale))
     return out, lse
 
 
