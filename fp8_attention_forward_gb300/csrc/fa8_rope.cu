@@ -8,10 +8,11 @@
 // turn is the low 64 bits of an integer product: exact at every position (an fp32 angle is off
 // by 2^-24 of itself, 0.06 rad at position 2^20), and no range reduction follows.
 //
-// Bound: HBM, 2 bytes read and 1 written per element.  A thread keeps the same 16 dims of a head
-// over all heads of its tokens and loads two 16-byte groups (both halves of 8 pairs) of up to four
-// tokens before it computes; the sines of a token are computed once, into shared memory, for all
-// its heads.
+// Bound: HBM, 2 bytes read and 1 written per element; next, the instructions per element.  A thread
+// keeps the same 16 dims of a head over the heads of one token, so its 8 pairs of sines serve all of
+// them, arithmetic goes two values an instruction, and no barrier follows the loads.  Measured, 8192
+// tokens of 32 + 2 x 8 heads of 128 dims (151 MB): 31 us, 4.85 TB/s; sines through shared memory, four
+// tokens a CTA: 57 us; sincospif per pair and heads by select: 46 us; one decode token: 3.2 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -41,198 +42,283 @@ struct RopeParams {
     const float *dq, *dk, *dv;
     long long dq_s[2], dk_s[2], dv_s[2];
     int T, B, Sq, Hq, Hkv, G, D, DV;
+    unsigned int g_magic;  // ceil(2^32 / G): q-head -> kv-head
     const int *cu_q, *cu_k;  // null: batched
     int kv_mode, Sk, total_k, num_pages;
     host::Table tab;
     unsigned int *status;
 };
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 constexpr int kRopeMaxPairs = 128;
 
-__device__ __forceinline__ float2 unpack2(uint32_t x, __nv_bfloat16) {
-    return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
+// w / 2pi modulo 1 in units of 2^-64 turns, from the bits of w = M 2^(e - 63): the high word of
+// M * (2^66 / 2pi) carries e - 1 binary places.  Integers, because fp64 arithmetic is slow here.
+__device__ __forceinline__ unsigned long long turns_of(const void *freq, int f64, int i) {
+    unsigned long long M;
+    int e;
+    bool neg;
+    if (f64) {
+        const unsigned long long u = static_cast<const unsigned long long *>(freq)[i];
+        e = (int)(u >> 52) & 2047;
+        M = e ? (u << 11) | 0x8000000000000000ull : 0;
+        e -= 1023;
+        neg = u >> 63;
+    } else {
+        const unsigned int u = static_cast<const unsigned int *>(freq)[i];
+        e = (int)(u >> 23) & 255;
+        M = e ? ((unsigned long long)u << 40) | 0x8000000000000000ull : 0;
+        e -= 127;
+        neg = u >> 31;
+    }
+    const unsigned long long hi = __umul64hi(M, 0xA2F9836E4E44152Aull);  // 2^66 / 2pi
+    const unsigned long long t = e <= 1 ? (1 - e < 64 ? hi >> (1 - e) : 0) : (e - 1 < 64 ? hi << (e - 1) : 0);
+    return neg ? 0 - t : t;
 }
-__device__ __forceinline__ float2 unpack2(uint32_t x, __half) {
+
+__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// Cosine and sine of two angles given in 2^-32 turns.  The nearest quarter turn is split off as an
+// integer; the rest, at most pi / 4, goes through the Taylor series to x^9 and x^8 (truncated below
+// 2e-9 and 3e-8), two angles per packed instruction.
+__device__ __forceinline__ void cossin2(unsigned int ph0, unsigned int ph1, uint64_t &co, uint64_t &si) {
+    const unsigned int q0 = (ph0 + 0x20000000u) >> 30, q1 = (ph1 + 0x20000000u) >> 30;
+    constexpr float kUnit = 1.4629180792671596e-9f;  // 2 pi / 2^32
+    const uint64_t x = fmul2(ptx::f2pack((float)(int)(ph0 - (q0 << 30)), (float)(int)(ph1 - (q1 << 30))), ptx::f2pack(kUnit, kUnit));
+    const uint64_t z = fmul2(x, x);
+    auto both = [](float v) { return ptx::f2pack(v, v); };
+    uint64_t s = ptx::ffma2(z, both(1.f / 362880.f), both(-1.f / 5040.f));
+    s = ptx::ffma2(z, s, both(1.f / 120.f));
+    s = ptx::ffma2(z, s, both(-1.f / 6.f));
+    s = ptx::ffma2(fmul2(x, z), s, x);
+    uint64_t c = ptx::ffma2(z, both(1.f / 40320.f), both(-1.f / 720.f));
+    c = ptx::ffma2(z, c, both(1.f / 24.f));
+    c = ptx::ffma2(z, c, both(-0.5f));
+    c = ptx::ffma2(z, c, both(1.f));
+    float s0, s1, c0, c1;
+    ptx::f2unpack(s, s0, s1);
+    ptx::f2unpack(c, c0, c1);
+    // quarter turns: odd ones swap the two, the sine is negative in 2 and 3, the cosine in 1 and 2
+    auto flip = [](float v, unsigned int q) { return __uint_as_float(__float_as_uint(v) ^ ((q & 2u) << 30)); };
+    co = ptx::f2pack(flip(q0 & 1 ? s0 : c0, q0 + 1), flip(q1 & 1 ? s1 : c1, q1 + 1));
+    si = ptx::f2pack(flip(q0 & 1 ? c0 : s0, q0), flip(q1 & 1 ? c1 : s1, q1));
+}
+
+// A 16-bit pair as two fp32 in one 64-bit register (the low half first).
+__device__ __forceinline__ uint64_t widen2(uint32_t x, __nv_bfloat16) {
+    return ptx::f2pack(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint64_t widen2(uint32_t x, __half) {
     float lo, hi;
     ptx::h2_to_f32(x, lo, hi);
-    return make_float2(lo, hi);
+    return ptx::f2pack(lo, hi);
+}
+// four fp32 (two pairs) -> four E4M3 bytes
+__device__ __forceinline__ uint32_t round4(uint64_t a, uint64_t b) {
+    float a0, a1, b0, b1;
+    ptx::f2unpack(a, a0, a1);
+    ptx::f2unpack(b, b0, b1);
+    return ptx::prmt_lo16(ptx::cvt_e4m3x2(a1, a0), ptx::cvt_e4m3x2(b1, b0));
 }
 
-// One CTA: TB consecutive tokens.  blockDim = (D / 16, 256 / (D / 16)): x = 16 dims of a head, y
-// (with grid y) = head among Hq q-heads, Hkv k-heads, Hkv v-heads.
-template <typename T, bool INTER, int TB>
-__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_constant__ RopeParams p) {
-    __shared__ unsigned long long turn[kRopeMaxPairs];  // w / 2pi, 2^-64 turns
-    __shared__ float2 cs[TB][kRopeMaxPairs];
-    __shared__ long long s_q[TB], s_k[TB], s_v[TB], s_qo[TB], s_ko[TB], s_vo[TB];
-    __shared__ int s_pos[TB], s_b[TB];
-    const int tid = threadIdx.y * blockDim.x + threadIdx.x;
-    const int nthreads = blockDim.x * blockDim.y;
-    const int pairs = p.rot >> 1;
-    for (int i = tid; i < pairs; i += nthreads) {
-        double f = p.freq_f64 ? static_cast<const double *>(p.inv_freq)[i]
-                              : (double)static_cast<const float *>(p.inv_freq)[i];
-        f *= 0.15915494309189533577;
-        f -= floor(f);  // positions are whole numbers: whole turns per position drop out
-        turn[i] = (unsigned long long)(f * 18446744073709551616.0);
-    }
-    if (tid < TB) {
-        const long long tok = (long long)blockIdx.x * TB + tid;
-        int b = -1, i = 0, Lq = 0, kstart = 0, Lk = 0, pos = 0;
-        long long ko = -1, vo = -1;
-        if (tok < p.T && locate_token(p.cu_q, p.B, p.Sq, (int)tok, &b, &i, &Lq)) {
-            if (p.kv_mode == 0) {
-                Lk = p.Sk;
-            } else {
-                kstart = p.cu_k[b];
-                Lk = p.cu_k[b + 1] - kstart;
-            }
-            const int j = Lk - Lq + i;  // key index of this token
-            bool ok = j >= 0;
-            long long outer = 0, row = 0;
-            if (ok) {
-                if (p.kv_mode == 2) {
-                    const int pi = j / p.tab.page_size;
-                    int page = -1;
-                    if (pi < p.tab.max_pages) page = p.tab.bt[(long long)b * p.tab.bt_stride + pi];
-                    ok = page >= 0 && page < p.num_pages;
-                    outer = page;
-                    row = j - pi * p.tab.page_size;
-                } else if (p.kv_mode == 1) {
-                    row = (long long)kstart + j;
-                    ok = kstart >= 0 && row < p.total_k;
-                } else {
-                    outer = b;
-                    row = j;
-                }
-            }
-            if (ok) {
-                ko = outer * p.ko_s[0] + row * p.ko_s[1];
-                vo = outer * p.vo_s[0] + row * p.vo_s[1];
-            } else {
-                atomicOr(p.status, kStatusBounds);
-            }
-            const long long bb = p.cu_q ? 0 : b, tt = p.cu_q ? tok : i;
-            s_q[tid] = bb * p.q_s[0] + tt * p.q_s[1];
-            s_k[tid] = bb * p.k_s[0] + tt * p.k_s[1];
-            s_v[tid] = bb * p.v_s[0] + tt * p.v_s[1];
-            s_qo[tid] = bb * p.qo_s[0] + tt * p.qo_s[1];
-            pos = p.pos ? p.pos[bb * p.pos_s[0] + tt * p.pos_s[1]] : j;
-        } else {
-            b = -1;
+// Rotates (ROT), scales and rounds one thread's 16 dims: two groups of 8, `gap` apart.
+template <typename T, bool INTER, bool ROT>
+__device__ __forceinline__ void rope_store(uint8_t *dst, int gap, const uint4 &ra, const uint4 &rb, float inv,
+                                           const uint64_t (&cc)[INTER ? 8 : 4], const uint64_t (&ss)[INTER ? 8 : 4],
+                                           const uint64_t (&ns)[INTER ? 1 : 4]) {
+    const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
+    const uint64_t sc = ptx::f2pack(inv, inv);
+    uint64_t a[4], c[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        a[e] = widen2(wa[e], T());
+        c[e] = widen2(wb[e], T());
+        if constexpr (ROT && INTER) {  // (x0, x1) {c, c} + (x1, x0) {-s, s}
+            float x0, x1;
+            ptx::f2unpack(a[e], x0, x1);
+            a[e] = ptx::ffma2(a[e], cc[e], fmul2(ptx::f2pack(x1, x0), ss[e]));
+            ptx::f2unpack(c[e], x0, x1);
+            c[e] = ptx::ffma2(c[e], cc[4 + e], fmul2(ptx::f2pack(x1, x0), ss[4 + e]));
+        } else if constexpr (ROT) {
+            const uint64_t y = ptx::ffma2(a[e], cc[e], fmul2(c[e], ns[e]));
+            c[e] = ptx::ffma2(a[e], ss[e], fmul2(c[e], cc[e]));
+            a[e] = y;
         }
-        s_ko[tid] = ko;
-        s_vo[tid] = vo;
-        s_pos[tid] = pos;
-        s_b[tid] = b;
+        a[e] = fmul2(a[e], sc);
+        c[e] = fmul2(c[e], sc);
     }
-    __syncthreads();
-    for (int i = tid; i < TB * pairs; i += nthreads) {
-        const int t = TB == 1 ? 0 : i / pairs, pr = TB == 1 ? i : i - t * pairs;
-        const unsigned long long ph = (unsigned long long)(long long)s_pos[t] * turn[pr];
-        float sn, cn;
-        sincospif((float)(int)(ph >> 32) * 0x1p-31f, &sn, &cn);
-        cs[t][pr] = make_float2(cn * p.rot_scale, sn * p.rot_scale);
-    }
-    __syncthreads();
+    *reinterpret_cast<uint2 *>(dst) = make_uint2(round4(a[0], a[1]), round4(a[2], a[3]));
+    *reinterpret_cast<uint2 *>(dst + gap) = make_uint2(round4(c[0], c[1]), round4(c[2], c[3]));
+}
 
-    const int x = threadIdx.x;
-    // this thread's two groups of 8 dims: both halves of 8 pairs, or 16 dims that pass through
-    int da, db, pr = -1;
-    const int ritems = p.rot >> 4;
-    const int first = p.rot_off >> 3;  // 8-dim groups ahead of the rotated ones
-    if (x < ritems) {
-        if (INTER) {
-            da = p.rot_off + 16 * x;
-            db = da + 8;
-        } else {
-            da = p.rot_off + 8 * x;
-            db = da + (p.rot >> 1);
-        }
-        pr = 8 * x;
+// A thread: 16 dims (x) of every blockDim.y-th head of one token.  blockDim = (D / 16, head lanes,
+// tokens).  The loads of its first K and V head and of a batch of NB q-heads go out first; the angles
+// of its 8 pairs, shared by all heads, and the cache slot are computed while they are in flight.
+template <typename T, bool INTER, int NB>
+__global__ void __launch_bounds__(kRopeThreads, 5) rope_append_kernel(const __grid_constant__ RopeParams p) {
+    __shared__ __align__(16) unsigned long long turn[kRopeMaxPairs];
+    const int x = threadIdx.x, Y = blockDim.y * gridDim.y;
+    const int y = blockIdx.y * blockDim.y + threadIdx.y;
+    const int tid = (threadIdx.z * blockDim.y + threadIdx.y) * blockDim.x + x;
+    const long long tok = (long long)blockIdx.x * blockDim.z + threadIdx.z;
+
+    // ---- this thread's two groups of 8 dims: both halves of 8 pairs, or 16 dims that pass through
+    int da, gap;
+    const bool rotated = x < (p.rot >> 4);
+    if (rotated) {
+        da = p.rot_off + (INTER ? 16 : 8) * x;
+        gap = INTER ? 8 : p.rot >> 1;
     } else {
-        const int g = 2 * (x - ritems);
+        const int g = 2 * (x - (p.rot >> 4)), first = p.rot_off >> 3;  // 8-dim groups ahead of the rotated ones
         da = 8 * g + (g < first ? 0 : p.rot);
-        db = 8 * (g + 1) + (g + 1 < first ? 0 : p.rot);
+        gap = 8 * (g + 1) + (g + 1 < first ? 0 : p.rot) - da;
     }
-    const int heads = p.Hq + 2 * p.Hkv;
-    for (int h = blockIdx.y * blockDim.y + threadIdx.y; h < heads; h += gridDim.y * blockDim.y) {
-        const int kind = h < p.Hq ? 0 : (h < p.Hq + p.Hkv ? 1 : 2);
-        const int hh = kind == 0 ? h : (kind == 1 ? h - p.Hq : h - p.Hq - p.Hkv);
-        if (kind == 2 && 16 * x >= p.DV) continue;
-        const int a0 = kind == 2 ? 16 * x : da, b0 = kind == 2 ? a0 + 8 : db;
-        const T *src = static_cast<const T *>(kind == 0 ? p.q : (kind == 1 ? p.k : p.v)) +
-                       hh * (kind == 0 ? p.q_s[2] : (kind == 1 ? p.k_s[2] : p.v_s[2]));
-        uint8_t *dst = kind == 0 ? p.qo + hh * p.qo_s[2] : (kind == 1 ? p.ko + hh * p.ko_s[2] : p.vo + hh * p.vo_s[2]);
-        const float *ds = kind == 0 ? p.dq : (kind == 1 ? p.dk : p.dv);
-        const long long *ds_s = kind == 0 ? p.dq_s : (kind == 1 ? p.dk_s : p.dv_s);
-        const int g = kind == 0 ? hh / p.G : hh;
-        const long long *from = kind == 0 ? s_q : (kind == 1 ? s_k : s_v);
-        const long long *to = kind == 0 ? s_qo : (kind == 1 ? s_ko : s_vo);
-        uint4 ra[TB], rb[TB];
-        float inv[TB];
-#pragma unroll
-        for (int t = 0; t < TB; ++t) {
-            const int b = s_b[t];
-            if (b < 0) continue;
-            ra[t] = __ldg(reinterpret_cast<const uint4 *>(src + from[t] + a0));
-            rb[t] = __ldg(reinterpret_cast<const uint4 *>(src + from[t] + b0));
-            inv[t] = ds ? 1.f / ds[b * ds_s[0] + g * ds_s[1]] : 1.f;
+    int b = 0, i = 0, Lq = 0;
+    const bool live = tok < p.T && locate_token(p.cu_q, p.B, p.Sq, (int)tok, &b, &i, &Lq);
+    const long long bb = p.cu_q ? 0 : b, tt = p.cu_q ? tok : i;
+    auto load = [](const T *s, int gap, uint4 &a, uint4 &b) {
+        a = __ldcs(reinterpret_cast<const uint4 *>(s));
+        b = __ldcs(reinterpret_cast<const uint4 *>(s + gap));
+    };
+    const T *sq = static_cast<const T *>(p.q) + bb * p.q_s[0] + tt * p.q_s[1] + y * p.q_s[2] + da;
+    const T *sk = static_cast<const T *>(p.k) + bb * p.k_s[0] + tt * p.k_s[1] + y * p.k_s[2] + da;
+    const T *sv = static_cast<const T *>(p.v) + bb * p.v_s[0] + tt * p.v_s[1] + y * p.v_s[2] + 16 * x;
+    const long long step_q = Y * p.q_s[2];
+    uint4 ka, kb, va, vb, qa[NB], qb[NB];
+    float kd = 1.f, vd = 1.f, qd[NB];
+    auto descale = [&](const float *d, const long long *s, int h) { return d ? __ldg(d + b * s[0] + h * s[1]) : 1.f; };
+    auto group = [&](int h) { return p.G == 1 ? h : (int)__umulhi((unsigned)h, p.g_magic); };
+    const bool has_v = 16 * x < p.DV;
+    if (live) {
+        if (y < p.Hkv) {
+            load(sk, gap, ka, kb);
+            kd = descale(p.dk, p.dk_s, y);
+            if (has_v) load(sv, 8, va, vb);
+            vd = descale(p.dv, p.dv_s, y);
         }
 #pragma unroll
-        for (int t = 0; t < TB; ++t) {
-            if (s_b[t] < 0 || to[t] < 0) continue;
-            const uint32_t wa[4] = {ra[t].x, ra[t].y, ra[t].z, ra[t].w};
-            const uint32_t wb[4] = {rb[t].x, rb[t].y, rb[t].z, rb[t].w};
-            float a[8], b[8];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 u = unpack2(wa[e], T()), w = unpack2(wb[e], T());
-                a[2 * e] = u.x;
-                a[2 * e + 1] = u.y;
-                b[2 * e] = w.x;
-                b[2 * e + 1] = w.y;
+        for (int k = 0; k < NB; ++k)
+            if (y + k * Y < p.Hq) {
+                load(sq + k * step_q, gap, qa[k], qb[k]);
+                qd[k] = descale(p.dq, p.dq_s, group(y + k * Y));
             }
-            if (kind != 2 && pr >= 0) {
+    }
+    for (int k = tid; k < (p.rot >> 1); k += blockDim.x * blockDim.y * blockDim.z) turn[k] = turns_of(p.inv_freq, p.freq_f64, k);
+    __syncthreads();
+    if (!live) return;
+    // ---- cache slot and position
+    int kstart = 0, Lk = p.Sk;
+    if (p.kv_mode != 0) {
+        kstart = p.cu_k[b];
+        Lk = p.cu_k[b + 1] - kstart;
+    }
+    const int j = Lk - Lq + i;  // key index of this token
+    bool ok = j >= 0;
+    long long outer = b, row = j;
+    if (ok && p.kv_mode == 2) {
+        const int pi = j / p.tab.page_size;
+        int page = -1;
+        if (pi < p.tab.max_pages) page = p.tab.bt[(long long)b * p.tab.bt_stride + pi];
+        ok = page >= 0 && page < p.num_pages;
+        outer = page;
+        row = j - pi * p.tab.page_size;
+    } else if (p.kv_mode == 1) {
+        outer = 0;
+        row = (long long)kstart + j;
+        ok = ok && kstart >= 0 && row < p.total_k;
+    }
+    if (!ok && x == 0 && y == 0) atomicOr(p.status, kStatusBounds);
+    // ---- cosines and sines of its 8 pairs, packed as rope_store takes them
+    uint64_t cc[INTER ? 8 : 4] = {}, ss[INTER ? 8 : 4] = {}, ns[INTER ? 1 : 4] = {};
+    if (rotated) {
+        const int pos = p.pos ? p.pos[bb * p.pos_s[0] + tt * p.pos_s[1]] : j;
+        const uint64_t rs = ptx::f2pack(p.rot_scale, p.rot_scale);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float2 c = cs[t][pr + e];
-                    float &x0 = INTER ? (e < 4 ? a[2 * e] : b[2 * e - 8]) : a[e];
-                    float &x1 = INTER ? (e < 4 ? a[2 * e + 1] : b[2 * e - 7]) : b[e];
-                    const float y0 = x0 * c.x - x1 * c.y, y1 = x0 * c.y + x1 * c.x;
-                    x0 = y0;
-                    x1 = y1;
+        for (int e = 0; e < 4; ++e) {
+            unsigned int ph[2];
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {  // position * turn, the upper half of its fraction
+                const unsigned long long w = turn[8 * x + 2 * e + f];
+                ph[f] = __umulhi((unsigned)pos, (unsigned)w) + (unsigned)pos * (unsigned)(w >> 32);
+                if (pos < 0) ph[f] -= (unsigned)w;
+            }
+            uint64_t co, si;
+            cossin2(ph[0], ph[1], co, si);
+            co = fmul2(co, rs);
+            si = fmul2(si, rs);
+            float s0, s1, c0, c1;
+            ptx::f2unpack(si, s0, s1);
+            ptx::f2unpack(co, c0, c1);
+            if constexpr (INTER) {
+                cc[2 * e] = ptx::f2pack(c0, c0);
+                cc[2 * e + 1] = ptx::f2pack(c1, c1);
+                ss[2 * e] = ptx::f2pack(-s0, s0);
+                ss[2 * e + 1] = ptx::f2pack(-s1, s1);
+            } else {
+                cc[e] = co;
+                ss[e] = si;
+                ns[e] = ptx::f2pack(-s0, -s1);
+            }
+        }
+    }
+    auto store = [&](uint8_t *dst, const uint4 &a, const uint4 &c, float d) {
+        const float inv = __fdividef(1.f, d);
+        if (rotated) rope_store<T, INTER, true>(dst, gap, a, c, inv, cc, ss, ns);
+        else rope_store<T, INTER, false>(dst, gap, a, c, inv, cc, ss, ns);
+    };
+    if (ok) {
+        uint8_t *dk = p.ko + outer * p.ko_s[0] + row * p.ko_s[1] + da;
+        uint8_t *dv = p.vo + outer * p.vo_s[0] + row * p.vo_s[1] + 16 * x;
+        for (int h = y; h < p.Hkv; h += Y) {
+            store(dk + h * p.ko_s[2], ka, kb, kd);
+            if (has_v) rope_store<T, INTER, false>(dv + h * p.vo_s[2], 8, va, vb, __fdividef(1.f, vd), cc, ss, ns);
+            if (h + Y < p.Hkv) {
+                sk += Y * p.k_s[2];
+                sv += Y * p.v_s[2];
+                load(sk, gap, ka, kb);
+                kd = descale(p.dk, p.dk_s, h + Y);
+                if (has_v) load(sv, 8, va, vb);
+                vd = descale(p.dv, p.dv_s, h + Y);
+            }
+        }
+    }
+    uint8_t *dq = p.qo + bb * p.qo_s[0] + tt * p.qo_s[1] + y * p.qo_s[2] + da;
+    const long long step_o = Y * p.qo_s[2];
+    for (int h = y; h < p.Hq; h += NB * Y) {
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+            if (h + k * Y < p.Hq) {
+                store(dq, qa[k], qb[k], qd[k]);
+                if (h + (k + NB) * Y < p.Hq) {
+                    load(sq + (k + NB) * step_q, gap, qa[k], qb[k]);
+                    qd[k] = descale(p.dq, p.dq_s, group(h + (k + NB) * Y));
                 }
             }
-            uint32_t oa[2], ob[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                oa[e] = ptx::prmt_lo16(ptx::cvt_e4m3x2(a[4 * e + 1] * inv[t], a[4 * e] * inv[t]),
-                                       ptx::cvt_e4m3x2(a[4 * e + 3] * inv[t], a[4 * e + 2] * inv[t]));
-                ob[e] = ptx::prmt_lo16(ptx::cvt_e4m3x2(b[4 * e + 1] * inv[t], b[4 * e] * inv[t]),
-                                       ptx::cvt_e4m3x2(b[4 * e + 3] * inv[t], b[4 * e + 2] * inv[t]));
-            }
-            *reinterpret_cast<uint2 *>(dst + to[t] + a0) = make_uint2(oa[0], oa[1]);
-            *reinterpret_cast<uint2 *>(dst + to[t] + b0) = make_uint2(ob[0], ob[1]);
+            dq += step_o;
         }
+        sq += NB * step_q;
     }
+}
+
+template <typename T, bool INTER, int NB>
+cudaError_t launch_rope_batch(const RopeParams &p, int lanes, int spread, cudaStream_t s) {
+    const int xs = p.D / 16;
+    const int ys = std::max(1, std::min(lanes, kRopeThreads / xs)), zs = kRopeThreads / (xs * ys);
+    const dim3 grid((unsigned)(((long long)p.T + zs - 1) / zs), (unsigned)((spread + ys - 1) / ys));
+    rope_append_kernel<T, INTER, NB><<<grid, dim3(xs, ys, zs), 0, s>>>(p);
+    return cudaGetLastError();
 }
 
 template <typename T, bool INTER>
 cudaError_t launch_rope(const RopeParams &p, int sm_count, cudaStream_t s) {
-    const int ipt = p.D / 16;
-    const dim3 block(ipt, kRopeThreads / ipt);
-    const int heads = p.Hq + 2 * p.Hkv;
-    // Few tokens: one per CTA and the heads split over CTAs, so that a decode step's loads are all
-    // in flight at once.  Many: four per CTA share the fixed-point frequencies.
-    if (p.T <= 4 * sm_count) {
-        const dim3 grid(p.T, (heads + block.y - 1) / block.y);
-        rope_append_kernel<T, INTER, 1><<<grid, block, 0, s>>>(p);
-    } else {
-        rope_append_kernel<T, INTER, 4><<<dim3((p.T + 3) / 4, 1), block, 0, s>>>(p);
-    }
-    return cudaGetLastError();
+    // Many tokens: as many head lanes as kv-heads (at most eight), so that a thread's q-heads share its
+    // angles.  Few: a lane per q-head, and the heads over several CTAs, to shorten the chain.
+    if (p.T >= sm_count) return launch_rope_batch<T, INTER, 2>(p, std::min(p.Hkv, 8), 1, s);
+    return launch_rope_batch<T, INTER, 1>(p, p.Hq, p.Hq, s);
 }
 
 }  // namespace fa8
@@ -353,6 +439,7 @@ fa8_status fa8_rope_append(const fa8_tensor *q, const fa8_tensor *k, const fa8_t
     p.Hq = (int)Hq;
     p.Hkv = (int)Hkv;
     p.G = (int)(Hq / Hkv);
+    p.g_magic = p.G > 1 ? (unsigned)((0x100000000ull + p.G - 1) / p.G) : 0u;
     p.D = (int)D;
     p.DV = (int)DV;
     // ---- rotation
