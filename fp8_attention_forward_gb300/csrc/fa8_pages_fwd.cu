@@ -50,6 +50,12 @@ struct PagesParams {
     unsigned int *status;
 };
 
+#ifndef MB
+#define MB 4
+#endif
+#ifndef CSF
+#define CSF 4
+#endif
 constexpr int kPgWarps = 4, kPgThreads = kPgWarps * 32;
 constexpr int kPgMaxCluster = 8;
 
@@ -66,9 +72,26 @@ struct PgCfg {
     // a lane's DV / 8 bytes of a V row: runs of 16, 8 and 4 bytes at 128-, 64- and 32-byte blocks
     static constexpr int NV16 = DV / 128, NV8 = (DV % 128) / 64, NV4 = (DV % 64) / 32;
     static constexpr int OPITCH = DV + 4;             // floats per row of a merge buffer
+    // a K row is D / 16 pieces of 16 bytes; KI copies per lane bring 8 rows
+    // (eight consecutive lanes read 128 consecutive bytes: one line, one request); V likewise
+    static constexpr int KP = D / 16, KI = (8 * KP + 31) / 32;
+    static constexpr int VP = DV / 16, VI = (8 * VP + 31) / 32;
+    static constexpr int K_STAGE = KC * D, V_STAGE = KC * DV, STAGE = K_STAGE + V_STAGE;
     static constexpr int Q_BYTES = NT * STEPS * 32 * 8;
     static constexpr int MERGE_BYTES = kPgWarps * ROWS * (OPITCH + 2) * 4;
-    static int smem(int K) { return std::max(Q_BYTES + ((K * 8 + 15) & ~15), MERGE_BYTES); }
+    static constexpr int OFF_Q = kPgWarps * STAGE, OFF_ENT = OFF_Q + Q_BYTES;
+    static int smem(int K) { return std::max(OFF_ENT + ((K * 8 + 15) & ~15), MERGE_BYTES); }
+    // byte offset of piece `ch` of K row `row` (0 .. KC - 1) in a stage: rows a multiple of 128 bytes
+    // long alternate their halves, so that the four lanes of two rows read different banks
+    static __device__ __forceinline__ int k_at(int row, int ch) {
+        return row * D + 16 * (D % 128 == 0 ? ch ^ ((row & 1) << 2) : ch);
+    }
+    // and of V row `row`: a lane reads piece r of rows 2c and 2c + 1, so pairs of rows are spread by c
+    static __device__ __forceinline__ int v_at(int row, int ch) {
+        const int g = (row >> 1) & 3;
+        if (DV == 96) return row * DV + 16 * ch;
+        return row * DV + 16 * (ch < DV / 128 * 8 ? ch ^ (g << 1) : ch ^ g);
+    }
 };
 
 // dv index of slot s (0 .. DV / 8 - 1) of the lane with row r
@@ -81,7 +104,7 @@ __device__ __forceinline__ int slot_dv(int s, int r) {
 }
 
 template <int D, int DV, int NT>
-__global__ void __launch_bounds__(kPgThreads) fwd_pages_kernel(const __grid_constant__ PagesParams p) {
+__global__ void __launch_bounds__(kPgThreads, D + DV <= 256 && NT == 1 ? MB : 1) fwd_pages_kernel(const __grid_constant__ PagesParams p) {
     using C = PgCfg<D, DV, NT>;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ int s_used;
@@ -108,8 +131,8 @@ __global__ void __launch_bounds__(kPgThreads) fwd_pages_kernel(const __grid_cons
     const int rows = min(C::ROWS, p.G - rb * C::ROWS);  // real rows
 
     // ---- the list: page and first key of every entry (page -1: nothing visible in it)
-    uint2 *qf = reinterpret_cast<uint2 *>(smem);
-    int2 *ent = reinterpret_cast<int2 *>(smem + C::Q_BYTES);
+    uint2 *qf = reinterpret_cast<uint2 *>(smem + C::OFF_Q);
+    int2 *ent = reinterpret_cast<int2 *>(smem + C::OFF_ENT);
     if (tid == 0) s_used = 0;
     __syncthreads();
     {
@@ -153,8 +176,84 @@ __global__ void __launch_bounds__(kPgThreads) fwd_pages_kernel(const __grid_cons
     const float dqv = p.dq ? p.dq[b * p.dq_s[0] + kvh * p.dq_s[1]] : 1.f;
     const float dkv = p.dk ? p.dk[b * p.dk_s[0] + kvh * p.dk_s[1]] : 1.f;
     const float cs = p.scale_log2 * dqv * dkv;
-    const uint8_t *kb = p.k + (long long)kvh * p.k_s[2] + (long long)r * p.k_s[1] + c * C::VK;
-    const uint8_t *vb = p.v + (long long)kvh * p.v_s[2] + (long long)(2 * c) * p.v_s[1];
+
+    // ---- the warp's chunk buffer, one of K and one of V: chunk it is groups first + it * stride ..
+    // + NG - 1, K fetched while the chunk before goes through softmax and PV, V during PV and S^T
+    const int first = (warp * CS + rank) * C::NG, stride = C::NG * CS * kPgWarps;
+    const uint32_t ks = ptx::smem_u32(smem) + warp * C::STAGE, vs = ks + C::K_STAGE;
+    const uint8_t *kb = p.k + (long long)kvh * p.k_s[2], *vb = p.v + (long long)kvh * p.v_s[2];
+    long long koff[C::KI];  // this lane's pieces of an 8-row group of K, in the pool and in the buffer
+    int krow[C::KI], kdst[C::KI];
+#pragma unroll
+    for (int u = 0; u < C::KI; ++u) {
+        const int x = 32 * u + lane, ch = x % C::KP;
+        krow[u] = x / C::KP;  // 8 or more: no piece
+        koff[u] = krow[u] * p.k_s[1] + 16 * ch;
+        kdst[u] = C::k_at(krow[u], ch);
+    }
+    long long voff[C::VI];
+    int vrow[C::VI], vdst[C::VI];
+#pragma unroll
+    for (int u = 0; u < C::VI; ++u) {
+        const int x = 32 * u + lane, ch = x % C::VP;
+        vrow[u] = x / C::VP;
+        voff[u] = vrow[u] * p.v_s[1] + 16 * ch;
+        vdst[u] = C::v_at(vrow[u], ch);
+    }
+    // lane i (mod NG) holds of group i of a chunk: its rows in the pool, how many keys are visible
+    long long ko, vo;
+    int lim;
+    bool full;  // of every group: all eight
+    auto locate = [&](int it) {
+        const int g = first + it * stride + (lane & (C::NG - 1));
+        ko = vo = 0;
+        lim = 0;
+        if (g < groups) {
+            const int e = gpp == 1 ? g : (int)__umulhi((unsigned)g, p.group_magic);
+            const int off = (g - e * gpp) * 8;
+            const int2 en = ent[e];
+            if (en.x >= 0) {
+                lim = vis - en.y - off;
+                ko = en.x * p.k_s[0] + off * p.k_s[1];
+                vo = en.x * p.v_s[0] + off * p.v_s[1];
+            }
+        }
+        full = __all_sync(0xffffffffu, lim >= 8);
+    };
+    auto fetch_k = [&]() {
+#pragma unroll
+        for (int i = 0; i < C::NG; ++i) {
+            const uint8_t *src = kb + __shfl_sync(0xffffffffu, ko, i);
+            const int li = full ? 8 : __shfl_sync(0xffffffffu, lim, i);
+#pragma unroll
+            for (int u = 0; u < C::KI; ++u)
+                if (8 * C::KP % 32 == 0 || krow[u] < 8) {
+                    const bool on = full || krow[u] < li;
+                    cp_async16(ks + 8 * i * D + kdst[u], on ? src + koff[u] : p.k, on ? 16 : 0);
+                }
+        }
+    };
+    auto fetch_v = [&]() {
+#pragma unroll
+        for (int i = 0; i < C::NG; ++i) {
+            const uint8_t *src = vb + __shfl_sync(0xffffffffu, vo, i);
+            const int li = full ? 8 : __shfl_sync(0xffffffffu, lim, i);
+#pragma unroll
+            for (int u = 0; u < C::VI; ++u)
+                if (8 * C::VP % 32 == 0 || vrow[u] < 8) {
+                    const bool on = full || vrow[u] < li;
+                    cp_async16(vs + 8 * i * DV + vdst[u], on ? src + voff[u] : p.v, on ? 16 : 0);
+                }
+        }
+    };
+    const int chunks = groups > first ? (groups - first + stride - 1) / stride : 0;
+    if (chunks > 0) {
+        locate(0);
+        fetch_k();
+        cp_async_commit();
+        fetch_v();
+    }
+    cp_async_commit();
 
     float m[NT][2], l[NT][2];  // running maximum (log2 units) and this lane's share of the sum, rows 2c, 2c + 1
     float o[C::DT][NT][4];
@@ -172,71 +271,25 @@ __global__ void __launch_bounds__(kPgThreads) fwd_pages_kernel(const __grid_cons
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[d][t][e] = 0.f;
 
-    for (int g0 = (warp * CS + rank) * C::NG; g0 < groups; g0 += C::NG * CS * kPgWarps) {
-        // the chunk's groups: row offsets and how many of the 8 keys are visible
-        long long ko[C::NG], vo[C::NG];
-        int lim[C::NG];
-#pragma unroll
-        for (int i = 0; i < C::NG; ++i) {
-            const int g = g0 + i;
-            lim[i] = 0;
-            ko[i] = vo[i] = 0;
-            if (g < groups) {
-                const int e = gpp == 1 ? g : (int)__umulhi((unsigned)g, p.group_magic);
-                const int off = (g - e * gpp) * 8;
-                const int2 en = ent[e];
-                if (en.x >= 0) {
-                    lim[i] = vis - en.y - off;
-                    ko[i] = en.x * p.k_s[0] + off * p.k_s[1];
-                    vo[i] = en.x * p.v_s[0] + off * p.v_s[1];
-                }
-            }
-        }
-        Bytes<C::VK> kr[C::NG][C::NKV];
-#pragma unroll
-        for (int i = 0; i < C::NG; ++i)
-#pragma unroll
-            for (int j = 0; j < C::NKV; ++j) {
-                if (r < lim[i]) kr[i][j] = ld_stream<C::VK>(kb + ko[i] + j * 4 * C::VK);
-                else kr[i][j] = Bytes<C::VK>{};
-            }
-        uint32_t vr[C::NG][2][DV / 32];
-#pragma unroll
-        for (int i = 0; i < C::NG; ++i)
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                const uint8_t *src = vb + vo[i] + y * p.v_s[1];
-                if (2 * c + y < lim[i]) {
-#pragma unroll
-                    for (int j = 0; j < C::NV16; ++j) {
-                        const Bytes<16> x = ld_stream<16>(src + 128 * j + 16 * r);
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) vr[i][y][4 * j + w] = x.w[w];
-                    }
-                    if constexpr (C::NV8 > 0) {
-                        const Bytes<8> x = ld_stream<8>(src + 128 * C::NV16 + 8 * r);
-                        vr[i][y][4 * C::NV16] = x.w[0];
-                        vr[i][y][4 * C::NV16 + 1] = x.w[1];
-                    }
-                    if constexpr (C::NV4 > 0) {
-                        const Bytes<4> x = ld_stream<4>(src + 128 * C::NV16 + 64 * C::NV8 + 4 * r);
-                        vr[i][y][4 * C::NV16 + 2 * C::NV8] = x.w[0];
-                    }
-                } else {
-#pragma unroll
-                    for (int w = 0; w < DV / 32; ++w) vr[i][y][w] = 0u;
-                }
-            }
+    for (int it = 0; it < chunks; ++it) {
+        cp_async_wait<1>();
+        __syncwarp();
         // ---- S^T
-        float s[C::MT][NT][4];
+        float s[C::MT][NT][4], s2[C::MT][NT][4];  // two sums each: shorter chains of dependent MMAs
 #pragma unroll
         for (int x = 0; x < C::MT; ++x)
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[x][t][e] = 0.f;
+                for (int e = 0; e < 4; ++e) s[x][t][e] = s2[x][t][e] = 0.f;
 #pragma unroll
-        for (int j = 0; j < C::NKV; ++j)
+        for (int j = 0; j < C::NKV; ++j) {
+            Bytes<C::VK> kr[C::NG];
+#pragma unroll
+            for (int i = 0; i < C::NG; ++i) {
+                const int at = C::VK == 16 ? C::k_at(8 * i + r, 4 * j + c) : (8 * i + r) * D + 32 * j + 8 * c;
+                kr[i] = ld_shared<C::VK>(ks + at);
+            }
 #pragma unroll
             for (int w = 0; w < C::VK / 4; ++w) {
                 uint2 bf[NT];
@@ -245,73 +298,130 @@ __global__ void __launch_bounds__(kPgThreads) fwd_pages_kernel(const __grid_cons
 #pragma unroll
                 for (int x = 0; x < C::MT; ++x) {
                     uint32_t a0, a1, a2, a3;
-                    e4m3x4_to_h2(kr[2 * x][j].w[w], a0, a2);
-                    e4m3x4_to_h2(kr[2 * x + 1][j].w[w], a1, a3);
+                    e4m3x4_to_h2(kr[2 * x].w[w], a0, a2);
+                    e4m3x4_to_h2(kr[2 * x + 1].w[w], a1, a3);
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) mma_f16(s[x][t], a0, a1, a2, a3, bf[t].x, bf[t].y);
+                    for (int t = 0; t < NT; ++t) mma_f16(w & 1 ? s2[x][t] : s[x][t], a0, a1, a2, a3, bf[t].x, bf[t].y);
                 }
             }
-        // ---- softmax: scale, mask, running maximum per row (over the lanes of equal c)
-        uint32_t pb[C::MT][NT][2];
+        }
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            float mx[2] = {-INFINITY, -INFINITY};
+        for (int x = 0; x < C::MT; ++x)
 #pragma unroll
-            for (int x = 0; x < C::MT; ++x)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float &y = s[x][t][2 * h + e];
-                        y = r < lim[2 * x + h] ? y * cs : -INFINITY;
-                        mx[e] = fmaxf(mx[e], y);
-                    }
-            float ref[2], alpha[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-#pragma unroll
-                for (int sh = 4; sh < 32; sh <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], sh));
-                const float mn = fmaxf(m[t][e], mx[e]);
-                ref[e] = mn == -INFINITY ? 0.f : mn;
-                alpha[e] = ptx::ex2(m[t][e] - ref[e]);  // 0 while nothing has been seen
-                m[t][e] = mn;
-                l[t][e] *= alpha[e];
-            }
-#pragma unroll
-            for (int d = 0; d < C::DT; ++d)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[d][t][e] *= alpha[e & 1];
+                for (int e = 0; e < 4; ++e) s[x][t][e] += s2[x][t][e];
+        // ---- softmax in log2 units of the scaled score: mask, running maximum per row (over the
+        // lanes of equal c), and O^T rescaled only when some row's maximum moved
+        if (!full) {
 #pragma unroll
             for (int x = 0; x < C::MT; ++x)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const float p0 = ptx::ex2(s[x][t][2 * h] - ref[0]), p1 = ptx::ex2(s[x][t][2 * h + 1] - ref[1]);
+                    const bool off = r >= __shfl_sync(0xffffffffu, lim, 2 * x + h);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            if (off) s[x][t][2 * h + e] = -INFINITY;
+                }
+        }
+        const bool more = it + 1 < chunks;
+        __syncwarp();  // every lane has read the K buffer
+        if (more) {
+            locate(it + 1);
+            fetch_k();
+        }
+        cp_async_commit();
+        uint32_t pb[C::MT][NT][2];
+        float mx[NT][2];
+        bool moved = false;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float y = -INFINITY;
+#pragma unroll
+                for (int x = 0; x < C::MT; ++x) y = fmaxf(y, fmaxf(s[x][t][e], s[x][t][2 + e]));
+#pragma unroll
+                for (int sh = 4; sh < 32; sh <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, sh));
+                mx[t][e] = y * cs;
+                moved |= mx[t][e] > m[t][e];
+            }
+        if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float mn = fmaxf(m[t][e], mx[t][e]);
+                    const float alpha = mn == -INFINITY ? 1.f : ptx::ex2(m[t][e] - mn);  // 0 while nothing has been seen
+                    m[t][e] = mn;
+                    l[t][e] *= alpha;
+#pragma unroll
+                    for (int d = 0; d < C::DT; ++d) {
+                        o[d][t][e] *= alpha;
+                        o[d][t][2 + e] *= alpha;
+                    }
+                }
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const float r0 = m[t][0] == -INFINITY ? 0.f : -m[t][0], r1 = m[t][1] == -INFINITY ? 0.f : -m[t][1];
+#pragma unroll
+            for (int x = 0; x < C::MT; ++x)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float p0 = ptx::ex2(fmaf(s[x][t][2 * h], cs, r0)), p1 = ptx::ex2(fmaf(s[x][t][2 * h + 1], cs, r1));
                     l[t][0] += p0;
                     l[t][1] += p1;
                     pb[x][t][h] = trans8x8(ptx::cvt_f16x2(p1, p0));
                 }
         }
         // ---- O^T
+        cp_async_wait<1>();
+        __syncwarp();
 #pragma unroll
-        for (int x = 0; x < C::MT; ++x)
+        for (int x = 0; x < C::MT; ++x) {
+            uint32_t vr[4][DV / 32];  // keys 2c, 2c + 1 of the tile's two groups
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const int row = 16 * x + 8 * (y >> 1) + 2 * c + (y & 1);
+#pragma unroll
+                for (int j = 0; j < C::NV16; ++j) {
+                    const Bytes<16> z = ld_shared<16>(vs + C::v_at(row, 8 * j + r));
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) vr[y][4 * j + w] = z.w[w];
+                }
+                if constexpr (C::NV8 > 0) {
+                    const Bytes<8> z = ld_shared<8>(vs + C::v_at(row, 8 * C::NV16 + (r >> 1)) + 8 * (r & 1));
+                    vr[y][4 * C::NV16] = z.w[0];
+                    vr[y][4 * C::NV16 + 1] = z.w[1];
+                }
+                if constexpr (C::NV4 > 0)
+                    vr[y][4 * C::NV16 + 2 * C::NV8] = ld_shared<4>(vs + C::v_at(row, 8 * C::NV16 + 4 * C::NV8 + (r >> 2)) + 4 * (r & 3)).w[0];
+            }
 #pragma unroll
             for (int w = 0; w < DV / 32; ++w) {
-                const uint32_t *k0 = vr[2 * x][0], *k1 = vr[2 * x][1], *k2 = vr[2 * x + 1][0], *k3 = vr[2 * x + 1][1];
                 uint32_t a[8];
-                e4m3x4_to_h2(zip_lo(k0[w], k1[w]), a[0], a[1]);
-                e4m3x4_to_h2(zip_hi(k0[w], k1[w]), a[2], a[3]);
-                e4m3x4_to_h2(zip_lo(k2[w], k3[w]), a[4], a[5]);
-                e4m3x4_to_h2(zip_hi(k2[w], k3[w]), a[6], a[7]);
+                e4m3x4_to_h2(zip_lo(vr[0][w], vr[1][w]), a[0], a[1]);
+                e4m3x4_to_h2(zip_hi(vr[0][w], vr[1][w]), a[2], a[3]);
+                e4m3x4_to_h2(zip_lo(vr[2][w], vr[3][w]), a[4], a[5]);
+                e4m3x4_to_h2(zip_hi(vr[2][w], vr[3][w]), a[6], a[7]);
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                     mma_f16(o[2 * w][t], a[0], a[1], a[4], a[5], pb[x][t][0], pb[x][t][1]);
                     mma_f16(o[2 * w + 1][t], a[2], a[3], a[6], a[7], pb[x][t][0], pb[x][t][1]);
                 }
             }
+        }
+        __syncwarp();  // and the V buffer
+        if (more) fetch_v();
+        cp_async_commit();
     }
 
     // ---- merge: warps through shared memory, CTAs through distributed shared memory
-    __syncthreads();  // the list and Q are done with
+    cp_async_wait<0>();
+    __syncthreads();  // the buffers, the list and Q are done with
     float *wo = reinterpret_cast<float *>(smem);                       // [warp][row][OPITCH]
     float *wm = wo + kPgWarps * C::ROWS * C::OPITCH, *wl = wm + kPgWarps * C::ROWS;  // [warp][row]
 #pragma unroll
@@ -536,7 +646,7 @@ extern "C" fa8_status fa8_fwd_pages(const fa8_tensor *q, const fa8_tensor *k, co
     // at least two chunks.
     const long long keys = (long long)p.K * page_size;
     p.cluster = 1;
-    while (p.cluster < fa8::kPgMaxCluster && tiles * p.cluster * 2 <= 4LL * ds->sm_count &&
+    while (p.cluster < fa8::kPgMaxCluster && tiles * p.cluster * 2 <= (long long)CSF * ds->sm_count &&
            keys >= 2LL * 32 * fa8::kPgWarps * p.cluster * 2)
         p.cluster *= 2;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
