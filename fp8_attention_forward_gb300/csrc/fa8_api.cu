@@ -547,6 +547,23 @@ fa8_status make_plan(const fa8_tensor *q, const fa8_tensor *k, const fa8_tensor 
 
 }  // namespace
 
+namespace fa8 {
+namespace host {
+
+fa8_status encode_kv(CUtensorMap *m, const fa8_tensor *t, int width, int rows) {
+    const uint64_t dims[4] = {(uint64_t)t->shape[3], (uint64_t)t->shape[2], (uint64_t)t->shape[1], (uint64_t)t->shape[0]};
+    const uint64_t strides[3] = {(uint64_t)t->stride[2], (uint64_t)t->stride[1], (uint64_t)t->stride[0]};
+    const uint32_t box[4] = {(uint32_t)width, 1, (uint32_t)rows, 1};
+    // no promotion past a head's own row: the next head's row belongs to another list
+    return encode4(m, t->data, dims, strides, box, width,
+                   t->shape[3] % 128 == 0 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B);
+}
+
+unsigned long long wait_timeout_ns() { return g_timeout_ns.load(); }
+
+}  // namespace host
+}  // namespace fa8
+
 extern "C" {
 
 int fa8_version(void) { return FA8_VERSION; }

@@ -2,6 +2,7 @@
 // the calling thread, per-device state, argument checks).  Defined in fa8_api.cu.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -42,6 +43,12 @@ struct Table {
     int B = 0, max_pages = 0, page_size = 0;
 };
 fa8_status check_table(const fa8_tensor *cu_k, const fa8_tensor *bt, int page_size, int B, Table *out);
+
+// TMA map of a paged K or V pool {d, head, row, page} whose boxes are `width` bytes of one head by
+// `rows` rows, with the swizzle of that width.
+fa8_status encode_kv(CUtensorMap *m, const fa8_tensor *t, int width, int rows);
+// The bound on every in-kernel wait (fa8_set_wait_timeout_ns).
+unsigned long long wait_timeout_ns();
 
 // Queries (B, Sq, Hq, D) or packed (T, Hq, D) with cu_seqlens_q; strides {request, token, head}.
 struct Queries {

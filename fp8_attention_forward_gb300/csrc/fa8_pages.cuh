@@ -87,17 +87,6 @@ __device__ __forceinline__ Bytes<N> ld_stream(const uint8_t *p) {
     return r;
 }
 
-// ---------------------------------------------------------------- asynchronous copies to shared memory
-// 16 bytes past L1; `bytes` = 0 reads nothing and writes zeros
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// waits until at most N of this thread's groups are pending
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 template <int N>
 __device__ __forceinline__ Bytes<N> ld_shared(uint32_t addr) {
     Bytes<N> r;

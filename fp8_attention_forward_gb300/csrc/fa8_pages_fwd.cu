@@ -7,12 +7,19 @@
 //   S^T (16 keys x 8 rows)  = K (M = keys, k = d) . Q^T        f16 MMAs on exactly widened E4M3
 //   O^T (16 dv x 8 rows)   += V^T (M = dv, k = keys) . P^T
 //
-// A warp works alone: it takes every (4 x cluster)-th chunk of 16 or 32 keys of the list, keeps its
-// own running maximum, sum and O^T in registers, and loads K and V fragments straight from global
-// memory (see fa8_pages.cuh); V's fragments pair the bytes of two keys with one byte permute.  P is
-// rounded to f16 (2^-11 relative; p <= 1 and the running maximum is exact, so nothing saturates),
-// not to E4M3 as in fa8_fwd: V widens to f16 anyway.  The four warps, then the CTAs of the cluster
-// through distributed shared memory, merge by their maxima, so no workspace and no second kernel.
+// A warp works alone: it takes every (warps x cluster)-th chunk of 16 or 32 keys of the list, keeps
+// its own running maximum, sum and O^T in registers, and has one K and one V buffer that TMA fills
+// (boxes of one head's rows of a page, swizzled): the next K while this chunk goes through softmax and
+// PV, the next V during PV and the next S^T.  V's fragments pair the bytes of two keys with one byte
+// permute.  P is rounded to f16 (2^-11 relative; p <= 1 and the running maximum is exact, so nothing
+// saturates), not to E4M3 as in fa8_fwd: V widens to f16 anyway.  The warps, then the CTAs of the
+// cluster through distributed shared memory, merge by their maxima: no workspace, no second kernel.
+//
+// Measured (d = dv = 128, 64 x 8 lists of 2048 keys, 267 MB): 48.5 us, 5.5 TB/s, 0.81 of the copy rate.
+// Many tokens of one request (512 x 8 lists of 2048 keys, 2.1 GB through L2): 211 us; the ALU pipe,
+// which widens E4M3 to f16, is at 62 %.  The same with fragments loaded straight to registers: 63 and
+// 303 us; by 16-byte asynchronous copies: 61 and 258 us (L2 is asked for every sector twice); QK by the
+// E4M3 warp MMA: 48.5 and 218 us (it widens too); three buffers and fewer CTAs per SM: slower.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -20,6 +27,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <numeric>
 
 #include "fa8.h"
 #include "fa8_host.h"
@@ -45,68 +53,60 @@ struct PagesParams {
     float *lse;
     long long lse_s[3];          // request, token, head
     int T, B, Sq, Hkv, G, K, causal, num_pages, cluster, row_blocks;
-    unsigned int group_magic;    // ceil(2^32 / (page_size / 8)): 8-key group -> list entry
+    int box;                     // keys of one TMA box: gcd(page_size, keys per chunk)
+    int box_shift;               // log2 of the boxes per chunk
+    unsigned int box_magic;      // ceil(2^32 / (page_size / box)): box -> list entry
+    unsigned long long timeout_ns;
     host::Table tab;
     unsigned int *status;
 };
 
-#ifndef MB
-#define MB 4
-#endif
-#ifndef CSF
-#define CSF 4
-#endif
-constexpr int kPgWarps = 4, kPgThreads = kPgWarps * 32;
 constexpr int kPgMaxCluster = 8;
 
-template <int D, int DV, int NT>
+template <int D, int DV, int NT, int PW>
 struct PgCfg {
     static constexpr int ROWS = 8 * NT;
     static constexpr int MT = D + DV <= 256 ? 2 : 1;  // 16-key tiles per chunk
     static constexpr int KC = 16 * MT;                // keys per chunk
     static constexpr int NG = 2 * MT;                 // 8-key groups per chunk
-    static constexpr int VK = D % 64 == 0 ? 16 : 8;   // bytes of one K vector load
-    static constexpr int NKV = D / (4 * VK);          // K vector loads per key and lane
+    // rows arrive as blocks of CW bytes, each block KC rows deep with the swizzle of its width
+    static constexpr int CW = D % 128 == 0 ? 128 : (D % 64 == 0 ? 64 : 32), NCK = D / CW;
+    static constexpr int CWV = DV % 128 == 0 ? 128 : (DV % 64 == 0 ? 64 : 32), NCV = DV / CWV;
+    static constexpr int VK = CW >= 64 ? 16 : 8;      // bytes of one K fragment load
+    static constexpr int NKV = D / (4 * VK);          // K fragment loads per key and lane
+    static constexpr int VB = CWV / 8;                // bytes of one V fragment load
     static constexpr int STEPS = D / 16;
     static constexpr int DT = DV / 16;                // 16-row tiles of O^T
-    // a lane's DV / 8 bytes of a V row: runs of 16, 8 and 4 bytes at 128-, 64- and 32-byte blocks
-    static constexpr int NV16 = DV / 128, NV8 = (DV % 128) / 64, NV4 = (DV % 64) / 32;
     static constexpr int OPITCH = DV + 4;             // floats per row of a merge buffer
-    // a K row is D / 16 pieces of 16 bytes; KI copies per lane bring 8 rows
-    // (eight consecutive lanes read 128 consecutive bytes: one line, one request); V likewise
-    static constexpr int KP = D / 16, KI = (8 * KP + 31) / 32;
-    static constexpr int VP = DV / 16, VI = (8 * VP + 31) / 32;
     static constexpr int K_STAGE = KC * D, V_STAGE = KC * DV, STAGE = K_STAGE + V_STAGE;
     static constexpr int Q_BYTES = NT * STEPS * 32 * 8;
-    static constexpr int MERGE_BYTES = kPgWarps * ROWS * (OPITCH + 2) * 4;
-    static constexpr int OFF_Q = kPgWarps * STAGE, OFF_ENT = OFF_Q + Q_BYTES;
-    static int smem(int K) { return std::max(OFF_ENT + ((K * 8 + 15) & ~15), MERGE_BYTES); }
-    // byte offset of piece `ch` of K row `row` (0 .. KC - 1) in a stage: rows a multiple of 128 bytes
-    // long alternate their halves, so that the four lanes of two rows read different banks
-    static __device__ __forceinline__ int k_at(int row, int ch) {
-        return row * D + 16 * (D % 128 == 0 ? ch ^ ((row & 1) << 2) : ch);
+    static constexpr int MERGE_BYTES = PW * ROWS * (OPITCH + 2) * 4;
+    static constexpr int OFF_Q = PW * STAGE, OFF_ENT = OFF_Q + Q_BYTES;
+    static int smem(int K) { return 1024 + std::max(OFF_ENT + ((K * 8 + 15) & ~15), MERGE_BYTES); }
+    // first of the VK channels that lane column c takes with fragment load v (rows of 128 bytes: the
+    // pieces 2c and 2c + 1 of a block, so that two rows' lanes meet different banks)
+    static __device__ __forceinline__ int k_dim(int v, int c) {
+        return CW == 128 ? (v >> 1) * 128 + 16 * (2 * c + (v & 1)) : 4 * VK * v + VK * c;
     }
-    // and of V row `row`: a lane reads piece r of rows 2c and 2c + 1, so pairs of rows are spread by c
-    static __device__ __forceinline__ int v_at(int row, int ch) {
-        const int g = (row >> 1) & 3;
-        if (DV == 96) return row * DV + 16 * ch;
-        return row * DV + 16 * (ch < DV / 128 * 8 ? ch ^ (g << 1) : ch ^ g);
+    // byte offset in a stage of byte x of a row of width-W blocks (TMA swizzle of W bytes)
+    template <int W>
+    static __device__ __forceinline__ int at(int row, int x) {
+        const int piece = (x % W) >> 4, sw = W == 128 ? row & 7 : (W == 64 ? (row >> 1) & 3 : (row >> 2) & 1);
+        return (x / W) * KC * W + row * W + 16 * (piece ^ sw) + (x & 15);
     }
+    // dv index of slot s (0 .. DV / 8 - 1) of the lane with row r
+    static __device__ __forceinline__ int slot_dv(int s, int r) { return (s / VB) * CWV + VB * r + s % VB; }
 };
 
-// dv index of slot s (0 .. DV / 8 - 1) of the lane with row r
-template <int DV>
-__device__ __forceinline__ int slot_dv(int s, int r) {
-    constexpr int n16 = DV / 128 * 16, n8 = (DV % 128) / 64 * 8;
-    if (s < n16) return (s >> 4) * 128 + 16 * r + (s & 15);
-    if (s < n16 + n8) return DV / 128 * 128 + 8 * r + (s - n16);
-    return DV / 128 * 128 + (DV % 128) / 64 * 64 + 4 * r + (s - n16 - n8);
-}
-
-template <int D, int DV, int NT>
-__global__ void __launch_bounds__(kPgThreads, D + DV <= 256 && NT == 1 ? MB : 1) fwd_pages_kernel(const __grid_constant__ PagesParams p) {
-    using C = PgCfg<D, DV, NT>;
-    extern __shared__ __align__(16) uint8_t smem[];
+template <int D, int DV, int NT, int PW>
+__global__ void __launch_bounds__(32 * PW, D + DV <= 256 && NT == 1 ? 16 / PW : 1) fwd_pages_kernel(
+    const __grid_constant__ PagesParams p, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
+    using C = PgCfg<D, DV, NT, PW>;
+    constexpr int kThreads = 32 * PW;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    __shared__ __align__(8) uint64_t s_bar[PW][2];
+    __shared__ int s_abort;
     __shared__ int s_used;
     __shared__ float s_m[C::ROWS], s_l[C::ROWS];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -120,27 +120,45 @@ __global__ void __launch_bounds__(kPgThreads, D + DV <= 256 && NT == 1 ? MB : 1)
     const int ps = p.tab.page_size;
     int b, ti, Lq;
     if (!locate_token(p.cu_q, p.B, p.Sq, tok, &b, &ti, &Lq)) return;
+    const long long bb = p.cu_q ? 0 : b, tt = p.cu_q ? tok : ti;
+    // the chain to the first copy is list -> block table -> page: its first link goes out at once
+    const int *list = p.list + bb * p.l_s[0] + tt * p.l_s[1] + kvh * p.l_s[2];
+    const int lp0 = tid < p.K ? __ldg(list + tid) : -1;
+    const float dqv = p.dq ? __ldg(p.dq + b * p.dq_s[0] + kvh * p.dq_s[1]) : 1.f;
+    const float dkv = p.dk ? __ldg(p.dk + b * p.dk_s[0] + kvh * p.dk_s[1]) : 1.f;
     const int Lk = p.tab.cu_k[b + 1] - p.tab.cu_k[b];
     int vis = p.causal ? min(Lk, Lk - Lq + ti + 1) : Lk;
     if (Lk < 0 || (long long)Lk > (long long)p.tab.max_pages * ps) {
         if (tid == 0) atomicOr(p.status, kStatusBounds);
         vis = 0;
     }
-    const long long bb = p.cu_q ? 0 : b, tt = p.cu_q ? tok : ti;
     const int h0 = kvh * p.G + rb * C::ROWS;            // first q-head of the tile
     const int rows = min(C::ROWS, p.G - rb * C::ROWS);  // real rows
 
     // ---- the list: page and first key of every entry (page -1: nothing visible in it)
     uint2 *qf = reinterpret_cast<uint2 *>(smem + C::OFF_Q);
     int2 *ent = reinterpret_cast<int2 *>(smem + C::OFF_ENT);
-    if (tid == 0) s_used = 0;
+    if (tid == 0) {
+        s_used = 0;
+        s_abort = 0;
+        if (p.num_pages > 0) {
+            ptx::prefetch_tmap(&tm_k);
+            ptx::prefetch_tmap(&tm_v);
+        }
+    }
+    const uint32_t bar_k = ptx::smem_u32(s_bar[warp]), bar_v = bar_k + 8;
+    if (lane == 0) {
+        ptx::mbar_init(bar_k, 1);
+        ptx::mbar_init(bar_v, 1);
+        ptx::fence_mbar_init();
+        ptx::fence_proxy_async_smem();
+    }
     __syncthreads();
     {
-        const int *list = p.list + bb * p.l_s[0] + tt * p.l_s[1] + kvh * p.l_s[2];
         const int *bt = p.tab.bt + (long long)b * p.tab.bt_stride;
         int used = 0;
-        for (int e = tid; e < p.K; e += kPgThreads) {
-            const int lp = list[e];
+        for (int e = tid; e < p.K; e += kThreads) {
+            const int lp = e == tid ? lp0 : list[e];
             int page = -1, key0 = 0;
             if (lp >= p.tab.max_pages) {
                 atomicOr(p.status, kStatusBounds);
@@ -160,100 +178,70 @@ __global__ void __launch_bounds__(kPgThreads, D + DV <= 256 && NT == 1 ? MB : 1)
         for (int o = 16; o > 0; o >>= 1) used = max(used, __shfl_xor_sync(0xffffffffu, used, o));
         if (lane == 0 && used) atomicMax(&s_used, used);
         const uint8_t *q = p.q + bb * p.q_s[0] + tt * p.q_s[1] + (long long)h0 * p.q_s[2];
-        for (int x = tid; x < NT * C::STEPS * 32; x += kPgThreads) {
+        for (int x = tid; x < NT * C::STEPS * 32; x += kThreads) {
             const int ln = x & 31, st = (x >> 5) % C::STEPS, nt = x / (32 * C::STEPS);
             const int qr = nt * 8 + (ln >> 2);
-            constexpr int SPV = C::VK / 4;  // k-steps fed by one vector load
-            const int pos = (st / SPV) * 4 * C::VK + (ln & 3) * C::VK + 4 * (st % SPV);
+            constexpr int SPV = C::VK / 4;  // k-steps fed by one fragment load
+            const int pos = C::k_dim(st / SPV, ln & 3) + 4 * (st % SPV);
             uint32_t lo = 0, hi = 0;
             if (qr < rows) e4m3x4_to_h2(*reinterpret_cast<const uint32_t *>(q + qr * p.q_s[2] + pos), lo, hi);
             qf[x] = make_uint2(lo, hi);
         }
     }
     __syncthreads();
-    const int gpp = ps >> 3;                   // 8-key groups per page
-    const int groups = s_used * gpp;           // groups of the list
-    const float dqv = p.dq ? p.dq[b * p.dq_s[0] + kvh * p.dq_s[1]] : 1.f;
-    const float dkv = p.dk ? p.dk[b * p.dk_s[0] + kvh * p.dk_s[1]] : 1.f;
+    const int bpp = ps / p.box;            // boxes per page
+    const int boxes = s_used * bpp;        // boxes of the list
     const float cs = p.scale_log2 * dqv * dkv;
 
-    // ---- the warp's chunk buffer, one of K and one of V: chunk it is groups first + it * stride ..
-    // + NG - 1, K fetched while the chunk before goes through softmax and PV, V during PV and S^T
-    const int first = (warp * CS + rank) * C::NG, stride = C::NG * CS * kPgWarps;
+    // ---- the warp's chunk buffer, one of K and one of V: chunk it is boxes (first + it * stride) <<
+    // box_shift ..; K is fetched while the chunk before goes through softmax and PV, V during PV and S^T
+    const int first = warp * CS + rank, stride = CS * PW;
     const uint32_t ks = ptx::smem_u32(smem) + warp * C::STAGE, vs = ks + C::K_STAGE;
-    const uint8_t *kb = p.k + (long long)kvh * p.k_s[2], *vb = p.v + (long long)kvh * p.v_s[2];
-    long long koff[C::KI];  // this lane's pieces of an 8-row group of K, in the pool and in the buffer
-    int krow[C::KI], kdst[C::KI];
-#pragma unroll
-    for (int u = 0; u < C::KI; ++u) {
-        const int x = 32 * u + lane, ch = x % C::KP;
-        krow[u] = x / C::KP;  // 8 or more: no piece
-        koff[u] = krow[u] * p.k_s[1] + 16 * ch;
-        kdst[u] = C::k_at(krow[u], ch);
-    }
-    long long voff[C::VI];
-    int vrow[C::VI], vdst[C::VI];
-#pragma unroll
-    for (int u = 0; u < C::VI; ++u) {
-        const int x = 32 * u + lane, ch = x % C::VP;
-        vrow[u] = x / C::VP;
-        voff[u] = vrow[u] * p.v_s[1] + 16 * ch;
-        vdst[u] = C::v_at(vrow[u], ch);
-    }
-    // lane i (mod NG) holds of group i of a chunk: its rows in the pool, how many keys are visible
-    long long ko, vo;
-    int lim;
-    bool full;  // of every group: all eight
+    const int nb = 1 << p.box_shift, mine = lane & (nb - 1), part = lane >> p.box_shift;
+    // this lane's box of the chunk: page, first row, and how many of its keys are visible
+    int page, prow, lim;
+    bool full;  // every key of the chunk
     auto locate = [&](int it) {
-        const int g = first + it * stride + (lane & (C::NG - 1));
-        ko = vo = 0;
+        const int bx = ((first + it * stride) << p.box_shift) + mine;
+        page = p.num_pages;  // out of range: TMA fills zeros
+        prow = 0;
         lim = 0;
-        if (g < groups) {
-            const int e = gpp == 1 ? g : (int)__umulhi((unsigned)g, p.group_magic);
-            const int off = (g - e * gpp) * 8;
+        if (bx < boxes) {
+            const int e = bpp == 1 ? bx : (int)__umulhi((unsigned)bx, p.box_magic);
             const int2 en = ent[e];
             if (en.x >= 0) {
-                lim = vis - en.y - off;
-                ko = en.x * p.k_s[0] + off * p.k_s[1];
-                vo = en.x * p.v_s[0] + off * p.v_s[1];
+                prow = (bx - e * bpp) * p.box;
+                lim = vis - en.y - prow;
+                if (lim > 0) page = en.x;
             }
         }
-        full = __all_sync(0xffffffffu, lim >= 8);
+        full = __all_sync(0xffffffffu, lim >= p.box);
+    };
+    // visible keys of 8-key group i (of all lanes)
+    auto group_lim = [&](int i) {
+        const int b0 = i * 8 / p.box;
+        return __shfl_sync(0xffffffffu, lim, b0) - (i * 8 - b0 * p.box);
     };
     auto fetch_k = [&]() {
-#pragma unroll
-        for (int i = 0; i < C::NG; ++i) {
-            const uint8_t *src = kb + __shfl_sync(0xffffffffu, ko, i);
-            const int li = full ? 8 : __shfl_sync(0xffffffffu, lim, i);
-#pragma unroll
-            for (int u = 0; u < C::KI; ++u)
-                if (8 * C::KP % 32 == 0 || krow[u] < 8) {
-                    const bool on = full || krow[u] < li;
-                    cp_async16(ks + 8 * i * D + kdst[u], on ? src + koff[u] : p.k, on ? 16 : 0);
-                }
-        }
+        if (lane == 0) ptx::mbar_arrive_expect_tx(bar_k, (uint32_t)C::K_STAGE);
+        __syncwarp();
+        if (part < C::NCK)
+            ptx::tma_load_4d(ks + part * C::KC * C::CW + mine * p.box * C::CW, &tm_k, bar_k, part * C::CW, kvh, prow, page);
     };
     auto fetch_v = [&]() {
-#pragma unroll
-        for (int i = 0; i < C::NG; ++i) {
-            const uint8_t *src = vb + __shfl_sync(0xffffffffu, vo, i);
-            const int li = full ? 8 : __shfl_sync(0xffffffffu, lim, i);
-#pragma unroll
-            for (int u = 0; u < C::VI; ++u)
-                if (8 * C::VP % 32 == 0 || vrow[u] < 8) {
-                    const bool on = full || vrow[u] < li;
-                    cp_async16(vs + 8 * i * DV + vdst[u], on ? src + voff[u] : p.v, on ? 16 : 0);
-                }
-        }
+        if (lane == 0) ptx::mbar_arrive_expect_tx(bar_v, (uint32_t)C::V_STAGE);
+        __syncwarp();
+        if (part < C::NCV)
+            ptx::tma_load_4d(vs + part * C::KC * C::CWV + mine * p.box * C::CWV, &tm_v, bar_v, part * C::CWV, kvh, prow, page);
     };
-    const int chunks = groups > first ? (groups - first + stride - 1) / stride : 0;
+    const int all = (boxes + nb - 1) >> p.box_shift;
+    const int chunks = all > first ? (all - first + stride - 1) / stride : 0;
+    const Waiter W{&s_abort, p.timeout_ns, p.status};
     if (chunks > 0) {
         locate(0);
         fetch_k();
-        cp_async_commit();
         fetch_v();
     }
-    cp_async_commit();
 
     float m[NT][2], l[NT][2];  // running maximum (log2 units) and this lane's share of the sum, rows 2c, 2c + 1
     float o[C::DT][NT][4];
@@ -272,8 +260,10 @@ __global__ void __launch_bounds__(kPgThreads, D + DV <= 256 && NT == 1 ? MB : 1)
             for (int e = 0; e < 4; ++e) o[d][t][e] = 0.f;
 
     for (int it = 0; it < chunks; ++it) {
-        cp_async_wait<1>();
-        __syncwarp();
+        if (!W.wait_warp(bar_k, it & 1)) {
+            W.drain(bar_v, it & 1);
+            break;
+        }
         // ---- S^T
         float s[C::MT][NT][4], s2[C::MT][NT][4];  // two sums each: shorter chains of dependent MMAs
 #pragma unroll
@@ -287,8 +277,7 @@ __global__ void __launch_bounds__(kPgThreads, D + DV <= 256 && NT == 1 ? MB : 1)
             Bytes<C::VK> kr[C::NG];
 #pragma unroll
             for (int i = 0; i < C::NG; ++i) {
-                const int at = C::VK == 16 ? C::k_at(8 * i + r, 4 * j + c) : (8 * i + r) * D + 32 * j + 8 * c;
-                kr[i] = ld_shared<C::VK>(ks + at);
+                kr[i] = ld_shared<C::VK>(ks + C::template at<C::CW>(8 * i + r, C::k_dim(j, c)));
             }
 #pragma unroll
             for (int w = 0; w < C::VK / 4; ++w) {
@@ -318,7 +307,7 @@ __global__ void __launch_bounds__(kPgThreads, D + DV <= 256 && NT == 1 ? MB : 1)
             for (int x = 0; x < C::MT; ++x)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const bool off = r >= __shfl_sync(0xffffffffu, lim, 2 * x + h);
+                    const bool off = r >= group_lim(2 * x + h);
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -326,13 +315,19 @@ __global__ void __launch_bounds__(kPgThreads, D + DV <= 256 && NT == 1 ? MB : 1)
                             if (off) s[x][t][2 * h + e] = -INFINITY;
                 }
         }
+        // V rows that are not visible may hold anything: their words become zeros below
+        const bool partial = !full;
+        int vlim[C::NG];
+        if (partial) {
+#pragma unroll
+            for (int i = 0; i < C::NG; ++i) vlim[i] = group_lim(i);
+        }
         const bool more = it + 1 < chunks;
         __syncwarp();  // every lane has read the K buffer
         if (more) {
             locate(it + 1);
             fetch_k();
         }
-        cp_async_commit();
         uint32_t pb[C::MT][NT][2];
         float mx[NT][2];
         bool moved = false;
@@ -378,8 +373,10 @@ __global__ void __launch_bounds__(kPgThreads, D + DV <= 256 && NT == 1 ? MB : 1)
                 }
         }
         // ---- O^T
-        cp_async_wait<1>();
-        __syncwarp();
+        if (!W.wait_warp(bar_v, it & 1)) {
+            if (more) W.drain(bar_k, (it + 1) & 1);
+            break;
+        }
 #pragma unroll
         for (int x = 0; x < C::MT; ++x) {
             uint32_t vr[4][DV / 32];  // keys 2c, 2c + 1 of the tile's two groups
@@ -387,18 +384,15 @@ __global__ void __launch_bounds__(kPgThreads, D + DV <= 256 && NT == 1 ? MB : 1)
             for (int y = 0; y < 4; ++y) {
                 const int row = 16 * x + 8 * (y >> 1) + 2 * c + (y & 1);
 #pragma unroll
-                for (int j = 0; j < C::NV16; ++j) {
-                    const Bytes<16> z = ld_shared<16>(vs + C::v_at(row, 8 * j + r));
+                for (int j = 0; j < C::NCV; ++j) {
+                    const Bytes<C::VB> z = ld_shared<C::VB>(vs + C::template at<C::CWV>(row, C::CWV * j + C::VB * r));
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) vr[y][4 * j + w] = z.w[w];
+                    for (int w = 0; w < C::VB / 4; ++w) vr[y][C::VB / 4 * j + w] = z.w[w];
                 }
-                if constexpr (C::NV8 > 0) {
-                    const Bytes<8> z = ld_shared<8>(vs + C::v_at(row, 8 * C::NV16 + (r >> 1)) + 8 * (r & 1));
-                    vr[y][4 * C::NV16] = z.w[0];
-                    vr[y][4 * C::NV16 + 1] = z.w[1];
+                if (partial && 2 * c + (y & 1) >= vlim[2 * x + (y >> 1)]) {
+#pragma unroll
+                    for (int w = 0; w < DV / 32; ++w) vr[y][w] = 0u;
                 }
-                if constexpr (C::NV4 > 0)
-                    vr[y][4 * C::NV16 + 2 * C::NV8] = ld_shared<4>(vs + C::v_at(row, 8 * C::NV16 + 4 * C::NV8 + (r >> 2)) + 4 * (r & 3)).w[0];
             }
 #pragma unroll
             for (int w = 0; w < DV / 32; ++w) {
@@ -416,14 +410,12 @@ __global__ void __launch_bounds__(kPgThreads, D + DV <= 256 && NT == 1 ? MB : 1)
         }
         __syncwarp();  // and the V buffer
         if (more) fetch_v();
-        cp_async_commit();
     }
 
     // ---- merge: warps through shared memory, CTAs through distributed shared memory
-    cp_async_wait<0>();
     __syncthreads();  // the buffers, the list and Q are done with
     float *wo = reinterpret_cast<float *>(smem);                       // [warp][row][OPITCH]
-    float *wm = wo + kPgWarps * C::ROWS * C::OPITCH, *wl = wm + kPgWarps * C::ROWS;  // [warp][row]
+    float *wm = wo + PW * C::ROWS * C::OPITCH, *wl = wm + PW * C::ROWS;  // [warp][row]
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -440,19 +432,19 @@ __global__ void __launch_bounds__(kPgThreads, D + DV <= 256 && NT == 1 ? MB : 1)
             for (int d = 0; d < C::DT; ++d)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    wo[(warp * C::ROWS + rw) * C::OPITCH + slot_dv<DV>(2 * d + h, r)] = o[d][t][2 * h + e];
+                    wo[(warp * C::ROWS + rw) * C::OPITCH + C::slot_dv(2 * d + h, r)] = o[d][t][2 * h + e];
         }
     __syncthreads();
     // warp buffers -> buffer of warp 0 (relative to the CTA's maximum), and the CTA's m and l
-    for (int x = tid; x < rows * (DV / 2); x += kPgThreads) {
+    for (int x = tid; x < rows * (DV / 2); x += kThreads) {
         const int rw = x / (DV / 2), d = 2 * (x - rw * (DV / 2));
         float M = wm[rw];
 #pragma unroll
-        for (int w = 1; w < kPgWarps; ++w) M = fmaxf(M, wm[w * C::ROWS + rw]);
+        for (int w = 1; w < PW; ++w) M = fmaxf(M, wm[w * C::ROWS + rw]);
         const float ref = M == -INFINITY ? 0.f : M;
         float a0 = 0.f, a1 = 0.f, L = 0.f;
 #pragma unroll
-        for (int w = 0; w < kPgWarps; ++w) {
+        for (int w = 0; w < PW; ++w) {
             const float f = ptx::ex2(wm[w * C::ROWS + rw] - ref);
             const float2 y = *reinterpret_cast<const float2 *>(wo + (w * C::ROWS + rw) * C::OPITCH + d);
             a0 = fmaf(f, y.x, a0);
@@ -471,7 +463,7 @@ __global__ void __launch_bounds__(kPgThreads, D + DV <= 256 && NT == 1 ? MB : 1)
     const uint32_t a_m = ptx::smem_u32(s_m), a_l = ptx::smem_u32(s_l), a_o = ptx::smem_u32(wo);
     // the cluster's CTAs share the tile's output: pair x of columns belongs to rank x mod CS's stretch
     const int total = rows * (DV / 2), share = (total + CS - 1) / CS;
-    for (int x = rank * share + tid; x < min(total, (rank + 1) * share); x += kPgThreads) {
+    for (int x = rank * share + tid; x < min(total, (rank + 1) * share); x += kThreads) {
         const int rw = x / (DV / 2), d = 2 * (x - rw * (DV / 2));
         float M, L, a0, a1;
         if (CS > 1) {
@@ -518,14 +510,26 @@ __global__ void __launch_bounds__(kPgThreads, D + DV <= 256 && NT == 1 ? MB : 1)
     if (CS > 1) cluster_sync();  // no CTA leaves while its shared memory is still read
 }
 
-template <int D, int DV, int NT>
-cudaError_t launch_pages(const PagesParams &p, unsigned int tiles, cudaStream_t s) {
-    const int smem = PgCfg<D, DV, NT>::smem(p.K);
-    cudaError_t e = cudaFuncSetAttribute(fwd_pages_kernel<D, DV, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
+template <int D, int DV, int NT, int PW>
+fa8_status launch_pages(PagesParams &p, const fa8_tensor *k, const fa8_tensor *v, unsigned int tiles, cudaStream_t s) {
+    using C = PgCfg<D, DV, NT, PW>;
+    const int ps = p.tab.page_size;
+    p.box = std::gcd(ps, C::KC);
+    p.box_shift = C::KC / p.box == 1 ? 0 : (C::KC / p.box == 2 ? 1 : 2);
+    p.box_magic = ps > p.box ? (unsigned)((0x100000000ull + ps / p.box - 1) / (ps / p.box)) : 0u;
+    CUtensorMap tk, tv;
+    memset(&tk, 0, sizeof(tk));
+    memset(&tv, 0, sizeof(tv));
+    if (p.num_pages > 0) {
+        fa8_status st;
+        if ((st = host::encode_kv(&tk, k, C::CW, p.box)) || (st = host::encode_kv(&tv, v, C::CWV, p.box))) return st;
+    }
+    const int smem = C::smem(p.K);
+    cudaError_t e = cudaFuncSetAttribute(fwd_pages_kernel<D, DV, NT, PW>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return host::cuda_fail(e, "page attention shared memory");
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(tiles * p.cluster);
-    cfg.blockDim = dim3(kPgThreads);
+    cfg.blockDim = dim3(32 * PW);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -534,7 +538,8 @@ cudaError_t launch_pages(const PagesParams &p, unsigned int tiles, cudaStream_t 
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fwd_pages_kernel<D, DV, NT>, p);
+    e = cudaLaunchKernelEx(&cfg, fwd_pages_kernel<D, DV, NT, PW>, p, tk, tv);
+    return e == cudaSuccess ? FA8_SUCCESS : host::cuda_fail(e, "page attention kernel launch");
 }
 
 }  // namespace fa8
@@ -640,21 +645,24 @@ extern "C" fa8_status fa8_fwd_pages(const fa8_tensor *q, const fa8_tensor *k, co
     p.causal = causal;
     p.num_pages = (int)k->shape[0];
     p.status = ds->status;
-    const unsigned gpp = (unsigned)page_size / 8;
-    p.group_magic = gpp > 1 ? (unsigned)((0x100000000ull + gpp - 1) / gpp) : 0u;
-    // Clusters split a list over CTAs while the grid is below four CTAs per SM and every warp keeps
-    // at least two chunks.
+    p.timeout_ns = wait_timeout_ns();
+    // Clusters split a list over CTAs while the grid is below 16 warps per SM and every warp keeps at
+    // least two chunks; where clusters of eight still leave SMs empty, CTAs of eight warps split it once
+    // more (8 lists of 4096 keys, d = dv = 256: 12.4 us against 15.2 with four warps; 512 lists of 2048
+    // keys, d = dv = 128: 53 against 48.5).
     const long long keys = (long long)p.K * page_size;
+    const int kc = qs.D + DV <= 256 ? 32 : 16;
     p.cluster = 1;
-    while (p.cluster < fa8::kPgMaxCluster && tiles * p.cluster * 2 <= (long long)CSF * ds->sm_count &&
-           keys >= 2LL * 32 * fa8::kPgWarps * p.cluster * 2)
+    while (p.cluster < fa8::kPgMaxCluster && tiles * p.cluster * 2 <= 4LL * ds->sm_count && keys >= 2LL * kc * 4 * p.cluster * 2)
         p.cluster *= 2;
+    const bool wide = p.cluster == fa8::kPgMaxCluster && tiles * p.cluster <= ds->sm_count && keys >= 2LL * kc * 8 * p.cluster;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = cudaErrorInvalidValue;
-#define FA8_PAGES(D_, DV_)                                                                             \
-    case D_ * 1000 + DV_:                                                                              \
-        e = nt == 1 ? fa8::launch_pages<D_, DV_, 1>(p, (unsigned)tiles, s) : fa8::launch_pages<D_, DV_, 2>(p, (unsigned)tiles, s); \
-        break;
+#define FA8_PAGES(D_, DV_)                                                                               \
+    case D_ * 1000 + DV_:                                                                                \
+        return nt == 1 ? (wide ? fa8::launch_pages<D_, DV_, 1, 8>(p, k, v, (unsigned)tiles, s)           \
+                               : fa8::launch_pages<D_, DV_, 1, 4>(p, k, v, (unsigned)tiles, s))          \
+                       : (wide ? fa8::launch_pages<D_, DV_, 2, 8>(p, k, v, (unsigned)tiles, s)           \
+                               : fa8::launch_pages<D_, DV_, 2, 4>(p, k, v, (unsigned)tiles, s));
     switch (qs.D * 1000 + DV) {
         FA8_PAGES(64, 64)
         FA8_PAGES(96, 96)
@@ -664,6 +672,5 @@ extern "C" fa8_status fa8_fwd_pages(const fa8_tensor *q, const fa8_tensor *k, co
         FA8_PAGES(256, 256)
     }
 #undef FA8_PAGES
-    if (e != cudaSuccess) return cuda_fail(e, "page attention kernel launch");
-    return FA8_SUCCESS;
+    return fail(FA8_ERR_UNSUPPORTED, "no page attention kernel for (%d, %d)", qs.D, DV);
 }

@@ -301,7 +301,7 @@ FA8_API fa8_status fa8_select_pages(const fa8_tensor *q, const fa8_tensor *bound
  *     nothing.  At most 4096 per token and kv-head.
  *   page_size: a multiple of 8 up to 4096.
  * Tokens with no visible listed key get O = 0 and LSE = -inf (the sink's logit with a
- * sink).  Keys that are not visible are not read.
+ * sink).  What the pool holds in rows that are not visible does not matter.
  */
 FA8_API fa8_status fa8_fwd_pages(const fa8_tensor *q, const fa8_tensor *k, const fa8_tensor *v,
                                  const fa8_tensor *pages, const fa8_tensor *descale_q,
