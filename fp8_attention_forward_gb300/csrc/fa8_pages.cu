@@ -121,28 +121,45 @@ struct SelectParams {
     long long o_s[3];  // request, token, head
     const int *cu_q;
     int T, B, Sq, Hkv, G, K, causal, keep_first, keep_last, num_pages, cluster;
+    unsigned long long timeout_ns;
     host::Table tab;
     unsigned int *status;
 };
 
-constexpr int kSelThreads = 256, kSelWarps = kSelThreads / 32;
-constexpr int kSelMaxTable = 16384;
+constexpr int kSelWarps = 4, kSelThreads = kSelWarps * 32;
+constexpr int kSelMaxTable = 16384;  // block_table columns
+constexpr int kSelMaxTable4 = 2048;  // of the kernel that takes four tokens at once
 constexpr int kSelMaxCluster = 8;
+constexpr int kSelBins = 256, kSelList = 256;
 
-// Shared memory, by table width: the q operand of one group of rows; 8 bytes a page (fp32 scores,
-// later the 64-bit keys of the undecided pages); two bit masks over the pages.
-template <int D, int NT>
+// TB tokens of one request per CTA.  TB = 1: the q-heads in groups of 8 NT rows, all four warps choose.
+// TB = 4: each token's q-heads padded to GP = 2, 4 or 8 rows, so that the four tokens are the 4 GP
+// columns of one pass over the bounds; then a warp chooses for each token.
+template <int D, int NT, int TB>
 struct SelCfg {
-    static constexpr int NV = 2 * D / 64;      // 16-byte vectors of a bounds row per lane
-    static constexpr int STEPS = 2 * D / 16;   // MMA k-steps
-    static constexpr int MT = D <= 128 ? 2 : 1;  // 16-page tiles in flight per warp (registers)
-    static constexpr int Q_BYTES = NT * STEPS * 32 * 8;
-    static int words(int table) { return (table + 31) / 32; }
-    static int smem(int table) { return Q_BYTES + words(table) * 32 * 8 + 2 * words(table) * 4; }
+    static constexpr int GP = 2 * NT;        // TB = 4: rows per token
+    static constexpr int ROW = 2 * D;        // bytes of a page's bounds
+    static constexpr int PITCH = ROW + (ROW % 128 == 0 ? 64 : 0);  // two rows' lanes meet different banks
+    static constexpr int NV = ROW / 64;      // 16-byte vectors of a row per lane
+    static constexpr int STEPS = ROW / 16;   // MMA k-steps
+    static constexpr int BUF = 16 * PITCH;   // 16 pages
+    static constexpr int RING = kSelWarps * 2 * BUF;
+    static constexpr int QR = TB == 1 ? 8 * NT : TB * GP;  // query rows of one pass
+    static constexpr int Q_BYTES = NT * STEPS * 32 * 8 + QR * D;  // as MMA fragments, and as they are
+    static constexpr int W = kSelWarps / TB;  // warps that choose for a token
+    // per token after the ring: fp32 scores, bins, list, scratch, two bit masks; the 64-bit keys of
+    // undecided pages take the ring's place
+    static __host__ __device__ int words(int table) { return (table + 31) / 32; }
+    static __host__ __device__ int token_bytes(int table) { return words(table) * (32 * 4 + 8) + kSelBins * 4 + kSelList * 4 + 64; }
+    static __host__ __device__ int front(int table) {
+        const int keys = TB * words(table) * 32 * 8;
+        return Q_BYTES + (keys > RING ? keys : RING);
+    }
+    static int smem(int table) { return 128 + front(table) + TB * ((token_bytes(table) + 15) & ~15); }
 };
 
 __device__ __forceinline__ unsigned int order_f32(float v) {
-    const unsigned int u = __float_as_uint(v);
+    const unsigned int u = __float_as_uint(v + 0.f);  // -0 counts as 0
     return u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
 }
 __device__ __forceinline__ float unorder_f32(unsigned int u) {
@@ -155,238 +172,504 @@ __device__ __forceinline__ int fixed_e4m3(unsigned int code) {
     return (code & 0x80u) ? -v : v;
 }
 
-// The rank-th largest (rank >= 1) of `count` ordered integers of BITS bits, key(i) for i in
-// [0, count) where on(i): 8 bits a pass, by histogram.  `left` returns how many equal to the
-// result are among the rank largest.  Called by all threads.
-template <int BITS, typename U, typename F>
-__device__ __forceinline__ U kth_largest(int count, int rank, unsigned int *hist, unsigned int *res, int *left, F key) {
-    U prefix = 0;
-    for (int shift = BITS - 8; shift >= 0; shift -= 8) {
-        for (int i = threadIdx.x; i < 256; i += kSelThreads) hist[i] = 0;
-        __syncthreads();
-        const U mask = shift + 8 >= BITS ? 0 : ~(U)0 << (shift + 8);
-        for (int i = threadIdx.x; i < count; i += kSelThreads) {
-            U u;
-            if (key(i, &u) && (u & mask) == prefix) atomicAdd(&hist[(unsigned int)(u >> shift) & 255u], 1u);
+// The threads that choose for one token: W warps with their own barrier.
+template <int W>
+struct Team {
+    int t, id;               // thread of the team, team of the CTA
+    unsigned int *bins, *words;  // kSelBins; 16 words of scratch
+    __device__ __forceinline__ void sync() const {
+        if constexpr (W == 1) __syncwarp();
+        else ptx::named_bar_sync(1 + id, 32 * W);
+    }
+    // f over [0, n), each index by one thread
+    template <typename F>
+    __device__ __forceinline__ void each(int n, F f) const {
+        for (int i = t; i < n; i += 32 * W) f(i);
+    }
+    // f(index, value) over scores [from, to), eight loads at a time
+    template <typename F>
+    __device__ __forceinline__ void scan(const float *scores, int from, int to, F f) const {
+        for (int i0 = from + t; i0 < to; i0 += 8 * 32 * W) {
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = scores[min(i0 + j * 32 * W, to - 1)];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (i0 + j * 32 * W < to) f(i0 + j * 32 * W, v[j]);
         }
-        __syncthreads();
-        if (threadIdx.x < 32) {  // lane l: bins 255 - 8 l downwards
-            const int lane = threadIdx.x;
-            int own = 0;
+    }
+    // lane l of the team's first warp: bins 8 l .. 8 l + 7; finds the bin that holds the rank-th entry from
+    // above and leaves it, the rank within it and its count in words[0 .. 2]
+    __device__ __forceinline__ void find_bin(int rank) const {
+        if (t >= 32) return;
+        const uint4 x = *reinterpret_cast<const uint4 *>(bins + 8 * t), y = *reinterpret_cast<const uint4 *>(bins + 8 * t + 4);
+        const int c[8] = {(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w};
+        int own = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) own += (int)hist[255 - 8 * lane - j];
-            int incl = own;
+        for (int j = 0; j < 8; ++j) own += c[j];
+        int incl = own;  // entries in this lane's bins and above
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int x = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += x;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_down_sync(0xffffffffu, incl, o);
+            if (t + o < 32) incl += v;
+        }
+        int above = incl - own;
+#pragma unroll
+        for (int j = 7; j >= 0; --j) {
+            if (above < rank && rank <= above + c[j]) {
+                words[0] = 8 * t + j;
+                words[1] = (unsigned int)(rank - above);
+                words[2] = (unsigned int)c[j];
             }
-            int above = incl - own;
-            if (above < rank && rank <= incl) {
-#pragma unroll 1
-                for (int j = 0; j < 8; ++j) {
-                    const int c = (int)hist[255 - 8 * lane - j];
-                    if (above + c >= rank) {
-                        res[0] = 255 - 8 * lane - j;
-                        res[1] = (unsigned int)(rank - above);
-                        break;
+            above += c[j];
+        }
+    }
+    __device__ __forceinline__ unsigned int max32(unsigned int v) const {
+        v = __reduce_max_sync(0xffffffffu, v);
+        if constexpr (W > 1) {
+            if ((t & 31) == 0) words[t >> 5] = v;
+            sync();
+            v = words[0];
+#pragma unroll
+            for (int i = 1; i < W; ++i) v = max(v, words[i]);
+            sync();
+        }
+        return v;
+    }
+    // The rank-th largest (rank >= 1) of scores [from, to): bins over the span that is left, which spreads
+    // real scores evenly whatever their exponents, until few enough share a bin to be ranked directly.
+    __device__ __forceinline__ float kth_score(const float *scores, int from, int to, int rank, int *list) const {
+        unsigned int hi = 0, nlo = 0;
+        scan(scores, from, to, [&](int, float v) {
+            const unsigned int u = order_f32(v);
+            hi = max(hi, u);
+            nlo = max(nlo, ~u);
+        });
+        hi = max32(hi);
+        unsigned int lo = ~max32(nlo);
+        while (lo < hi) {
+            const int bits = 32 - __clz((int)(hi - lo)), shift = bits > 8 ? bits - 8 : 0;
+            each(kSelBins, [&](int i) { bins[i] = 0; });
+            if (t == 0) words[3] = 0;
+            sync();
+            scan(scores, from, to, [&](int, float v) {
+                const unsigned int u = order_f32(v);
+                if (u >= lo && u <= hi) atomicAdd(&bins[(u - lo) >> shift], 1u);
+            });
+            sync();
+            find_bin(rank);
+            sync();
+            lo += words[0] << shift;
+            rank = (int)words[1];
+            const int count = (int)words[2];
+            if (hi - lo > (1u << shift) - 1u) hi = lo + ((1u << shift) - 1u);
+            if (count <= 64 && lo < hi) {
+                scan(scores, from, to, [&](int, float v) {
+                    const unsigned int u = order_f32(v);
+                    if (u >= lo && u <= hi) list[atomicAdd(&words[3], 1u)] = (int)u;
+                });
+                sync();
+                each(count, [&](int i) {
+                    const unsigned int u = (unsigned int)list[i];
+                    int above = 0, same = 0;
+                    for (int j = 0; j < count; ++j) {
+                        const unsigned int o = (unsigned int)list[j];
+                        above += o > u;
+                        same += o == u;
                     }
-                    above += c;
+                    if (above < rank && rank <= above + same) words[4] = u;
+                });
+                sync();
+                lo = hi = words[4];
+            }
+            sync();
+        }
+        return unorder_f32(lo);
+    }
+    // maximum (unsigned) over the team of one value a thread
+    __device__ __forceinline__ unsigned long long max64(unsigned long long v) const {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+        if constexpr (W > 1) {
+            unsigned long long *w = reinterpret_cast<unsigned long long *>(words);
+            if ((t & 31) == 0) w[t >> 5] = v;
+            sync();
+            v = w[0];
+#pragma unroll
+            for (int i = 1; i < W; ++i) v = max(v, w[i]);
+            sync();
+        }
+        return v;
+    }
+    // The same over the 64-bit keys that key(i, &u) yields for i in [0, n); `left`: how many keys equal
+    // to the result are among the rank largest.
+    template <typename F>
+    __device__ __forceinline__ unsigned long long kth_key(int n, int rank, int *left, F key) const {
+        unsigned long long hi = 0, nlo = 0, u;
+        each(n, [&](int i) {
+            if (key(i, &u)) {
+                hi = max(hi, u);
+                nlo = max(nlo, ~u);
+            }
+        });
+        hi = max64(hi);
+        unsigned long long lo = ~max64(nlo);
+        while (lo < hi) {
+            const int bits = 64 - __clzll((long long)(hi - lo)), shift = bits > 8 ? bits - 8 : 0;
+            each(kSelBins, [&](int i) { bins[i] = 0; });
+            sync();
+            each(n, [&](int i) {
+                if (key(i, &u) && u >= lo && u <= hi) atomicAdd(&bins[(unsigned int)((u - lo) >> shift)], 1u);
+            });
+            sync();
+            find_bin(rank);
+            sync();
+            lo += (unsigned long long)words[0] << shift;
+            rank = (int)words[1];
+            if (hi - lo > (1ull << shift) - 1ull) hi = lo + ((1ull << shift) - 1ull);
+            sync();
+        }
+        *left = rank;
+        return lo;
+    }
+};
+
+// Exact score of one page for one token, by a warp: sum_c max(q_c lo_c, q_c hi_c) in units of 2^-18 for
+// each q-head, the largest; a NaN ranks above all.  Order-preserving unsigned key.
+template <int D>
+__device__ __forceinline__ unsigned long long exact_key(const uint8_t *src, const uint8_t *q, long long q_sh, int G, int lane) {
+    constexpr int NW = (D / 4 + 31) / 32;  // words of four channels per lane
+    auto has_nan = [](uint32_t w) { return (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0; };
+    int lo[NW][4], hi[NW][4];
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+        const int wd = lane + 32 * i;
+        const uint32_t l = wd < D / 4 ? *reinterpret_cast<const uint32_t *>(src + 4 * wd) : 0u;
+        const uint32_t h = wd < D / 4 ? *reinterpret_cast<const uint32_t *>(src + D + 4 * wd) : 0u;
+        nan |= has_nan(l) || has_nan(h);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            lo[i][e] = fixed_e4m3(l >> (8 * e) & 0xFFu);
+            hi[i][e] = fixed_e4m3(h >> (8 * e) & 0xFFu);
+        }
+    }
+    long long best = LLONG_MIN;
+    for (int h0 = 0; h0 < G; h0 += 4) {
+        uint32_t w[4][NW];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int i = 0; i < NW; ++i)
+                w[k][i] = lane + 32 * i < D / 4 ? *reinterpret_cast<const uint32_t *>(q + min(h0 + k, G - 1) * q_sh + 4 * (lane + 32 * i)) : 0u;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            long long s = 0;
+            bool bad = nan;
+#pragma unroll
+            for (int i = 0; i < NW; ++i) {
+                bad |= has_nan(w[k][i]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int x = fixed_e4m3(w[k][i] >> (8 * e) & 0xFFu);
+                    s += (long long)x * (x < 0 ? lo[i][e] : hi[i][e]);
                 }
             }
+            // |s| < 2^40: 20 low bits and the rest are summed apart
+            const unsigned int low = __reduce_add_sync(0xffffffffu, (unsigned int)s & 0xFFFFFu);
+            const int high = __reduce_add_sync(0xffffffffu, (int)(s >> 20));
+            const long long sum = ((long long)high << 20) + low;
+            best = max(best, __any_sync(0xffffffffu, bad) ? LLONG_MAX : sum);
         }
-        __syncthreads();
-        prefix |= (U)res[0] << shift;
-        rank = (int)res[1];
-        __syncthreads();
     }
-    *left = rank;
-    return prefix;
+    return (unsigned long long)best ^ 0x8000000000000000ull;
 }
 
-// A cluster of CTAs per (token, kv-head).  Every CTA scores a share of the pages with f16 MMAs
-// (pages on M, q-heads on N; the contraction runs over [lo | hi] against [min(q,0) | max(q,0)],
-// which is sum_c max(q_c lo_c, q_c hi_c)), and rank 0 chooses.
+// Every CTA scores its pages with f16 MMAs (pages on M, query rows on N; the contraction runs over
+// [lo | hi] against [min(q,0) | max(q,0)], which is sum_c max(q_c lo_c, q_c hi_c)); a page's 2 D bytes
+// arrive by one bulk copy, 16 pages a buffer, two buffers a warp.  With few rows a cluster of CTAs
+// shares a token's pages and rank 0 chooses.
 //
 // Exact choice from fp32 scores: E4M3 products are exact, an MMA adds 16 of them to the running
 // sum, and what it drops is below 2^-22 of the largest magnitude passing through, itself at most
-// A = max_h |q_h|_1 * max|bound|.  So a score is off by at most eps = 2^-16 A (2 D / 16 <= 32
-// steps, and a factor two to spare).  With t the k-th largest fp32 score, pages above t + 2 eps
+// A = max_h |q_h|_1 * max|bound|.  So a score is off by at most eps = (2 D / 16 + 1) 2^-21 A: the MMA
+// steps and the sum of their two chains, with a factor two to spare.  With t the k-th largest fp32 score, pages above t + 2 eps
 // are in and pages below t - 2 eps out whatever the true scores; the few between are scored again
 // in 64-bit integers (E4M3 is a whole number of 2^-9) and ranked by (score, lower index).
-// Bound: HBM/L2, 2 D bytes per page and kv-head, for long requests; launch and chain latency for
-// short ones.
-template <int D, int NT>
+template <int D, int NT, int TB>
 __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_constant__ SelectParams p) {
-    using C = SelCfg<D, NT>;
-    extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ unsigned int hist[256];
-    __shared__ unsigned int res[2];
-    __shared__ float s_l1[kSelWarps], s_kmax[kSelMaxCluster], s_kw[kSelWarps];
-    __shared__ int s_in, s_amb, s_list[256], s_cnt, s_scan[kSelWarps];
+    using C = SelCfg<D, NT, TB>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
+    __shared__ __align__(8) uint64_t s_bar[kSelWarps][2];
+    __shared__ int s_abort;
+    __shared__ float s_l1[kSelWarps][TB], s_kmax[kSelMaxCluster], s_kw[kSelWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int CS = p.cluster;
+    const int CS = TB == 1 ? p.cluster : 1;
     const int rank = CS > 1 ? (int)cluster_rank() : 0;
     const int row = blockIdx.x / CS;
-    const int kvh = row % p.Hkv, tok = row / p.Hkv;
+    const int kvh = row % p.Hkv, unit = row / p.Hkv;
     const int ps = p.tab.page_size;
-    int b, i, Lq;
-    if (!locate_token(p.cu_q, p.B, p.Sq, tok, &b, &i, &Lq)) return;
+    // ---- tokens tok0 .. tok0 + ntok - 1: the i0-th of request b's Lq new ones on
+    int b, i0, Lq, tok0, ntok = 1;
+    if constexpr (TB == 1) {
+        tok0 = unit;
+        if (!locate_token(p.cu_q, p.B, p.Sq, tok0, &b, &i0, &Lq)) return;
+    } else {
+        int blk;
+        if (!p.cu_q) {
+            const int per = (p.Sq + TB - 1) / TB;
+            b = unit / per;
+            blk = unit - b * per;
+            Lq = p.Sq;
+            tok0 = b * p.Sq;
+        } else {  // request b's blocks start at slot cu_q[b] / TB + b
+            int lo = 0, hi = p.B - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (p.cu_q[mid] / TB + mid <= unit) lo = mid;
+                else hi = mid - 1;
+            }
+            b = lo;
+            tok0 = p.cu_q[b];
+            Lq = p.cu_q[b + 1] - tok0;
+            blk = unit - (tok0 / TB + b);
+        }
+        i0 = blk * TB;
+        tok0 += i0;
+        ntok = min(TB, Lq - i0);
+        if (ntok <= 0 || tok0 < 0 || (long long)tok0 + ntok > p.T) return;
+    }
     const int Lk = p.tab.cu_k[b + 1] - p.tab.cu_k[b];
-    int vis = p.causal ? min(Lk, Lk - Lq + i + 1) : Lk;
-    if (Lk < 0 || (long long)Lk > (long long)p.tab.max_pages * ps) {
-        if (tid == 0) atomicOr(p.status, kStatusBounds);
-        vis = 0;
-    }
-    const int n = vis > 0 ? (vis - 1) / ps + 1 : 0;
-    const long long bb = p.cu_q ? 0 : b, tt = p.cu_q ? tok : i;
-    int *out = p.pages + bb * p.o_s[0] + tt * p.o_s[1] + kvh * p.o_s[2];
-    if (n <= p.K) {
-        if (rank == 0)
-            for (int j = tid; j < p.K; j += kSelThreads) out[j] = j < n ? j : -1;
-        return;
-    }
+    bool bad = Lk < 0 || (long long)Lk > (long long)p.tab.max_pages * ps;
+    if (bad && tid == 0) atomicOr(p.status, kStatusBounds);
+    // pages with a key that the i-th token sees
+    auto pages_of = [&](int i) {
+        const int vis = bad ? 0 : (p.causal ? min(Lk, Lk - Lq + i + 1) : Lk);
+        return vis > 0 ? (vis - 1) / ps + 1 : 0;
+    };
+    const long long bb = p.cu_q ? 0 : b;
+    const long long t0 = p.cu_q ? tok0 : i0;
+    const int n_last = pages_of(i0 + ntok - 1);  // the most of the CTA's tokens
+    // ---- this thread's team chooses for one token
+    Team<C::W> team;
+    team.id = TB == 1 ? 0 : warp;
+    team.t = TB == 1 ? tid : lane;
+    const int words = C::words(p.tab.max_pages);
+    uint8_t *mine = smem + C::front(p.tab.max_pages) + team.id * ((C::token_bytes(p.tab.max_pages) + 15) & ~15);
+    float *scores = reinterpret_cast<float *>(mine);
+    team.bins = reinterpret_cast<unsigned int *>(mine + words * 128);
+    int *list = reinterpret_cast<int *>(team.bins + kSelBins);
+    team.words = reinterpret_cast<unsigned int *>(list + kSelList);
+    unsigned int *sel = team.words + 16, *amb = sel + words;
+    unsigned long long *keys = reinterpret_cast<unsigned long long *>(smem + C::Q_BYTES) + (size_t)team.id * words * 32;
+    const int n = team.id < ntok ? pages_of(i0 + team.id) : 0;
+    int *out = p.pages + bb * p.o_s[0] + (t0 + team.id) * p.o_s[1] + kvh * p.o_s[2];
+    if (team.id < ntok && n <= p.K && rank == 0) team.each(p.K, [&](int j) { out[j] = j < n ? j : -1; });
+    if (n_last <= p.K) return;
     if (CS > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 
-    uint2 *qf = reinterpret_cast<uint2 *>(smem);
-    const int words = (p.tab.max_pages + 31) >> 5;
-    float *scores = reinterpret_cast<float *>(smem + C::Q_BYTES);
-    unsigned long long *keys = reinterpret_cast<unsigned long long *>(smem + C::Q_BYTES);
-    unsigned int *sel = reinterpret_cast<unsigned int *>(smem + C::Q_BYTES + (size_t)words * 32 * 8);
-    unsigned int *amb = sel + words;
     const int *bt = p.tab.bt + (long long)b * p.tab.bt_stride;
-    const uint8_t *q = p.q + bb * p.q_s[0] + tt * p.q_s[1] + (long long)kvh * p.G * p.q_s[2];
+    const uint8_t *q = p.q + bb * p.q_s[0] + t0 * p.q_s[1] + (long long)kvh * p.G * p.q_s[2];
     const uint8_t *bounds = p.bounds + (long long)kvh * p.b_s[1];
-    const int from = p.keep_first, to = n - p.keep_last;  // pages that go by score
+    const int from = p.keep_first, to = n_last - p.keep_last;  // pages that go by score
 
-    // ---- scores of this CTA's pages
-    uint32_t kmax2 = 0;
-    float l1 = 0.f;
-    for (int g0 = 0; g0 < p.G; g0 += 8 * NT) {
-        if (g0) __syncthreads();
-        for (int x = tid; x < NT * C::STEPS * 32; x += kSelThreads) {
-            const int ln = x & 31, st = (x >> 5) % C::STEPS, nt = x / (32 * C::STEPS);
-            // padding rows repeat row g0: the maximum over rows does not see them
-            const int hr = g0 + nt * 8 + (ln >> 2) < p.G ? g0 + nt * 8 + (ln >> 2) : g0;
-            const int pos = 64 * (st >> 2) + 16 * (ln & 3) + 4 * (st & 3);
-            const bool low = pos < D;
-            const uint32_t w = *reinterpret_cast<const uint32_t *>(q + hr * p.q_s[2] + (low ? pos : pos - D));
-            const uint32_t neg = ((w >> 7) & 0x01010101u) * 0xFFu;  // bytes with the sign bit
-            const uint32_t part = low ? (w & neg) : (w & ~neg);
-            uint32_t lo, hi;
-            e4m3x4_to_h2(part, lo, hi);
-            qf[x] = make_uint2(lo, hi);
-        }
-        for (int r = warp; r < min(8 * NT, p.G - g0); r += kSelWarps) {
-            float s = 0.f;
-            for (int c = lane * 2; c < D; c += 64) {
-                float x0, x1;
-                ptx::e4m3x2_to_f32(*reinterpret_cast<const uint16_t *>(q + (g0 + r) * p.q_s[2] + c), x0, x1);
-                s += fabsf(x0) + fabsf(x1);
-            }
+    // ---- scores of this CTA's pages: chunk it is pages from + 16 ((warp + 4 it) CS + rank) ..
+    uint2 *qf = reinterpret_cast<uint2 *>(smem);
+    const uint32_t ring = ptx::smem_u32(smem + C::Q_BYTES) + warp * 2 * C::BUF, bar = ptx::smem_u32(s_bar[warp]);
+    if (lane == 0) {
+        ptx::mbar_init(bar, 1);
+        ptx::mbar_init(bar + 8, 1);
+        ptx::fence_mbar_init();
+        ptx::fence_proxy_async_smem();
+    }
+    if (tid == 0) s_abort = 0;
+    __syncthreads();
+    const Waiter W{&s_abort, p.timeout_ns, p.status};
+    const int p0 = from + 16 * (warp * CS + rank), stride = 16 * kSelWarps * CS;
+    const int chunks = to > p0 ? (to - p0 + stride - 1) / stride : 0;
+    uint32_t uses = 0;  // fills of each buffer so far: the parity of its barrier
+    uint32_t kmax2[4] = {0, 0, 0, 0};
+    float l1[TB];
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            l1 = fmaxf(l1, s);
+    for (int t = 0; t < TB; ++t) l1[t] = 0.f;
+    for (int g0 = 0; g0 < (TB == 1 ? p.G : 1); g0 += 8 * NT) {
+        unsigned int on[2] = {0, 0};  // valid pages of each buffer
+        auto id_of = [&](int it) { return lane < 16 && it < chunks && p0 + it * stride + lane < to ? bt[p0 + it * stride + lane] : -1; };
+        int id = id_of(0);
+        auto fetch = [&](int it) {
+            const bool ok = id >= 0 && id < p.num_pages;
+            if (!ok && lane < 16 && p0 + it * stride + lane < to) atomicOr(p.status, kStatusBounds);
+            const unsigned int m = __ballot_sync(0xffffffffu, ok);
+            const uint32_t bb = bar + 8 * (it & 1);
+            if (lane == 0) ptx::mbar_arrive_expect_tx(bb, (uint32_t)(__popc(m) * C::ROW));
+            __syncwarp();
+            if (ok) bulk_load(ring + (it & 1) * C::BUF + lane * C::PITCH, bounds + (long long)id * p.b_s[0], C::ROW, bb);
+            on[it & 1] = m;
+            id = id_of(it + 1);
+        };
+        if (chunks > 0) fetch(0);
+        if (chunks > 1) fetch(1);
+        // the query rows, while the first pages arrive; padding rows repeat a real one: the maximum
+        // does not see them
+        if (g0) __syncthreads();
+        uint8_t *qraw = smem + NT * C::STEPS * 32 * 8;
+        for (int x = tid; x < C::QR * (D / 16); x += kSelThreads) {
+            const int r = x / (D / 16), ch = x - r * (D / 16);
+            const int tk = TB == 1 ? 0 : min(r / C::GP, ntok - 1);
+            const int h = TB == 1 ? (g0 + r < p.G ? g0 + r : g0) : (r % C::GP < p.G ? r % C::GP : 0);
+            *reinterpret_cast<uint4 *>(qraw + 16 * x) = __ldg(reinterpret_cast<const uint4 *>(q + tk * p.q_s[1] + h * p.q_s[2] + 16 * ch));
         }
         __syncthreads();
-        constexpr int PP = 16 * C::MT;  // pages per warp step
-        for (int p0 = from + (warp * CS + rank) * PP; p0 < to; p0 += PP * CS * kSelWarps) {
-            int id = -1;
-            if (lane < PP && p0 + lane < to) {
-                id = bt[p0 + lane];
-                if (id < 0 || id >= p.num_pages) {
-                    id = -1;
-                    atomicOr(p.status, kStatusBounds);
+#pragma unroll 4
+        for (int x = tid; x < NT * C::STEPS * 32; x += kSelThreads) {
+            const int ln = x & 31, st = (x >> 5) % C::STEPS, col = 8 * (x / (32 * C::STEPS)) + (ln >> 2);
+            const int pos = 64 * (st >> 2) + 16 * (ln & 3) + 4 * (st & 3);
+            const bool low = pos < D;
+            const uint32_t w = *reinterpret_cast<const uint32_t *>(qraw + col * D + (low ? pos : pos - D));
+            const uint32_t neg = ((w >> 7) & 0x01010101u) * 0xFFu;  // bytes with the sign bit
+            uint32_t lo, hi;
+            e4m3x4_to_h2(low ? (w & neg) : (w & ~neg), lo, hi);
+            qf[x] = make_uint2(lo, hi);
+        }
+        // sums of |q|: eight lanes a row
+#pragma unroll
+        for (int r0 = 0; r0 < C::QR; r0 += 4 * kSelWarps) {
+            const int r = r0 + 4 * warp + (lane >> 3);
+            float s = 0.f;
+            if (r < C::QR) {
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t lo, hi;
+                    float x0, x1, x2, x3;
+                    e4m3x4_to_h2(*reinterpret_cast<const uint32_t *>(qraw + r * D + c + 4 * (lane & 7)), lo, hi);
+                    ptx::h2_to_f32(lo, x0, x1);
+                    ptx::h2_to_f32(hi, x2, x3);
+                    s += (fabsf(x0) + fabsf(x1)) + (fabsf(x2) + fabsf(x3));
                 }
             }
-            Bytes<16> raw[2 * C::MT][C::NV];
 #pragma unroll
-            for (int m = 0; m < 2 * C::MT; ++m) {
-                const int pg = __shfl_sync(0xffffffffu, id, 8 * m + (lane >> 2));
-                const uint8_t *src = bounds + (long long)max(pg, 0) * p.b_s[0] + 16 * (lane & 3);
+            for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
 #pragma unroll
-                for (int v = 0; v < C::NV; ++v) {
-                    if (pg >= 0) raw[m][v] = ld_stream<16>(src + 64 * v);
-                    else raw[m][v] = Bytes<16>{};
-                }
+            for (int t = 0; t < TB; ++t)
+                if (TB == 1 || r / C::GP == t) l1[t] = fmaxf(l1[t], s);
+        }
+        __syncthreads();
+        bool alive = true;
+        for (int it = 0; it < chunks; ++it) {
+            const int bi = it & 1;
+            if (!W.wait_warp(bar + 8 * bi, (uses >> bi) & 1)) {
+                if (it + 1 < chunks) W.drain(bar + 8 * (bi ^ 1), (uses >> (bi ^ 1)) & 1);
+                alive = false;
+                break;
             }
-            float acc[C::MT][NT][4];
+            uses ^= 1u << bi;
+            const uint32_t buf = ring + bi * C::BUF + (lane >> 2) * C::PITCH + 16 * (lane & 3);
+            float acc[NT][4], acc2[NT][4];  // two chains of dependent MMAs
 #pragma unroll
-            for (int m = 0; m < C::MT; ++m)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
+                for (int e = 0; e < 4; ++e) acc[t][e] = acc2[t][e] = 0.f;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[m][t][e] = 0.f;
-#pragma unroll
-            for (int v = 0; v < C::NV; ++v)
+            for (int v = 0; v < C::NV; ++v) {
+                const Bytes<16> x = ld_shared<16>(buf + 64 * v), y = ld_shared<16>(buf + 8 * C::PITCH + 64 * v);
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
-                    uint2 bf[NT];
+                    uint32_t a[4];
+                    e4m3x4_to_h2(x.w[s], a[0], a[2]);
+                    e4m3x4_to_h2(y.w[s], a[1], a[3]);
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) bf[t] = qf[(t * C::STEPS + 4 * v + s) * 32 + lane];
+                    for (int t = 0; t < NT; ++t) {
+                        const uint2 bf = qf[(t * C::STEPS + 4 * v + s) * 32 + lane];
+                        mma_f16(s & 1 ? acc2[t] : acc[t], a[0], a[1], a[2], a[3], bf.x, bf.y);
+                    }
 #pragma unroll
-                    for (int m = 0; m < C::MT; ++m) {
-                        uint32_t a0, a1, a2, a3;
-                        e4m3x4_to_h2(raw[2 * m][v].w[s], a0, a2);
-                        e4m3x4_to_h2(raw[2 * m + 1][v].w[s], a1, a3);
-#pragma unroll
-                        for (int t = 0; t < NT; ++t) mma_f16(acc[m][t], a0, a1, a2, a3, bf[t].x, bf[t].y);
-                        const __half2 x = __hmax2(__hmax2(__habs2(*reinterpret_cast<__half2 *>(&a0)), __habs2(*reinterpret_cast<__half2 *>(&a1))),
-                                                  __hmax2(__habs2(*reinterpret_cast<__half2 *>(&a2)), __habs2(*reinterpret_cast<__half2 *>(&a3))));
-                        const __half2 y = __hmax2(x, *reinterpret_cast<__half2 *>(&kmax2));
-                        kmax2 = *reinterpret_cast<const uint32_t *>(&y);
+                    for (int e = 0; e < 4; ++e) {
+                        const __half2 z = __hmax2(__habs2(*reinterpret_cast<__half2 *>(&a[e])), *reinterpret_cast<__half2 *>(&kmax2[e]));
+                        kmax2[e] = *reinterpret_cast<const uint32_t *>(&z);
                     }
                 }
+            }
 #pragma unroll
-            for (int m = 0; m < C::MT; ++m)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    float s = -INFINITY;
-                    bool nan = false;
+                for (int e = 0; e < 4; ++e) acc[t][e] += acc2[t][e];
+            const unsigned int ok = on[bi];
+            __syncwarp();  // the buffer has been read
+            if (it + 2 < chunks) fetch(it + 2);
 #pragma unroll
-                    for (int t = 0; t < NT; ++t)
+            for (int half = 0; half < 2; ++half) {
+                const int pl = 8 * half + (lane >> 2), pg = p0 + it * stride + pl, c = lane & 3;
+                auto put = [&](int token, float s) {
+                    float *dst = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(scores) +
+                                                           (TB == 1 ? 0 : (token - team.id) * ((C::token_bytes(p.tab.max_pages) + 15) & ~15)));
+                    if (pg >= to) return;
+                    if (!(ok >> pl & 1u)) s = -INFINITY;
+                    if (TB == 1 && g0) s = fmaxf(s, dst[pg]);
+                    dst[pg] = s;
+                };
+                // maximum over two columns; a NaN ranks above all
+                auto top = [&](int t) {
+                    const float x = acc[t][2 * half], y = acc[t][2 * half + 1];
+                    return x != x || y != y ? INFINITY : fmaxf(x, y);
+                };
+                if constexpr (TB == 1) {
+                    float s = top(0);
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float x = acc[m][t][2 * half + e];
-                            nan |= x != x;
-                            s = fmaxf(s, x);
-                        }
-                    if (nan) s = INFINITY;
+                    for (int t = 1; t < NT; ++t) s = fmaxf(s, top(t));
                     s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, 1));
                     s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, 2));
-                    const int pl = 16 * m + 8 * half + (lane >> 2);
-                    const int pg = __shfl_sync(0xffffffffu, id, pl);
-                    if ((lane & 3) == 0 && p0 + pl < to) {
-                        if (pg < 0) s = -INFINITY;
-                        if (g0) s = fmaxf(s, scores[p0 + pl]);
-                        scores[p0 + pl] = s;
+                    if (c == 0) put(0, s);
+                } else if constexpr (C::GP == 8) {
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        float s = top(t);
+                        s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, 1));
+                        s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, 2));
+                        if (c == t) put(t, s);
                     }
+                } else if constexpr (C::GP == 4) {
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        float s = top(t);
+                        s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, 1));
+                        if ((c & 1) == t) put(2 * t + (c >> 1), s);
+                    }
+                } else {
+                    put(c, top(0));
                 }
+            }
         }
+        if (!alive) break;
     }
     {
-        float k = fmaxf(__low2float(*reinterpret_cast<__half2 *>(&kmax2)), __high2float(*reinterpret_cast<__half2 *>(&kmax2)));
+        float k = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const __half2 x = *reinterpret_cast<__half2 *>(&kmax2[e]);
+            k = fmaxf(k, fmaxf(__low2float(x), __high2float(x)));
+        }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) k = fmaxf(k, __shfl_xor_sync(0xffffffffu, k, o));
+#pragma unroll
+        for (int t = 0; t < TB; ++t)
+#pragma unroll
+            for (int o = 16; o > 4; o >>= 1) l1[t] = fmaxf(l1[t], __shfl_xor_sync(0xffffffffu, l1[t], o));
         if (lane == 0) {
             s_kw[warp] = k;
-            s_l1[warp] = l1;
+#pragma unroll
+            for (int t = 0; t < TB; ++t) s_l1[warp][t] = l1[t];
         }
     }
-    if (tid == 0) s_in = s_amb = s_cnt = 0;
     __syncthreads();
     if (CS > 1) {
         asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
         if (rank > 0) {  // hand the scores over to rank 0
-            constexpr int PP = 16 * C::MT;
             const uint32_t dst = map_rank(ptx::smem_u32(scores), 0);
-            for (int t = tid; ; t += kSelThreads) {
-                const int pg = from + ((t / PP) * CS + rank) * PP + t % PP;
-                if (pg >= to) {
-                    if (from + ((t / PP) * CS + rank) * PP >= to) break;
-                    continue;
-                }
-                st_cluster_f32(dst + 4u * (uint32_t)pg, scores[pg]);
+            for (int t = tid;; t += kSelThreads) {
+                const int base = from + ((t >> 4) * CS + rank) * 16, pg = base + (t & 15);
+                if (base >= to) break;
+                if (pg < to) st_cluster_f32(dst + 4u * (uint32_t)pg, scores[pg]);
             }
         }
         if (tid == 0) {
@@ -397,104 +680,105 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
         cluster_sync();
         if (rank > 0) return;
     }
+    if (team.id >= ntok || n <= p.K) return;
 
     // ---- the choice
-    float a_l1 = s_l1[0], a_k = s_kw[0];
-    for (int w = 1; w < kSelWarps; ++w) {
-        a_l1 = fmaxf(a_l1, s_l1[w]);
+    const int last = n - p.keep_last, want = p.K - p.keep_first - p.keep_last;
+    float a_l1 = 0.f, a_k = 0.f;
+    for (int w = 0; w < kSelWarps; ++w) {
+        a_l1 = fmaxf(a_l1, s_l1[w][TB == 1 ? 0 : team.id]);
         a_k = fmaxf(a_k, s_kw[w]);
     }
     for (int r = 0; CS > 1 && r < CS; ++r) a_k = fmaxf(a_k, s_kmax[r]);
-    float eps2 = 2.f * 0x1p-16f * a_l1 * a_k;
-    if (!(eps2 < INFINITY)) eps2 = 0.f;  // a NaN query: every score is NaN, decided by index
-    const int m = to - from, want = p.K - p.keep_first - p.keep_last;
+    const float eps2 = 2.f * (C::STEPS + 1) * 0x1p-21f * a_l1 * a_k;
     float t_hi = INFINITY, t_lo = INFINITY;
     if (want > 0) {
-        int left;
-        const unsigned int u = kth_largest<32, unsigned int>(m, want, hist, res, &left, [&](int j, unsigned int *v) {
-            *v = order_f32(scores[from + j]);
-            return true;
-        });
-        const float t = unorder_f32(u);
+        const float t = team.kth_score(scores, from, last, want, list);
         t_hi = __fadd_ru(t, eps2);
         t_lo = __fsub_rd(t, eps2);
     }
-    const int nw = (n + 31) >> 5;
-    for (int w = warp; w < nw; w += kSelWarps) {
+    const int nw = (n + 31) >> 5, tw = team.t >> 5;
+    int n_in = 0, n_amb = 0;  // the same in every lane of a warp
+#pragma unroll 4
+    for (int w = tw; w < nw; w += C::W) {
         const int pg = 32 * w + lane;
-        bool in = pg < n && (pg < from || pg >= to), maybe = false;
-        if (pg >= from && pg < to && want > 0) {
+        const bool scored = pg >= from && pg < last;
+        bool in = false, maybe = false;
+        if (scored && want > 0) {
             const float s = scores[pg];
             in = s > t_hi;
             maybe = !in && s >= t_lo;
         }
-        const unsigned int bi = __ballot_sync(0xffffffffu, in), bm = __ballot_sync(0xffffffffu, maybe);
-        const unsigned int bs = __ballot_sync(0xffffffffu, in && pg >= from && pg < to);
+        const unsigned int bs = __ballot_sync(0xffffffffu, in), bm = __ballot_sync(0xffffffffu, maybe);
+        const unsigned int bf = __ballot_sync(0xffffffffu, pg < n && !scored);
+        n_in += __popc(bs);
+        n_amb += __popc(bm);
         if (lane == 0) {
-            sel[w] = bi;
+            sel[w] = bs | bf;
             amb[w] = bm;
-            atomicAdd(&s_in, __popc(bs));
-            atomicAdd(&s_amb, __popc(bm));
         }
     }
-    __syncthreads();
-    const int slots = want - s_in;  // places for the undecided pages
-    if (s_amb == slots) {
-        for (int w = tid; w < nw; w += kSelThreads) sel[w] |= amb[w];
-    } else if (slots > 0) {
-        // 64-bit scores of the undecided pages, a warp per page; keys overwrite the fp32 scores
-        for (int w = warp; w < nw; w += kSelWarps) {
+    if constexpr (C::W > 1) {
+        if (lane == 0) {
+            team.words[2 * tw] = (unsigned)n_in;
+            team.words[2 * tw + 1] = (unsigned)n_amb;
+        }
+        team.sync();
+        n_in = n_amb = 0;
+        for (int w = 0; w < C::W; ++w) {
+            n_in += (int)team.words[2 * w];
+            n_amb += (int)team.words[2 * w + 1];
+        }
+    }
+    team.sync();
+    const int places = want - n_in;  // for the undecided pages
+    if (n_amb == places) {
+        team.each(nw, [&](int w) { sel[w] |= amb[w]; });
+    } else if (places > 0 && n_amb > 0) {
+        // Keys that order the undecided pages exactly.  All-zero queries or bounds leave exact zeros.
+        const bool exact = !(eps2 > 0.f);
+        for (int w = tw; w < nw; w += C::W) {
             for (unsigned int bits = amb[w]; bits; bits &= bits - 1) {
                 const int pg = 32 * w + __ffs(bits) - 1;
-                const int id = bt[pg];
                 unsigned long long key = 0;
-                if (id >= 0 && id < p.num_pages) {
-                    const uint8_t *src = bounds + (long long)id * p.b_s[0];
-                    long long best = LLONG_MIN;
-                    for (int h = 0; h < p.G; ++h) {
-                        long long s = 0;
-                        bool nan = false;
-                        for (int c = lane; c < D; c += 32) {
-                            const unsigned int qc = q[h * p.q_s[2] + c];
-                            const unsigned int lc = src[c], hc = src[D + c];
-                            const unsigned int bc = (qc & 0x80u) ? lc : hc;
-                            nan |= (qc & 0x7Fu) == 0x7Fu || (lc & 0x7Fu) == 0x7Fu || (hc & 0x7Fu) == 0x7Fu;
-                            s += (long long)fixed_e4m3(qc) * fixed_e4m3(bc);
-                        }
-#pragma unroll
-                        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-                        if (__any_sync(0xffffffffu, nan)) s = LLONG_MAX;
-                        best = max(best, s);
-                    }
-                    key = (unsigned long long)best ^ 0x8000000000000000ull;
+                if (exact) {
+                    key = order_f32(scores[pg]);
+                } else {
+                    const int id = bt[pg];
+                    if (id >= 0 && id < p.num_pages)
+                        key = exact_key<D>(bounds + (long long)id * p.b_s[0], q + (TB == 1 ? 0 : team.id) * p.q_s[1], p.q_s[2], p.G, lane);
                 }
                 if (lane == 0) keys[pg] = key;
             }
         }
-        __syncthreads();
-        if (s_amb <= 256) {
+        team.sync();
+        if (n_amb <= kSelList) {
             // by rank among the undecided
-            for (int w = tid; w < nw; w += kSelThreads)
-                for (unsigned int bits = amb[w]; bits; bits &= bits - 1) s_list[atomicAdd(&s_cnt, 1)] = 32 * w + __ffs(bits) - 1;
-            __syncthreads();
-            if (tid < s_amb) {
-                const int pg = s_list[tid];
+            unsigned int *cnt = team.words + 14;
+            if (team.t == 0) *cnt = 0;
+            team.sync();
+            team.each(nw, [&](int w) {
+                for (unsigned int bits = amb[w]; bits; bits &= bits - 1) list[atomicAdd(cnt, 1u)] = 32 * w + __ffs(bits) - 1;
+            });
+            team.sync();
+            team.each(n_amb, [&](int i) {
+                const int pg = list[i];
                 const unsigned long long key = keys[pg];
                 int ahead = 0;
-                for (int j = 0; j < s_amb; ++j) {
-                    const int o = s_list[j];
+                for (int j = 0; j < n_amb; ++j) {
+                    const int o = list[j];
                     ahead += keys[o] > key || (keys[o] == key && o < pg);
                 }
-                if (ahead < slots) atomicOr(&sel[pg >> 5], 1u << (pg & 31));
-            }
+                if (ahead < places) atomicOr(&sel[pg >> 5], 1u << (pg & 31));
+            });
         } else {
             int left;
-            const unsigned long long t = kth_largest<64, unsigned long long>(n, slots, hist, res, &left, [&](int j, unsigned long long *v) {
+            const unsigned long long t = team.kth_key(n, places, &left, [&](int j, unsigned long long *v) {
                 if (!(amb[j >> 5] >> (j & 31) & 1u)) return false;
                 *v = keys[j];
                 return true;
             });
-            if (warp == 0) {  // ties at the threshold in index order
+            if (tw == 0) {  // ties at the threshold in index order
                 for (int w = 0; w < nw; ++w) {
                     const bool on = amb[w] >> lane & 1u;
                     const unsigned long long key = on ? keys[32 * w + lane] : 0;
@@ -510,30 +794,32 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
             }
         }
     }
-    __syncthreads();
+    team.sync();
     // ---- the chosen pages in ascending order: thread t lists words [t per, (t + 1) per)
-    const int per = (nw + kSelThreads - 1) / kSelThreads;
+    const int per = (nw + 32 * C::W - 1) / (32 * C::W);
     int cnt = 0;
-    for (int w = tid * per; w < min(nw, (tid + 1) * per); ++w) cnt += __popc(sel[w]);
+    for (int w = team.t * per; w < min(nw, (team.t + 1) * per); ++w) cnt += __popc(sel[w]);
     int incl = cnt;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int x = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += x;
     }
-    if (lane == 31) s_scan[warp] = incl;
-    __syncthreads();
     int at = incl - cnt;
-    for (int w = 0; w < warp; ++w) at += s_scan[w];
-    for (int w = tid * per; w < min(nw, (tid + 1) * per); ++w)
+    if constexpr (C::W > 1) {
+        if (lane == 31) team.words[tw] = (unsigned)incl;
+        team.sync();
+        for (int w = 0; w < tw; ++w) at += (int)team.words[w];
+    }
+    for (int w = team.t * per; w < min(nw, (team.t + 1) * per); ++w)
         for (unsigned int bits = sel[w]; bits; bits &= bits - 1)
             if (at < p.K) out[at++] = 32 * w + __ffs(bits) - 1;
 }
 
-template <int D, int NT>
+template <int D, int NT, int TB>
 cudaError_t launch_select(const SelectParams &p, unsigned int rows, cudaStream_t s) {
-    const int smem = SelCfg<D, NT>::smem(p.tab.max_pages);
-    cudaError_t e = cudaFuncSetAttribute(select_pages_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const int smem = SelCfg<D, NT, TB>::smem(p.tab.max_pages);
+    cudaError_t e = cudaFuncSetAttribute(select_pages_kernel<D, NT, TB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(rows * p.cluster);
@@ -545,8 +831,14 @@ cudaError_t launch_select(const SelectParams &p, unsigned int rows, cudaStream_t
     attr[0].val.clusterDim.x = p.cluster;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, select_pages_kernel<D, NT>, p);
+    cfg.numAttrs = p.cluster > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, select_pages_kernel<D, NT, TB>, p);
+}
+
+template <int D>
+cudaError_t launch_select_dim(const SelectParams &p, unsigned int rows, bool four, cudaStream_t s) {
+    if (four) return p.G <= 2 ? launch_select<D, 1, 4>(p, rows, s) : (p.G <= 4 ? launch_select<D, 2, 4>(p, rows, s) : launch_select<D, 4, 4>(p, rows, s));
+    return p.G <= 8 ? launch_select<D, 1, 1>(p, rows, s) : launch_select<D, 2, 1>(p, rows, s);
 }
 
 }  // namespace fa8
@@ -674,25 +966,28 @@ fa8_status fa8_select_pages(const fa8_tensor *q, const fa8_tensor *bounds, fa8_t
     p.keep_last = keep_last;
     p.num_pages = (int)bounds->shape[0];
     p.status = ds->status;
-    // Few (token, kv-head) pairs: a cluster of CTAs shares each pair's pages, as long as every CTA
-    // keeps two steps of its eight warps (512 pages) and the clusters fit the GPU at once.
+    p.timeout_ns = wait_timeout_ns();
+    // Several tokens per request and enough of them to fill the GPU in blocks of four: one pass over
+    // the bounds serves four tokens.  Else a token at a time, and where there are few (token, kv-head)
+    // pairs a cluster of CTAs shares each pair's pages, 128 or more a CTA.
+    const long long blocks = p.cu_q ? (long long)qs.T / 4 + qs.B : (long long)qs.B * ((qs.Sq + 3) / 4);
+    const bool four = p.G <= 8 && (long long)qs.T >= 4LL * qs.B && blocks * Hkv >= 2LL * ds->sm_count &&
+                      p.tab.max_pages <= fa8::kSelMaxTable4;
     p.cluster = 1;
-    while (p.cluster < fa8::kSelMaxCluster && rows * p.cluster * 2 <= ds->sm_count && p.tab.max_pages >= 256 * p.cluster * 2)
-        p.cluster *= 2;
+    if (!four)
+        while (p.cluster < fa8::kSelMaxCluster && rows * p.cluster * 2 <= 4LL * ds->sm_count && p.tab.max_pages >= 128 * p.cluster * 2)
+            p.cluster *= 2;
+    if (blocks * Hkv > 0x7fffffffLL) return fail(FA8_ERR_UNSUPPORTED, "problem too large for the grid");
+    const unsigned grid = (unsigned)(four ? blocks * Hkv : rows);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaErrorInvalidValue;
-#define FA8_SELECT(D_)                                                                   \
-    case D_:                                                                             \
-        e = p.G <= 8 ? fa8::launch_select<D_, 1>(p, (unsigned)rows, s) : fa8::launch_select<D_, 2>(p, (unsigned)rows, s); \
-        break;
     switch (qs.D) {
-        FA8_SELECT(64)
-        FA8_SELECT(96)
-        FA8_SELECT(128)
-        FA8_SELECT(192)
-        FA8_SELECT(256)
+        case 64: e = fa8::launch_select_dim<64>(p, grid, four, s); break;
+        case 96: e = fa8::launch_select_dim<96>(p, grid, four, s); break;
+        case 128: e = fa8::launch_select_dim<128>(p, grid, four, s); break;
+        case 192: e = fa8::launch_select_dim<192>(p, grid, four, s); break;
+        case 256: e = fa8::launch_select_dim<256>(p, grid, four, s); break;
     }
-#undef FA8_SELECT
     if (e != cudaSuccess) return cuda_fail(e, "page selection kernel launch");
     return FA8_SUCCESS;
 }

@@ -99,6 +99,14 @@ __device__ __forceinline__ Bytes<N> ld_shared(uint32_t addr) {
     return r;
 }
 
+// `bytes` (a multiple of 16) from global to shared memory, both 16-byte aligned; completion is
+// signalled on `bar` as transaction bytes
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
 // ---------------------------------------------------------------- clusters
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;

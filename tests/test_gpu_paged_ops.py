@@ -83,6 +83,13 @@ SELECT = [
     dict(keys=[8200], new=[1], K=64, ps=8, Hq=8, Hkv=1, width=1100),       # clusters
     dict(keys=[33000], new=[1], K=100, ps=8, Hq=16, Hkv=1, width=4200, D=64),
     dict(keys=[2, 5], new=[4, 9], K=2, packed=True),                         # more new tokens than keys
+    # enough tokens for blocks of four: 1, 2, 3 and 8 q-heads per kv-head, ragged blocks, short and empty
+    # requests, tokens on both sides of top_k
+    dict(keys=[300, 400], new=[90] * 2, K=11, Hq=13, Hkv=13, ps=8, D=64),
+    dict(keys=[300, 91], new=[91] * 2, K=4, Hq=26, Hkv=13, ps=8, D=96),
+    dict(keys=[250, 0, 333, 60], new=[101, 0, 222, 60], K=5, Hq=15, Hkv=5, packed=True, tail=2),
+    dict(keys=[600, 500], new=[77] * 2, K=9, Hq=64, Hkv=8, ps=16, D=192, causal=False),
+    dict(keys=[200], new=[200], K=20, Hq=48, Hkv=8, ps=8, D=256, kf=2, kl=3),
 ]
 
 
@@ -101,10 +108,11 @@ def test_select_pages(c):
     assert (lists[p.T:] == -7).all() if p.packed else True  # rows behind the last sequence
 
 
+@pytest.mark.parametrize("four", [False, True], ids=["one", "four"])
 @pytest.mark.parametrize("K", [2, 37, 300])
 @pytest.mark.parametrize("kind", ["all_equal", "zero_query", "few_levels", "cancel", "one_ulp", "nan_page", "nan_query",
                                   "many_ties"])
-def test_select_pages_ties_and_close_scores(kind, K):
+def test_select_pages_ties_and_close_scores(kind, K, four):
     """Scores that are equal, or differ only below fp32: the choice is that of exact numbers."""
     p = Problem([8 * 700], [1], Hq=8, Hkv=1, D=128, ps=8, seed=5)
     n = 700
@@ -135,7 +143,15 @@ def test_select_pages_ties_and_close_scores(kind, K):
         bnd[phys[50:650]] = bnd[phys[50]].clone()
     p.q = q.float().to(E4M3)
     b8 = bnd.float().to(E4M3)
-    assert torch.equal(run_select(p, b8, K)[0, 0], ref.select(p, b8, K)[0])
+    want = ref.select(p, b8, K)[0]
+    if four:  # the same token many times over, enough of them for blocks of four
+        m = 1301
+        p.q = p.q.view(torch.uint8).expand(1, m, -1, -1).contiguous().view(E4M3)
+        p.new, p.T = [m], m
+        got = run_select(p, b8, K, causal=False)
+        assert (got == want).all()
+    else:
+        assert torch.equal(run_select(p, b8, K)[0, 0], want)
 
 
 def test_select_pages_strided():
