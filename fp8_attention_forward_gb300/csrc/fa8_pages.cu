@@ -121,7 +121,6 @@ struct SelectParams {
     long long o_s[3];  // request, token, head
     const int *cu_q;
     int T, B, Sq, Hkv, G, K, causal, keep_first, keep_last, num_pages, cluster;
-    unsigned long long timeout_ns;
     host::Table tab;
     unsigned int *status;
 };
@@ -130,6 +129,10 @@ constexpr int kSelWarps = 4, kSelThreads = kSelWarps * 32;
 constexpr int kSelMaxTable = 16384;  // block_table columns
 constexpr int kSelMaxTable4 = 2048;  // of the kernel that takes four tokens at once
 constexpr int kSelMaxCluster = 8;
+#ifndef SB
+#define SB 2
+#endif
+constexpr int kSelBufs = SB;  // buffers of a warp, 16 pages each
 constexpr int kSelBins = 256, kSelList = 256;
 
 // TB tokens of one request per CTA.  TB = 1: the q-heads in groups of 8 NT rows, all four warps choose.
@@ -143,7 +146,7 @@ struct SelCfg {
     static constexpr int NV = ROW / 64;      // 16-byte vectors of a row per lane
     static constexpr int STEPS = ROW / 16;   // MMA k-steps
     static constexpr int BUF = 16 * PITCH;   // 16 pages
-    static constexpr int RING = kSelWarps * 2 * BUF;
+    static constexpr int RING = kSelWarps * kSelBufs * BUF;
     static constexpr int QR = TB == 1 ? 8 * NT : TB * GP;  // query rows of one pass
     static constexpr int Q_BYTES = NT * STEPS * 32 * 8 + QR * D;  // as MMA fragments, and as they are
     static constexpr int W = kSelWarps / TB;  // warps that choose for a token
@@ -272,6 +275,7 @@ struct Team {
                 each(count, [&](int i) {
                     const unsigned int u = (unsigned int)list[i];
                     int above = 0, same = 0;
+#pragma unroll 8
                     for (int j = 0; j < count; ++j) {
                         const unsigned int o = (unsigned int)list[j];
                         above += o > u;
@@ -334,10 +338,10 @@ struct Team {
     }
 };
 
-// Exact score of one page for one token, by a warp: sum_c max(q_c lo_c, q_c hi_c) in units of 2^-18 for
-// each q-head, the largest; a NaN ranks above all.  Order-preserving unsigned key.
+// Exact score of one page for q-heads [first, end) of a token, by a warp: sum_c max(q_c lo_c, q_c hi_c) in
+// units of 2^-18, the largest of the heads; a NaN ranks above all.  Order-preserving unsigned key.
 template <int D>
-__device__ __forceinline__ unsigned long long exact_key(const uint8_t *src, const uint8_t *q, long long q_sh, int G, int lane) {
+__device__ __forceinline__ unsigned long long exact_key(const uint8_t *src, const uint8_t *q, long long q_sh, int first, int end, int lane) {
     constexpr int NW = (D / 4 + 31) / 32;  // words of four channels per lane
     auto has_nan = [](uint32_t w) { return (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0; };
     int lo[NW][4], hi[NW][4];
@@ -355,13 +359,13 @@ __device__ __forceinline__ unsigned long long exact_key(const uint8_t *src, cons
         }
     }
     long long best = LLONG_MIN;
-    for (int h0 = 0; h0 < G; h0 += 4) {
+    for (int h0 = first; h0 < end; h0 += 4) {
         uint32_t w[4][NW];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
 #pragma unroll
             for (int i = 0; i < NW; ++i)
-                w[k][i] = lane + 32 * i < D / 4 ? *reinterpret_cast<const uint32_t *>(q + min(h0 + k, G - 1) * q_sh + 4 * (lane + 32 * i)) : 0u;
+                w[k][i] = lane + 32 * i < D / 4 ? *reinterpret_cast<const uint32_t *>(q + min(h0 + k, end - 1) * q_sh + 4 * (lane + 32 * i)) : 0u;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             long long s = 0;
@@ -387,7 +391,7 @@ __device__ __forceinline__ unsigned long long exact_key(const uint8_t *src, cons
 
 // Every CTA scores its pages with f16 MMAs (pages on M, query rows on N; the contraction runs over
 // [lo | hi] against [min(q,0) | max(q,0)], which is sum_c max(q_c lo_c, q_c hi_c)); a page's 2 D bytes
-// arrive by one bulk copy, 16 pages a buffer, two buffers a warp.  With few rows a cluster of CTAs
+// arrive by asynchronous copies, 16 pages a buffer, two buffers a warp.  With few rows a cluster of CTAs
 // shares a token's pages and rank 0 chooses.
 //
 // Exact choice from fp32 scores: E4M3 products are exact, an MMA adds 16 of them to the running
@@ -401,8 +405,6 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
     using C = SelCfg<D, NT, TB>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
-    __shared__ __align__(8) uint64_t s_bar[kSelWarps][2];
-    __shared__ int s_abort;
     __shared__ float s_l1[kSelWarps][TB], s_kmax[kSelMaxCluster], s_kw[kSelWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int CS = TB == 1 ? p.cluster : 1;
@@ -476,40 +478,39 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
 
     // ---- scores of this CTA's pages: chunk it is pages from + 16 ((warp + 4 it) CS + rank) ..
     uint2 *qf = reinterpret_cast<uint2 *>(smem);
-    const uint32_t ring = ptx::smem_u32(smem + C::Q_BYTES) + warp * 2 * C::BUF, bar = ptx::smem_u32(s_bar[warp]);
-    if (lane == 0) {
-        ptx::mbar_init(bar, 1);
-        ptx::mbar_init(bar + 8, 1);
-        ptx::fence_mbar_init();
-        ptx::fence_proxy_async_smem();
-    }
-    if (tid == 0) s_abort = 0;
-    __syncthreads();
-    const Waiter W{&s_abort, p.timeout_ns, p.status};
+    const uint32_t ring = ptx::smem_u32(smem + C::Q_BYTES) + warp * kSelBufs * C::BUF;
     const int p0 = from + 16 * (warp * CS + rank), stride = 16 * kSelWarps * CS;
     const int chunks = to > p0 ? (to - p0 + stride - 1) / stride : 0;
-    uint32_t uses = 0;  // fills of each buffer so far: the parity of its barrier
     uint32_t kmax2[4] = {0, 0, 0, 0};
     float l1[TB];
 #pragma unroll
     for (int t = 0; t < TB; ++t) l1[t] = 0.f;
     for (int g0 = 0; g0 < (TB == 1 ? p.G : 1); g0 += 8 * NT) {
-        unsigned int on[2] = {0, 0};  // valid pages of each buffer
+        // lane i < 16 holds the i-th page of the chunk that is fetched next; eight consecutive lanes copy
+        // 128 consecutive bytes
         auto id_of = [&](int it) { return lane < 16 && it < chunks && p0 + it * stride + lane < to ? bt[p0 + it * stride + lane] : -1; };
         int id = id_of(0);
-        auto fetch = [&](int it) {
+        auto fetch = [&](int it, int buf) {
             const bool ok = id >= 0 && id < p.num_pages;
             if (!ok && lane < 16 && p0 + it * stride + lane < to) atomicOr(p.status, kStatusBounds);
             const unsigned int m = __ballot_sync(0xffffffffu, ok);
-            const uint32_t bb = bar + 8 * (it & 1);
-            if (lane == 0) ptx::mbar_arrive_expect_tx(bb, (uint32_t)(__popc(m) * C::ROW));
-            __syncwarp();
-            if (ok) bulk_load(ring + (it & 1) * C::BUF + lane * C::PITCH, bounds + (long long)id * p.b_s[0], C::ROW, bb);
-            on[it & 1] = m;
+            const long long off = ok ? id * p.b_s[0] : 0;
+#pragma unroll
+            for (int u = 0; u < C::ROW / 32; ++u) {
+                const int x = 32 * u + lane, r = x / (C::ROW / 16), ch = x - r * (C::ROW / 16);
+                const uint8_t *src = bounds + __shfl_sync(0xffffffffu, off, r) + 16 * ch;
+                const bool there = m >> r & 1u;
+                cp_async16(ring + buf * C::BUF + r * C::PITCH + 16 * ch, there ? src : p.bounds, there ? 16 : 0);
+            }
             id = id_of(it + 1);
+            return m;
         };
-        if (chunks > 0) fetch(0);
-        if (chunks > 1) fetch(1);
+        unsigned int live[kSelBufs];
+#pragma unroll
+        for (int i = 0; i < kSelBufs; ++i) {
+            live[i] = i < chunks ? fetch(i, i) : 0;
+            cp_async_commit();
+        }
         // the query rows, while the first pages arrive; padding rows repeat a real one: the maximum
         // does not see them
         if (g0) __syncthreads();
@@ -555,15 +556,13 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
                 if (TB == 1 || r / C::GP == t) l1[t] = fmaxf(l1[t], s);
         }
         __syncthreads();
-        bool alive = true;
-        for (int it = 0; it < chunks; ++it) {
-            const int bi = it & 1;
-            if (!W.wait_warp(bar + 8 * bi, (uses >> bi) & 1)) {
-                if (it + 1 < chunks) W.drain(bar + 8 * (bi ^ 1), (uses >> (bi ^ 1)) & 1);
-                alive = false;
-                break;
-            }
-            uses ^= 1u << bi;
+        for (int it0 = 0; it0 < chunks; it0 += kSelBufs)
+#pragma unroll
+        for (int bi = 0; bi < kSelBufs; ++bi) {
+            const int it = it0 + bi;
+            if (it >= chunks) break;
+            cp_async_wait<kSelBufs - 1>();
+            __syncwarp();
             const uint32_t buf = ring + bi * C::BUF + (lane >> 2) * C::PITCH + 16 * (lane & 3);
             float acc[NT][4], acc2[NT][4];  // two chains of dependent MMAs
 #pragma unroll
@@ -594,9 +593,10 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[t][e] += acc2[t][e];
-            const unsigned int ok = on[bi];
+            const unsigned int ok = live[bi];
             __syncwarp();  // the buffer has been read
-            if (it + 2 < chunks) fetch(it + 2);
+            if (it + kSelBufs < chunks) live[bi] = fetch(it + kSelBufs, bi);
+            cp_async_commit();
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const int pl = 8 * half + (lane >> 2), pg = p0 + it * stride + pl, c = lane & 3;
@@ -640,7 +640,7 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
                 }
             }
         }
-        if (!alive) break;
+        cp_async_wait<0>();
     }
     {
         float k = 0.f;
@@ -737,18 +737,30 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
     } else if (places > 0 && n_amb > 0) {
         // Keys that order the undecided pages exactly.  All-zero queries or bounds leave exact zeros.
         const bool exact = !(eps2 > 0.f);
-        for (int w = tw; w < nw; w += C::W) {
+        // Many pages: one to a warp.  Few: every warp takes a part of each page's heads.
+        const bool split = C::W > 1 && n_amb < 4 * C::W;
+        const int hs = split ? tw * p.G / C::W : 0, he = split ? (tw + 1) * p.G / C::W : p.G;
+        if (split) {
+            team.each(nw, [&](int w) {
+                for (unsigned int bits = amb[w]; bits; bits &= bits - 1) keys[32 * w + __ffs(bits) - 1] = 0;
+            });
+            team.sync();
+        }
+        for (int w = split ? 0 : tw; w < nw; w += split ? 1 : C::W) {
             for (unsigned int bits = amb[w]; bits; bits &= bits - 1) {
                 const int pg = 32 * w + __ffs(bits) - 1;
                 unsigned long long key = 0;
                 if (exact) {
                     key = order_f32(scores[pg]);
-                } else {
+                } else if (hs < he) {
                     const int id = bt[pg];
                     if (id >= 0 && id < p.num_pages)
-                        key = exact_key<D>(bounds + (long long)id * p.b_s[0], q + (TB == 1 ? 0 : team.id) * p.q_s[1], p.q_s[2], p.G, lane);
+                        key = exact_key<D>(bounds + (long long)id * p.b_s[0], q + (TB == 1 ? 0 : team.id) * p.q_s[1], p.q_s[2], hs, he, lane);
                 }
-                if (lane == 0) keys[pg] = key;
+                if (lane == 0) {
+                    if (split) atomicMax(&keys[pg], key);
+                    else keys[pg] = key;
+                }
             }
         }
         team.sync();
@@ -966,7 +978,6 @@ fa8_status fa8_select_pages(const fa8_tensor *q, const fa8_tensor *bounds, fa8_t
     p.keep_last = keep_last;
     p.num_pages = (int)bounds->shape[0];
     p.status = ds->status;
-    p.timeout_ns = wait_timeout_ns();
     // Several tokens per request and enough of them to fill the GPU in blocks of four: one pass over
     // the bounds serves four tokens.  Else a token at a time, and where there are few (token, kv-head)
     // pairs a cluster of CTAs shares each pair's pages, 128 or more a CTA.
