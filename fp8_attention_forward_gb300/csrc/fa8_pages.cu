@@ -129,11 +129,8 @@ constexpr int kSelWarps = 4, kSelThreads = kSelWarps * 32;
 constexpr int kSelMaxTable = 16384;  // block_table columns
 constexpr int kSelMaxTable4 = 2048;  // of the kernel that takes four tokens at once
 constexpr int kSelMaxCluster = 8;
-#ifndef SB
-#define SB 2
-#endif
-constexpr int kSelBufs = SB;  // buffers of a warp, 16 pages each
-constexpr int kSelBins = 256, kSelList = 256;
+constexpr int kSelList = 256;  // undecided pages that are ranked directly
+constexpr int kSelHeld = 16;   // scores that a thread keeps in registers while it chooses
 
 // TB tokens of one request per CTA.  TB = 1: the q-heads in groups of 8 NT rows, all four warps choose.
 // TB = 4: each token's q-heads padded to GP = 2, 4 or 8 rows, so that the four tokens are the 4 GP
@@ -146,14 +143,14 @@ struct SelCfg {
     static constexpr int NV = ROW / 64;      // 16-byte vectors of a row per lane
     static constexpr int STEPS = ROW / 16;   // MMA k-steps
     static constexpr int BUF = 16 * PITCH;   // 16 pages
-    static constexpr int RING = kSelWarps * kSelBufs * BUF;
+    static constexpr int RING = kSelWarps * 2 * BUF;
     static constexpr int QR = TB == 1 ? 8 * NT : TB * GP;  // query rows of one pass
     static constexpr int Q_BYTES = NT * STEPS * 32 * 8 + QR * D;  // as MMA fragments, and as they are
     static constexpr int W = kSelWarps / TB;  // warps that choose for a token
-    // per token after the ring: fp32 scores, bins, list, scratch, two bit masks; the 64-bit keys of
-    // undecided pages take the ring's place
+    // per token after the ring: fp32 scores, list, scratch, two bit masks; the 64-bit keys of undecided
+    // pages take the ring's place
     static __host__ __device__ int words(int table) { return (table + 31) / 32; }
-    static __host__ __device__ int token_bytes(int table) { return words(table) * (32 * 4 + 8) + kSelBins * 4 + kSelList * 4 + 64; }
+    static __host__ __device__ int token_bytes(int table) { return words(table) * (32 * 4 + 8) + kSelList * 4 + 64; }
     static __host__ __device__ int front(int table) {
         const int keys = TB * words(table) * 32 * 8;
         return Q_BYTES + (keys > RING ? keys : RING);
@@ -175,11 +172,12 @@ __device__ __forceinline__ int fixed_e4m3(unsigned int code) {
     return (code & 0x80u) ? -v : v;
 }
 
-// The threads that choose for one token: W warps with their own barrier.
+// The threads that choose for one token: W warps with their own barrier.  Most of what they run, they
+// run once: short loops, because fetching unrolled code costs more than it saves.
 template <int W>
 struct Team {
-    int t, id;               // thread of the team, team of the CTA
-    unsigned int *bins, *words;  // kSelBins; 16 words of scratch
+    int t, id;            // thread of the team, team of the CTA
+    unsigned int *words;  // 16 words of scratch
     __device__ __forceinline__ void sync() const {
         if constexpr (W == 1) __syncwarp();
         else ptx::named_bar_sync(1 + id, 32 * W);
@@ -187,153 +185,83 @@ struct Team {
     // f over [0, n), each index by one thread
     template <typename F>
     __device__ __forceinline__ void each(int n, F f) const {
+#pragma unroll 1
         for (int i = t; i < n; i += 32 * W) f(i);
     }
-    // f(index, value) over scores [from, to), eight loads at a time
-    template <typename F>
-    __device__ __forceinline__ void scan(const float *scores, int from, int to, F f) const {
-        for (int i0 = from + t; i0 < to; i0 += 8 * 32 * W) {
-            float v[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = scores[min(i0 + j * 32 * W, to - 1)];
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (i0 + j * 32 * W < to) f(i0 + j * 32 * W, v[j]);
-        }
-    }
-    // lane l of the team's first warp: bins 8 l .. 8 l + 7; finds the bin that holds the rank-th entry from
-    // above and leaves it, the rank within it and its count in words[0 .. 2]
-    __device__ __forceinline__ void find_bin(int rank) const {
-        if (t >= 32) return;
-        const uint4 x = *reinterpret_cast<const uint4 *>(bins + 8 * t), y = *reinterpret_cast<const uint4 *>(bins + 8 * t + 4);
-        const int c[8] = {(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w};
-        int own = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) own += c[j];
-        int incl = own;  // entries in this lane's bins and above
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_down_sync(0xffffffffu, incl, o);
-            if (t + o < 32) incl += v;
-        }
-        int above = incl - own;
-#pragma unroll
-        for (int j = 7; j >= 0; --j) {
-            if (above < rank && rank <= above + c[j]) {
-                words[0] = 8 * t + j;
-                words[1] = (unsigned int)(rank - above);
-                words[2] = (unsigned int)c[j];
-            }
-            above += c[j];
-        }
-    }
-    __device__ __forceinline__ unsigned int max32(unsigned int v) const {
-        v = __reduce_max_sync(0xffffffffu, v);
+    // sum over the team of one value a thread; its maximum (MAX)
+    template <bool MAX>
+    __device__ __forceinline__ unsigned int reduce(unsigned int v) const {
+        v = MAX ? __reduce_max_sync(0xffffffffu, v) : __reduce_add_sync(0xffffffffu, v);
         if constexpr (W > 1) {
+            sync();  // the words have been read
             if ((t & 31) == 0) words[t >> 5] = v;
             sync();
             v = words[0];
 #pragma unroll
-            for (int i = 1; i < W; ++i) v = max(v, words[i]);
-            sync();
+            for (int i = 1; i < W; ++i) v = MAX ? max(v, words[i]) : v + words[i];
         }
         return v;
     }
-    // The rank-th largest (rank >= 1) of scores [from, to): bins over the span that is left, which spreads
-    // real scores evenly whatever their exponents, until few enough share a bin to be ranked directly.
-    __device__ __forceinline__ float kth_score(const float *scores, int from, int to, int rank, int *list) const {
-        unsigned int hi = 0, nlo = 0;
-        scan(scores, from, to, [&](int, float v) {
-            const unsigned int u = order_f32(v);
+    // The rank-th largest (rank >= 1) of scores [0, n), as ordered integers: bisection by counting, done
+    // when exactly `rank` scores lie in the upper part (after about as many steps as n has bits).
+    __device__ __forceinline__ unsigned int kth_score(const float *scores, int n, unsigned int rank) const {
+        unsigned int v[kSelHeld], hi = 0, nlo = 0;
+#pragma unroll
+        for (int j = 0; j < kSelHeld; ++j) {
+            const int i = t + 32 * W * j;
+            v[j] = i < n ? order_f32(scores[i]) : 0u;  // no score is 0: that is a NaN's place
+        }
+#pragma unroll
+        for (int j = 0; j < kSelHeld; ++j) {
+            hi = max(hi, v[j]);
+            if (v[j]) nlo = max(nlo, ~v[j]);
+        }
+#pragma unroll 1
+        for (int i = t + 32 * W * kSelHeld; i < n; i += 32 * W) {
+            const unsigned int u = order_f32(scores[i]);
             hi = max(hi, u);
             nlo = max(nlo, ~u);
-        });
-        hi = max32(hi);
-        unsigned int lo = ~max32(nlo);
+        }
+        hi = reduce<true>(hi);
+        unsigned int lo = ~reduce<true>(nlo);
+#pragma unroll 1
         while (lo < hi) {
-            const int bits = 32 - __clz((int)(hi - lo)), shift = bits > 8 ? bits - 8 : 0;
-            each(kSelBins, [&](int i) { bins[i] = 0; });
-            if (t == 0) words[3] = 0;
-            sync();
-            scan(scores, from, to, [&](int, float v) {
-                const unsigned int u = order_f32(v);
-                if (u >= lo && u <= hi) atomicAdd(&bins[(u - lo) >> shift], 1u);
-            });
-            sync();
-            find_bin(rank);
-            sync();
-            lo += words[0] << shift;
-            rank = (int)words[1];
-            const int count = (int)words[2];
-            if (hi - lo > (1u << shift) - 1u) hi = lo + ((1u << shift) - 1u);
-            if (count <= 64 && lo < hi) {
-                scan(scores, from, to, [&](int, float v) {
-                    const unsigned int u = order_f32(v);
-                    if (u >= lo && u <= hi) list[atomicAdd(&words[3], 1u)] = (int)u;
-                });
-                sync();
-                each(count, [&](int i) {
-                    const unsigned int u = (unsigned int)list[i];
-                    int above = 0, same = 0;
-#pragma unroll 8
-                    for (int j = 0; j < count; ++j) {
-                        const unsigned int o = (unsigned int)list[j];
-                        above += o > u;
-                        same += o == u;
-                    }
-                    if (above < rank && rank <= above + same) words[4] = u;
-                });
-                sync();
-                lo = hi = words[4];
-            }
-            sync();
-        }
-        return unorder_f32(lo);
-    }
-    // maximum (unsigned) over the team of one value a thread
-    __device__ __forceinline__ unsigned long long max64(unsigned long long v) const {
+            const unsigned int mid = lo + (hi - lo + 1) / 2;
+            unsigned int c = 0, low = 0;  // scores from mid up: how many, and the complement of the least
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
-        if constexpr (W > 1) {
-            unsigned long long *w = reinterpret_cast<unsigned long long *>(words);
-            if ((t & 31) == 0) w[t >> 5] = v;
-            sync();
-            v = w[0];
-#pragma unroll
-            for (int i = 1; i < W; ++i) v = max(v, w[i]);
-            sync();
-        }
-        return v;
-    }
-    // The same over the 64-bit keys that key(i, &u) yields for i in [0, n); `left`: how many keys equal
-    // to the result are among the rank largest.
-    template <typename F>
-    __device__ __forceinline__ unsigned long long kth_key(int n, int rank, int *left, F key) const {
-        unsigned long long hi = 0, nlo = 0, u;
-        each(n, [&](int i) {
-            if (key(i, &u)) {
-                hi = max(hi, u);
-                nlo = max(nlo, ~u);
+            for (int j = 0; j < kSelHeld; ++j) c += v[j] >= mid;
+#pragma unroll 1
+            for (int i = t + 32 * W * kSelHeld; i < n; i += 32 * W) c += order_f32(scores[i]) >= mid;
+            c = reduce<false>(c);
+            if (c < rank) {
+                hi = mid - 1;
+                continue;
             }
-        });
-        hi = max64(hi);
-        unsigned long long lo = ~max64(nlo);
+            lo = mid;
+            if (c > rank) continue;
+#pragma unroll
+            for (int j = 0; j < kSelHeld; ++j)
+                if (v[j] >= mid) low = max(low, ~v[j]);
+#pragma unroll 1
+            for (int i = t + 32 * W * kSelHeld; i < n; i += 32 * W) {
+                const unsigned int u = order_f32(scores[i]);
+                if (u >= mid) low = max(low, ~u);
+            }
+            return ~reduce<true>(low);
+        }
+        return lo;
+    }
+    // The largest key that at least `rank` (>= 1) of keys [0, n) reach.  Keys of 0 are none.
+    __device__ __forceinline__ unsigned long long kth_key(const unsigned long long *keys, int n, unsigned int rank) const {
+        unsigned long long lo = 0, hi = ~0ull;
+#pragma unroll 1
         while (lo < hi) {
-            const int bits = 64 - __clzll((long long)(hi - lo)), shift = bits > 8 ? bits - 8 : 0;
-            each(kSelBins, [&](int i) { bins[i] = 0; });
-            sync();
-            each(n, [&](int i) {
-                if (key(i, &u) && u >= lo && u <= hi) atomicAdd(&bins[(unsigned int)((u - lo) >> shift)], 1u);
-            });
-            sync();
-            find_bin(rank);
-            sync();
-            lo += (unsigned long long)words[0] << shift;
-            rank = (int)words[1];
-            if (hi - lo > (1ull << shift) - 1ull) hi = lo + ((1ull << shift) - 1ull);
-            sync();
+            const unsigned long long mid = lo + (hi - lo) / 2 + 1;
+            unsigned int c = 0;
+            each(n, [&](int i) { c += keys[i] >= mid; });
+            if (reduce<false>(c) >= rank) lo = mid;
+            else hi = mid - 1;
         }
-        *left = rank;
         return lo;
     }
 };
@@ -359,32 +287,25 @@ __device__ __forceinline__ unsigned long long exact_key(const uint8_t *src, cons
         }
     }
     long long best = LLONG_MIN;
-    for (int h0 = first; h0 < end; h0 += 4) {
-        uint32_t w[4][NW];
+#pragma unroll 1
+    for (int h = first; h < end; ++h) {
+        long long s = 0;
+        bool bad = nan;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int i = 0; i < NW; ++i) {
+            const uint32_t w = lane + 32 * i < D / 4 ? *reinterpret_cast<const uint32_t *>(q + h * q_sh + 4 * (lane + 32 * i)) : 0u;
+            bad |= has_nan(w);
 #pragma unroll
-            for (int i = 0; i < NW; ++i)
-                w[k][i] = lane + 32 * i < D / 4 ? *reinterpret_cast<const uint32_t *>(q + min(h0 + k, end - 1) * q_sh + 4 * (lane + 32 * i)) : 0u;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            long long s = 0;
-            bool bad = nan;
-#pragma unroll
-            for (int i = 0; i < NW; ++i) {
-                bad |= has_nan(w[k][i]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int x = fixed_e4m3(w[k][i] >> (8 * e) & 0xFFu);
-                    s += (long long)x * (x < 0 ? lo[i][e] : hi[i][e]);
-                }
+            for (int e = 0; e < 4; ++e) {
+                const int x = fixed_e4m3(w >> (8 * e) & 0xFFu);
+                s += (long long)x * (x < 0 ? lo[i][e] : hi[i][e]);
             }
-            // |s| < 2^40: 20 low bits and the rest are summed apart
-            const unsigned int low = __reduce_add_sync(0xffffffffu, (unsigned int)s & 0xFFFFFu);
-            const int high = __reduce_add_sync(0xffffffffu, (int)(s >> 20));
-            const long long sum = ((long long)high << 20) + low;
-            best = max(best, __any_sync(0xffffffffu, bad) ? LLONG_MAX : sum);
         }
+        // |s| < 2^40: 20 low bits and the rest are summed apart
+        const unsigned int low = __reduce_add_sync(0xffffffffu, (unsigned int)s & 0xFFFFFu);
+        const int high = __reduce_add_sync(0xffffffffu, (int)(s >> 20));
+        const long long sum = ((long long)high << 20) + low;
+        best = max(best, __any_sync(0xffffffffu, bad) ? LLONG_MAX : sum);
     }
     return (unsigned long long)best ^ 0x8000000000000000ull;
 }
@@ -460,8 +381,7 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
     const int words = C::words(p.tab.max_pages);
     uint8_t *mine = smem + C::front(p.tab.max_pages) + team.id * ((C::token_bytes(p.tab.max_pages) + 15) & ~15);
     float *scores = reinterpret_cast<float *>(mine);
-    team.bins = reinterpret_cast<unsigned int *>(mine + words * 128);
-    int *list = reinterpret_cast<int *>(team.bins + kSelBins);
+    int *list = reinterpret_cast<int *>(mine + words * 128);
     team.words = reinterpret_cast<unsigned int *>(list + kSelList);
     unsigned int *sel = team.words + 16, *amb = sel + words;
     unsigned long long *keys = reinterpret_cast<unsigned long long *>(smem + C::Q_BYTES) + (size_t)team.id * words * 32;
@@ -478,7 +398,7 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
 
     // ---- scores of this CTA's pages: chunk it is pages from + 16 ((warp + 4 it) CS + rank) ..
     uint2 *qf = reinterpret_cast<uint2 *>(smem);
-    const uint32_t ring = ptx::smem_u32(smem + C::Q_BYTES) + warp * kSelBufs * C::BUF;
+    const uint32_t ring = ptx::smem_u32(smem + C::Q_BYTES) + warp * 2 * C::BUF;
     const int p0 = from + 16 * (warp * CS + rank), stride = 16 * kSelWarps * CS;
     const int chunks = to > p0 ? (to - p0 + stride - 1) / stride : 0;
     uint32_t kmax2[4] = {0, 0, 0, 0};
@@ -489,26 +409,29 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
         // lane i < 16 holds the i-th page of the chunk that is fetched next; eight consecutive lanes copy
         // 128 consecutive bytes
         auto id_of = [&](int it) { return lane < 16 && it < chunks && p0 + it * stride + lane < to ? bt[p0 + it * stride + lane] : -1; };
-        int id = id_of(0);
-        auto fetch = [&](int it, int buf) {
+        int id = id_of(0), id2 = id_of(1);
+        unsigned int live = 0;  // bit 16 b + i: page i of buffer b is there
+        auto fetch = [&](int it) {
+            const int buf = it & 1;
             const bool ok = id >= 0 && id < p.num_pages;
-            if (!ok && lane < 16 && p0 + it * stride + lane < to) atomicOr(p.status, kStatusBounds);
+            if (!ok && lane < 16 && it < chunks && p0 + it * stride + lane < to) atomicOr(p.status, kStatusBounds);
             const unsigned int m = __ballot_sync(0xffffffffu, ok);
             const long long off = ok ? id * p.b_s[0] : 0;
+            const uint32_t dst = ring + buf * C::BUF;
 #pragma unroll
             for (int u = 0; u < C::ROW / 32; ++u) {
                 const int x = 32 * u + lane, r = x / (C::ROW / 16), ch = x - r * (C::ROW / 16);
                 const uint8_t *src = bounds + __shfl_sync(0xffffffffu, off, r) + 16 * ch;
                 const bool there = m >> r & 1u;
-                cp_async16(ring + buf * C::BUF + r * C::PITCH + 16 * ch, there ? src : p.bounds, there ? 16 : 0);
+                cp_async16(dst + r * C::PITCH + 16 * ch, there ? src : p.bounds, there ? 16 : 0);
             }
-            id = id_of(it + 1);
-            return m;
+            live = buf ? (live & 0xFFFFu) | m << 16 : (live & 0xFFFF0000u) | m;
+            id = id2;
+            id2 = id_of(it + 2);
         };
-        unsigned int live[kSelBufs];
-#pragma unroll
-        for (int i = 0; i < kSelBufs; ++i) {
-            live[i] = i < chunks ? fetch(i, i) : 0;
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+            if (i < chunks) fetch(i);
             cp_async_commit();
         }
         // the query rows, while the first pages arrive; padding rows repeat a real one: the maximum
@@ -522,7 +445,7 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
             *reinterpret_cast<uint4 *>(qraw + 16 * x) = __ldg(reinterpret_cast<const uint4 *>(q + tk * p.q_s[1] + h * p.q_s[2] + 16 * ch));
         }
         __syncthreads();
-#pragma unroll 4
+#pragma unroll 2
         for (int x = tid; x < NT * C::STEPS * 32; x += kSelThreads) {
             const int ln = x & 31, st = (x >> 5) % C::STEPS, col = 8 * (x / (32 * C::STEPS)) + (ln >> 2);
             const int pos = 64 * (st >> 2) + 16 * (ln & 3) + 4 * (st & 3);
@@ -556,14 +479,11 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
                 if (TB == 1 || r / C::GP == t) l1[t] = fmaxf(l1[t], s);
         }
         __syncthreads();
-        for (int it0 = 0; it0 < chunks; it0 += kSelBufs)
-#pragma unroll
-        for (int bi = 0; bi < kSelBufs; ++bi) {
-            const int it = it0 + bi;
-            if (it >= chunks) break;
-            cp_async_wait<kSelBufs - 1>();
+#pragma unroll 1
+        for (int it = 0; it < chunks; ++it) {
+            cp_async_wait<1>();
             __syncwarp();
-            const uint32_t buf = ring + bi * C::BUF + (lane >> 2) * C::PITCH + 16 * (lane & 3);
+            const uint32_t buf = ring + (it & 1) * C::BUF + (lane >> 2) * C::PITCH + 16 * (lane & 3);
             float acc[NT][4], acc2[NT][4];  // two chains of dependent MMAs
 #pragma unroll
             for (int t = 0; t < NT; ++t)
@@ -593,9 +513,9 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[t][e] += acc2[t][e];
-            const unsigned int ok = live[bi];
+            const unsigned int ok = live >> (16 * (it & 1));
             __syncwarp();  // the buffer has been read
-            if (it + kSelBufs < chunks) live[bi] = fetch(it + kSelBufs, bi);
+            if (it + 2 < chunks) fetch(it + 2);
             cp_async_commit();
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -693,13 +613,13 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
     const float eps2 = 2.f * (C::STEPS + 1) * 0x1p-21f * a_l1 * a_k;
     float t_hi = INFINITY, t_lo = INFINITY;
     if (want > 0) {
-        const float t = team.kth_score(scores, from, last, want, list);
+        const float t = unorder_f32(team.kth_score(scores + from, last - from, want));
         t_hi = __fadd_ru(t, eps2);
         t_lo = __fsub_rd(t, eps2);
     }
     const int nw = (n + 31) >> 5, tw = team.t >> 5;
     int n_in = 0, n_amb = 0;  // the same in every lane of a warp
-#pragma unroll 4
+#pragma unroll 2
     for (int w = tw; w < nw; w += C::W) {
         const int pg = 32 * w + lane;
         const bool scored = pg >= from && pg < last;
@@ -719,6 +639,7 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
         }
     }
     if constexpr (C::W > 1) {
+        team.sync();  // the scratch words have been read
         if (lane == 0) {
             team.words[2 * tw] = (unsigned)n_in;
             team.words[2 * tw + 1] = (unsigned)n_amb;
@@ -740,13 +661,13 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
         // Many pages: one to a warp.  Few: every warp takes a part of each page's heads.
         const bool split = C::W > 1 && n_amb < 4 * C::W;
         const int hs = split ? tw * p.G / C::W : 0, he = split ? (tw + 1) * p.G / C::W : p.G;
-        if (split) {
-            team.each(nw, [&](int w) {
-                for (unsigned int bits = amb[w]; bits; bits &= bits - 1) keys[32 * w + __ffs(bits) - 1] = 0;
-            });
+        if (split || n_amb > kSelList) {
+            team.each(n, [&](int i) { keys[i] = 0; });
             team.sync();
         }
+#pragma unroll 1
         for (int w = split ? 0 : tw; w < nw; w += split ? 1 : C::W) {
+#pragma unroll 1
             for (unsigned int bits = amb[w]; bits; bits &= bits - 1) {
                 const int pg = 32 * w + __ffs(bits) - 1;
                 unsigned long long key = 0;
@@ -777,6 +698,7 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
                 const int pg = list[i];
                 const unsigned long long key = keys[pg];
                 int ahead = 0;
+#pragma unroll 2
                 for (int j = 0; j < n_amb; ++j) {
                     const int o = list[j];
                     ahead += keys[o] > key || (keys[o] == key && o < pg);
@@ -784,12 +706,10 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
                 if (ahead < places) atomicOr(&sel[pg >> 5], 1u << (pg & 31));
             });
         } else {
-            int left;
-            const unsigned long long t = team.kth_key(n, places, &left, [&](int j, unsigned long long *v) {
-                if (!(amb[j >> 5] >> (j & 31) & 1u)) return false;
-                *v = keys[j];
-                return true;
-            });
+            const unsigned long long t = team.kth_key(keys, n, places);
+            unsigned int c = 0;
+            team.each(n, [&](int i) { c += keys[i] > t; });
+            int left = places - (int)team.template reduce<false>(c);  // of the keys equal to t
             if (tw == 0) {  // ties at the threshold in index order
                 for (int w = 0; w < nw; ++w) {
                     const bool on = amb[w] >> lane & 1u;
