@@ -129,6 +129,9 @@ constexpr int kSelWarps = 4, kSelThreads = kSelWarps * 32;
 constexpr int kSelMaxTable = 16384;  // block_table columns
 constexpr int kSelMaxTable4 = 2048;  // of the kernel that takes four tokens at once
 constexpr int kSelMaxCluster = 8;
+#ifndef CF
+#define CF 4
+#endif
 constexpr int kSelList = 256;  // undecided pages that are ranked directly
 constexpr int kSelHeld = 16;   // scores that a thread keeps in registers while it chooses
 
@@ -618,7 +621,10 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
         t_lo = __fsub_rd(t, eps2);
     }
     const int nw = (n + 31) >> 5, tw = team.t >> 5;
-    int n_in = 0, n_amb = 0;  // the same in every lane of a warp
+    int n_in = 0;  // the same in every lane of a warp
+    unsigned int *n_list = team.words + 14;
+    if (team.t == 0) *n_list = 0;
+    team.sync();
 #pragma unroll 2
     for (int w = tw; w < nw; w += C::W) {
         const int pg = 32 * w + lane;
@@ -632,80 +638,67 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
         const unsigned int bs = __ballot_sync(0xffffffffu, in), bm = __ballot_sync(0xffffffffu, maybe);
         const unsigned int bf = __ballot_sync(0xffffffffu, pg < n && !scored);
         n_in += __popc(bs);
-        n_amb += __popc(bm);
+        if (maybe) {
+            const unsigned int at = atomicAdd(n_list, 1u);
+            if (at < kSelList) list[at] = pg;
+        }
         if (lane == 0) {
             sel[w] = bs | bf;
             amb[w] = bm;
         }
     }
     if constexpr (C::W > 1) {
-        team.sync();  // the scratch words have been read
-        if (lane == 0) {
-            team.words[2 * tw] = (unsigned)n_in;
-            team.words[2 * tw + 1] = (unsigned)n_amb;
-        }
+        if (lane == 0) team.words[tw] = (unsigned)n_in;
         team.sync();
-        n_in = n_amb = 0;
-        for (int w = 0; w < C::W; ++w) {
-            n_in += (int)team.words[2 * w];
-            n_amb += (int)team.words[2 * w + 1];
-        }
+        n_in = 0;
+#pragma unroll
+        for (int w = 0; w < C::W; ++w) n_in += (int)team.words[w];
     }
     team.sync();
+    const int n_amb = (int)*n_list;
     const int places = want - n_in;  // for the undecided pages
     if (n_amb == places) {
         team.each(nw, [&](int w) { sel[w] |= amb[w]; });
     } else if (places > 0 && n_amb > 0) {
         // Keys that order the undecided pages exactly.  All-zero queries or bounds leave exact zeros.
         const bool exact = !(eps2 > 0.f);
-        // Many pages: one to a warp.  Few: every warp takes a part of each page's heads.
-        const bool split = C::W > 1 && n_amb < 4 * C::W;
-        const int hs = split ? tw * p.G / C::W : 0, he = split ? (tw + 1) * p.G / C::W : p.G;
-        if (split || n_amb > kSelList) {
-            team.each(n, [&](int i) { keys[i] = 0; });
-            team.sync();
-        }
-#pragma unroll 1
-        for (int w = split ? 0 : tw; w < nw; w += split ? 1 : C::W) {
-#pragma unroll 1
-            for (unsigned int bits = amb[w]; bits; bits &= bits - 1) {
-                const int pg = 32 * w + __ffs(bits) - 1;
-                unsigned long long key = 0;
-                if (exact) {
-                    key = order_f32(scores[pg]);
-                } else if (hs < he) {
-                    const int id = bt[pg];
-                    if (id >= 0 && id < p.num_pages)
-                        key = exact_key<D>(bounds + (long long)id * p.b_s[0], q + (TB == 1 ? 0 : team.id) * p.q_s[1], p.q_s[2], hs, he, lane);
-                }
-                if (lane == 0) {
-                    if (split) atomicMax(&keys[pg], key);
-                    else keys[pg] = key;
-                }
-            }
-        }
-        team.sync();
+        auto key_of = [&](int pg, int hs, int he) {
+            if (exact) return (unsigned long long)order_f32(scores[pg]);
+            const int id = bt[pg];
+            if (id < 0 || id >= p.num_pages || hs >= he) return 0ull;
+            return exact_key<D>(bounds + (long long)id * p.b_s[0], q + (TB == 1 ? 0 : team.id) * p.q_s[1], p.q_s[2], hs, he, lane);
+        };
         if (n_amb <= kSelList) {
-            // by rank among the undecided
-            unsigned int *cnt = team.words + 14;
-            if (team.t == 0) *cnt = 0;
+            // by rank among the undecided; every warp scores a part of each page's heads
+            team.each(n_amb, [&](int i) { keys[i] = 0; });
             team.sync();
-            team.each(nw, [&](int w) {
-                for (unsigned int bits = amb[w]; bits; bits &= bits - 1) list[atomicAdd(cnt, 1u)] = 32 * w + __ffs(bits) - 1;
-            });
+#pragma unroll 1
+            for (int i = 0; i < n_amb; ++i) {
+                const unsigned long long key = key_of(list[i], tw * p.G / C::W, (tw + 1) * p.G / C::W);
+                if (lane == 0) atomicMax(&keys[i], key);
+            }
             team.sync();
             team.each(n_amb, [&](int i) {
                 const int pg = list[i];
-                const unsigned long long key = keys[pg];
+                const unsigned long long key = keys[i];
                 int ahead = 0;
 #pragma unroll 2
-                for (int j = 0; j < n_amb; ++j) {
-                    const int o = list[j];
-                    ahead += keys[o] > key || (keys[o] == key && o < pg);
-                }
+                for (int j = 0; j < n_amb; ++j) ahead += keys[j] > key || (keys[j] == key && list[j] < pg);
                 if (ahead < places) atomicOr(&sel[pg >> 5], 1u << (pg & 31));
             });
         } else {
+            // many (equal or nearly equal pages): a warp per page, then bisection over the keys
+            team.each(n, [&](int i) { keys[i] = 0; });
+            team.sync();
+#pragma unroll 1
+            for (int w = tw; w < nw; w += C::W)
+#pragma unroll 1
+                for (unsigned int bits = amb[w]; bits; bits &= bits - 1) {
+                    const int pg = 32 * w + __ffs(bits) - 1;
+                    const unsigned long long key = key_of(pg, 0, p.G);
+                    if (lane == 0) keys[pg] = key;
+                }
+            team.sync();
             const unsigned long long t = team.kth_key(keys, n, places);
             unsigned int c = 0;
             team.each(n, [&](int i) { c += keys[i] > t; });
@@ -906,7 +899,7 @@ fa8_status fa8_select_pages(const fa8_tensor *q, const fa8_tensor *bounds, fa8_t
                       p.tab.max_pages <= fa8::kSelMaxTable4;
     p.cluster = 1;
     if (!four)
-        while (p.cluster < fa8::kSelMaxCluster && rows * p.cluster * 2 <= 4LL * ds->sm_count && p.tab.max_pages >= 128 * p.cluster * 2)
+        while (p.cluster < fa8::kSelMaxCluster && rows * p.cluster * 2 <= (long long)CF * ds->sm_count && p.tab.max_pages >= 128 * p.cluster * 2)
             p.cluster *= 2;
     if (blocks * Hkv > 0x7fffffffLL) return fail(FA8_ERR_UNSUPPORTED, "problem too large for the grid");
     const unsigned grid = (unsigned)(four ? blocks * Hkv : rows);
