@@ -23,7 +23,7 @@ struct BoundsParams {
     long long b_s[2];  // page, head
     const int *cu_q;   // may be null
     int new_tokens;    // without cu_q; < 0: all
-    int D, chunks, npg, blocks_per_req, num_pages;
+    int D, chunks, groups, npg, blocks_per_req, num_pages;
     host::Table tab;
     unsigned int *status;
 };
@@ -41,74 +41,85 @@ __device__ __forceinline__ uint32_t hmax2_nan(uint32_t a, uint32_t b) {
     return d;
 }
 
-// A thread owns 16 channels of one kv-head of one page and walks the page's rows.  E4M3 -> f16 is
+// A warp takes 128 bytes (eight 16-channel pieces, a whole line of every row) of one page: lane l holds
+// piece l mod 8 of rows l / 8, l / 8 + 4, ..; then the four row parts meet by shuffles.  E4M3 -> f16 is
 // exact, so the packed f16 minimum and maximum (NaN-propagating) are, and so is the way back.
-// Bound: HBM, one read of the pages' K.
+// Bound: HBM, one read of the pages' K.  Measured, 2048 pages of 64 keys x 8 heads of 128 (137 MB): 26 us,
+// 5.2 TB/s, 0.77 of the copy rate (a thread per 16 channels walking all rows: 32 us); the one new page of
+// 64 requests: 3.0 us (4.6).
 __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const __grid_constant__ BoundsParams p) {
     const int b = blockIdx.x / p.blocks_per_req;
-    const int item = (blockIdx.x - b * p.blocks_per_req) * kBoundsThreads + threadIdx.x;
-    const int slot = item / p.chunks;
+    const int lane = threadIdx.x & 31;
+    const int item = (blockIdx.x - b * p.blocks_per_req) * (kBoundsThreads / 32) + (threadIdx.x >> 5);
+    const int slot = item / p.groups;
     if (slot >= p.npg) return;
     const int ps = p.tab.page_size;
-    const int Lk = p.tab.cu_k[b + 1] - p.tab.cu_k[b];
+    // the chain is lengths -> page -> rows; with all pages asked for, the page does not wait for the lengths
+    const int *bt = p.tab.bt + (long long)b * p.tab.bt_stride;
+    const bool all = !p.cu_q && p.new_tokens < 0;
+    int page = all ? __ldg(bt + slot) : -1;
+    const int Lk = __ldg(p.tab.cu_k + b + 1) - __ldg(p.tab.cu_k + b);
     if (Lk < 0 || (long long)Lk > (long long)p.tab.max_pages * ps) {
-        atomicOr(p.status, kStatusBounds);
+        if (lane == 0) atomicOr(p.status, kStatusBounds);
         return;
     }
-    int first = 0;
-    const int m = p.cu_q ? p.cu_q[b + 1] - p.cu_q[b] : p.new_tokens;
-    if (m >= 0) {
-        if (m == 0) return;
-        first = max(0, Lk - m) / ps;
+    int pi = slot;
+    if (!all) {
+        const int m = p.cu_q ? p.cu_q[b + 1] - p.cu_q[b] : p.new_tokens;
+        if (m <= 0) return;
+        pi += max(0, Lk - m) / ps;
     }
-    const int pi = first + slot;
     if ((long long)pi * ps >= Lk) return;
-    const int page = p.tab.bt[(long long)b * p.tab.bt_stride + pi];
+    if (!all) page = bt[pi];
     if (page < 0 || page >= p.num_pages) {
-        atomicOr(p.status, kStatusBounds);
+        if (lane == 0) atomicOr(p.status, kStatusBounds);
         return;
     }
-    const int chunk = item - slot * p.chunks;
-    const int per = p.D >> 4, h = chunk / per, c = chunk - h * per;
-    const int rows = min(ps, Lk - pi * ps);
+    const int rows = min(ps, Lk - pi * ps), part = lane >> 3;
+    const int chunk = (item - slot * p.groups) * 8 + (lane & 7);
+    const bool on = chunk < p.chunks;
+    const int per = p.D >> 4, h = on ? chunk / per : 0, c = on ? chunk - h * per : 0;
     const uint8_t *src = p.k + (long long)page * p.k_s[0] + (long long)h * p.k_s[2] + 16 * c;
     uint32_t lo[8], hi[8];
-    {
+    {  // every part starts from row 0: a part may have no row of its own
         const Bytes<16> v = ld_stream<16>(src);
 #pragma unroll
         for (int i = 0; i < 4; ++i) e4m3x4_to_h2(v.w[i], lo[2 * i], lo[2 * i + 1]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) hi[i] = lo[i];
     }
-    auto take = [&](const Bytes<16> &v) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t a, d;
-            e4m3x4_to_h2(v.w[i], a, d);
-            lo[2 * i] = hmin2_nan(lo[2 * i], a);
-            hi[2 * i] = hmax2_nan(hi[2 * i], a);
-            lo[2 * i + 1] = hmin2_nan(lo[2 * i + 1], d);
-            hi[2 * i + 1] = hmax2_nan(hi[2 * i + 1], d);
-        }
-    };
-    int r = 1;
-    for (; r + 8 <= rows; r += 8) {  // eight loads in flight
+    for (int r = part; r < rows; r += 32) {  // eight loads in flight
         Bytes<16> v[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) v[u] = ld_stream<16>(src + (long long)(r + u) * p.k_s[1]);
+        for (int u = 0; u < 8; ++u) v[u] = ld_stream<16>(src + (long long)min(r + 4 * u, rows - 1) * p.k_s[1]);
 #pragma unroll
-        for (int u = 0; u < 8; ++u) take(v[u]);
-    }
-    for (; r < rows; ++r) take(ld_stream<16>(src + (long long)r * p.k_s[1]));
-    uint32_t wl[4], wh[4];
+        for (int u = 0; u < 8; ++u) {
+            if (r + 4 * u >= rows) break;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        wl[i] = ptx::prmt_lo16(ptx::cvt_e4m3x2_h2(lo[2 * i]), ptx::cvt_e4m3x2_h2(lo[2 * i + 1]));
-        wh[i] = ptx::prmt_lo16(ptx::cvt_e4m3x2_h2(hi[2 * i]), ptx::cvt_e4m3x2_h2(hi[2 * i + 1]));
+            for (int i = 0; i < 4; ++i) {
+                uint32_t a, d;
+                e4m3x4_to_h2(v[u].w[i], a, d);
+                lo[2 * i] = hmin2_nan(lo[2 * i], a);
+                hi[2 * i] = hmax2_nan(hi[2 * i], a);
+                lo[2 * i + 1] = hmin2_nan(lo[2 * i + 1], d);
+                hi[2 * i + 1] = hmax2_nan(hi[2 * i + 1], d);
+            }
+        }
     }
-    uint8_t *dst = p.bounds + (long long)page * p.b_s[0] + (long long)h * p.b_s[1] + 16 * c;
-    *reinterpret_cast<uint4 *>(dst) = make_uint4(wl[0], wl[1], wl[2], wl[3]);
-    *reinterpret_cast<uint4 *>(dst + p.D) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int o = 8; o < 32; o <<= 1) {
+            lo[i] = hmin2_nan(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o));
+            hi[i] = hmax2_nan(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o));
+        }
+    if (part > 1 || !on) return;
+    uint32_t w[4];  // part 0 writes the minima, part 1 the maxima
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] = ptx::prmt_lo16(ptx::cvt_e4m3x2_h2(part ? hi[2 * i] : lo[2 * i]), ptx::cvt_e4m3x2_h2(part ? hi[2 * i + 1] : lo[2 * i + 1]));
+    uint8_t *dst = p.bounds + (long long)page * p.b_s[0] + (long long)h * p.b_s[1] + 16 * c + part * p.D;
+    *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // ------------------------------------------------------------------------------ page selection
@@ -129,9 +140,6 @@ constexpr int kSelWarps = 4, kSelThreads = kSelWarps * 32;
 constexpr int kSelMaxTable = 16384;  // block_table columns
 constexpr int kSelMaxTable4 = 2048;  // of the kernel that takes four tokens at once
 constexpr int kSelMaxCluster = 8;
-#ifndef CF
-#define CF 4
-#endif
 constexpr int kSelList = 256;  // undecided pages that are ranked directly
 constexpr int kSelHeld = 16;   // scores that a thread keeps in registers while it chooses
 
@@ -146,7 +154,10 @@ struct SelCfg {
     static constexpr int NV = ROW / 64;      // 16-byte vectors of a row per lane
     static constexpr int STEPS = ROW / 16;   // MMA k-steps
     static constexpr int BUF = 16 * PITCH;   // 16 pages
-    static constexpr int RING = kSelWarps * 2 * BUF;
+    // chunks in a warp's ring: one where four tokens share a pass (more CTAs per SM hide the copies: 49.7
+    // against 55 us for 512 tokens of 512 pages), two else (56 against 58 us for the ragged batch)
+    static constexpr int NBUF = TB == 1 ? 2 : 1;
+    static constexpr int RING = kSelWarps * NBUF * BUF;
     static constexpr int QR = TB == 1 ? 8 * NT : TB * GP;  // query rows of one pass
     static constexpr int Q_BYTES = NT * STEPS * 32 * 8 + QR * D;  // as MMA fragments, and as they are
     static constexpr int W = kSelWarps / TB;  // warps that choose for a token
@@ -315,7 +326,7 @@ __device__ __forceinline__ unsigned long long exact_key(const uint8_t *src, cons
 
 // Every CTA scores its pages with f16 MMAs (pages on M, query rows on N; the contraction runs over
 // [lo | hi] against [min(q,0) | max(q,0)], which is sum_c max(q_c lo_c, q_c hi_c)); a page's 2 D bytes
-// arrive by asynchronous copies, 16 pages a buffer, two buffers a warp.  With few rows a cluster of CTAs
+// arrive by asynchronous copies, 16 pages a buffer.  With few rows a cluster of CTAs
 // shares a token's pages and rank 0 chooses.
 //
 // Exact choice from fp32 scores: E4M3 products are exact, an MMA adds 16 of them to the running
@@ -401,7 +412,7 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
 
     // ---- scores of this CTA's pages: chunk it is pages from + 16 ((warp + 4 it) CS + rank) ..
     uint2 *qf = reinterpret_cast<uint2 *>(smem);
-    const uint32_t ring = ptx::smem_u32(smem + C::Q_BYTES) + warp * 2 * C::BUF;
+    const uint32_t ring = ptx::smem_u32(smem + C::Q_BYTES) + warp * C::NBUF * C::BUF;
     const int p0 = from + 16 * (warp * CS + rank), stride = 16 * kSelWarps * CS;
     const int chunks = to > p0 ? (to - p0 + stride - 1) / stride : 0;
     uint32_t kmax2[4] = {0, 0, 0, 0};
@@ -414,26 +425,28 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
         auto id_of = [&](int it) { return lane < 16 && it < chunks && p0 + it * stride + lane < to ? bt[p0 + it * stride + lane] : -1; };
         int id = id_of(0), id2 = id_of(1);
         unsigned int live = 0;  // bit 16 b + i: page i of buffer b is there
+        constexpr int RP = C::ROW / 16;  // 16-byte pieces of a row
         auto fetch = [&](int it) {
-            const int buf = it & 1;
+            const int buf = C::NBUF == 1 ? 0 : it & 1;
             const bool ok = id >= 0 && id < p.num_pages;
-            if (!ok && lane < 16 && it < chunks && p0 + it * stride + lane < to) atomicOr(p.status, kStatusBounds);
+            if (!ok && lane < 16 && p0 + it * stride + lane < to) atomicOr(p.status, kStatusBounds);
             const unsigned int m = __ballot_sync(0xffffffffu, ok);
             const long long off = ok ? id * p.b_s[0] : 0;
-            const uint32_t dst = ring + buf * C::BUF;
 #pragma unroll
-            for (int u = 0; u < C::ROW / 32; ++u) {
-                const int x = 32 * u + lane, r = x / (C::ROW / 16), ch = x - r * (C::ROW / 16);
-                const uint8_t *src = bounds + __shfl_sync(0xffffffffu, off, r) + 16 * ch;
-                const bool there = m >> r & 1u;
-                cp_async16(dst + r * C::PITCH + 16 * ch, there ? src : p.bounds, there ? 16 : 0);
+            for (int u = 0; u < RP / 2; ++u) {
+                const int r = 32 % RP == 0 ? (32 / RP) * u + lane / RP : (32 * u + lane) / RP;
+                const int ch = 32 % RP == 0 ? lane % RP : (32 * u + lane) % RP;
+                const uint8_t *src = bounds + 16 * ch + __shfl_sync(0xffffffffu, off, r);
+                const uint32_t dst = ring + buf * C::BUF + r * C::PITCH + 16 * ch;
+                if (m == 0xFFFFu) cp_async16(dst, src, 16);
+                else cp_async16(dst, m >> r & 1u ? src : p.bounds, m >> r & 1u ? 16 : 0);
             }
             live = buf ? (live & 0xFFFFu) | m << 16 : (live & 0xFFFF0000u) | m;
             id = id2;
             id2 = id_of(it + 2);
         };
 #pragma unroll 1
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < C::NBUF; ++i) {
             if (i < chunks) fetch(i);
             cp_async_commit();
         }
@@ -484,9 +497,9 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
         __syncthreads();
 #pragma unroll 1
         for (int it = 0; it < chunks; ++it) {
-            cp_async_wait<1>();
+            cp_async_wait<C::NBUF - 1>();
             __syncwarp();
-            const uint32_t buf = ring + (it & 1) * C::BUF + (lane >> 2) * C::PITCH + 16 * (lane & 3);
+            const uint32_t buf = ring + (C::NBUF == 1 ? 0 : it & 1) * C::BUF + (lane >> 2) * C::PITCH + 16 * (lane & 3);
             float acc[NT][4], acc2[NT][4];  // two chains of dependent MMAs
 #pragma unroll
             for (int t = 0; t < NT; ++t)
@@ -516,9 +529,9 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[t][e] += acc2[t][e];
-            const unsigned int ok = live >> (16 * (it & 1));
+            const unsigned int ok = C::NBUF == 1 ? live : live >> (16 * (it & 1));
             __syncwarp();  // the buffer has been read
-            if (it + 2 < chunks) fetch(it + 2);
+            if (it + C::NBUF < chunks) fetch(it + C::NBUF);
             cp_async_commit();
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -829,9 +842,10 @@ fa8_status fa8_page_bounds(const fa8_tensor *k, fa8_tensor *bounds, const fa8_te
         if (new_tokens == 0) return FA8_SUCCESS;
         p.npg = (int)std::min<long long>(p.npg, ((long long)new_tokens - 1 + page_size - 1) / page_size + 1);
     }
-    const long long items = (long long)p.npg * p.chunks;
-    const long long per_req = (items + fa8::kBoundsThreads - 1) / fa8::kBoundsThreads;
-    if (items > 0x7fffffffLL - fa8::kBoundsThreads || per_req * B > 0x7fffffffLL)
+    p.groups = (p.chunks + 7) / 8;
+    const long long items = (long long)p.npg * p.groups, warps = fa8::kBoundsThreads / 32;
+    const long long per_req = (items + warps - 1) / warps;
+    if (items > 0x7fffffffLL - warps || per_req * B > 0x7fffffffLL)
         return fail(FA8_ERR_UNSUPPORTED, "problem too large for the grid");
     p.blocks_per_req = (int)per_req;
     DeviceState *ds = nullptr;
@@ -893,13 +907,14 @@ fa8_status fa8_select_pages(const fa8_tensor *q, const fa8_tensor *bounds, fa8_t
     p.status = ds->status;
     // Several tokens per request and enough of them to fill the GPU in blocks of four: one pass over
     // the bounds serves four tokens.  Else a token at a time, and where there are few (token, kv-head)
-    // pairs a cluster of CTAs shares each pair's pages, 128 or more a CTA.
+    // pairs a cluster of CTAs shares each pair's pages, 128 or more a CTA, up to four CTAs per SM in all
+    // (512 pairs: 51 us without clusters, 53 with two CTAs each, 58 with four).
     const long long blocks = p.cu_q ? (long long)qs.T / 4 + qs.B : (long long)qs.B * ((qs.Sq + 3) / 4);
     const bool four = p.G <= 8 && (long long)qs.T >= 4LL * qs.B && blocks * Hkv >= 2LL * ds->sm_count &&
                       p.tab.max_pages <= fa8::kSelMaxTable4;
     p.cluster = 1;
     if (!four)
-        while (p.cluster < fa8::kSelMaxCluster && rows * p.cluster * 2 <= (long long)CF * ds->sm_count && p.tab.max_pages >= 128 * p.cluster * 2)
+        while (p.cluster < fa8::kSelMaxCluster && rows * p.cluster * 2 <= 4LL * ds->sm_count && p.tab.max_pages >= 128 * p.cluster * 2)
             p.cluster *= 2;
     if (blocks * Hkv > 0x7fffffffLL) return fail(FA8_ERR_UNSUPPORTED, "problem too large for the grid");
     const unsigned grid = (unsigned)(four ? blocks * Hkv : rows);
