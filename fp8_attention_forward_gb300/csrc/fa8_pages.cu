@@ -88,23 +88,24 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const __gri
 #pragma unroll
         for (int i = 0; i < 8; ++i) hi[i] = lo[i];
     }
+    auto take = [&](const Bytes<16> &v) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t a, d;
+            e4m3x4_to_h2(v.w[i], a, d);
+            lo[2 * i] = hmin2_nan(lo[2 * i], a);
+            hi[2 * i] = hmax2_nan(hi[2 * i], a);
+            lo[2 * i + 1] = hmin2_nan(lo[2 * i + 1], d);
+            hi[2 * i + 1] = hmax2_nan(hi[2 * i + 1], d);
+        }
+    };
     for (int r = part; r < rows; r += 32) {  // eight loads in flight
         Bytes<16> v[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u) v[u] = ld_stream<16>(src + (long long)min(r + 4 * u, rows - 1) * p.k_s[1]);
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            if (r + 4 * u >= rows) break;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t a, d;
-                e4m3x4_to_h2(v[u].w[i], a, d);
-                lo[2 * i] = hmin2_nan(lo[2 * i], a);
-                hi[2 * i] = hmax2_nan(hi[2 * i], a);
-                lo[2 * i + 1] = hmin2_nan(lo[2 * i + 1], d);
-                hi[2 * i + 1] = hmax2_nan(hi[2 * i + 1], d);
-            }
-        }
+        for (int u = 0; u < 8; ++u)
+            if (r + 4 * u < rows) take(v[u]);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
