@@ -11,12 +11,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libfa8.so")
+ARGS = os.path.join(BUILD, "fa8_args.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -51,12 +53,33 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(f) <= t for f in _sources() + _headers() + [__file__])
 
 
+def build_args():
+    """Compiles csrc/fa8_args.c, the CPython module that packs tensor views (needs Python's headers:
+    without them the binding packs the views itself)."""
+    src = os.path.join(CSRC, "fa8_args.c")
+    inc = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(inc, "Python.h")):
+        return None
+    deps = [src, os.path.join(ROOT, "include", "fa8.h"), __file__]
+    if os.path.exists(ARGS) and all(os.path.getmtime(f) <= os.path.getmtime(ARGS) for f in deps):
+        return ARGS
+    os.makedirs(BUILD, exist_ok=True)
+    tmp = ARGS + f".tmp{os.getpid()}"
+    r = subprocess.run(["gcc", "-O2", "-Wall", "-fPIC", "-shared", "-fvisibility=hidden", "-I", inc, "-I",
+                        os.path.join(ROOT, "include"), src, "-o", tmp], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("gcc failed on fa8_args.c:\n" + r.stdout + r.stderr)
+    os.replace(tmp, ARGS)
+    return ARGS
+
+
 def build(force: bool = False, ptxas_verbose: bool = False, jobs: int | None = None,
           out_dir: str | None = None, defines=(), src_dir: str | None = None) -> str:
     """Compiles csrc/*.cu and links libfa8.so into ``out_dir`` (default: the in-tree
     _build/); ``defines`` are extra -D macros (e.g. FA8_TRACE for the pipeline trace);
     ``src_dir`` compiles another copy of the sources instead of csrc/."""
     build_dir = out_dir or BUILD
+    build_args()
     lib = os.path.join(build_dir, "libfa8.so")
     if not force and not ptxas_verbose and not defines and out_dir is None and src_dir is None and up_to_date():
         return LIB

@@ -243,46 +243,91 @@ def rope_inv_freq(rotary_dim, base=10000.0, *, scaling="none", factor=1.0, origi
 _ARG = [struct.Struct("Qii%dq%dx%dq%dx" % (n, 32 - 8 * n, n, 32 - 8 * n)) for n in range(5)]  # fa8_tensor of n dims
 _ARGS = ctypes.c_char * (ctypes.sizeof(Fa8Tensor) * 16)
 _SCALARS = (type(None), int, float)
-_direct = {}
+
+
+def _packed(name):
+    """The entry point as a function of tensors and numbers, the views packed into one buffer here."""
+    res, types = SIGNATURES[name]
+    fn = lib()[name]
+    fn.restype, fn.argtypes = res, [ctypes.c_void_p if t is _P else t for t in types]
+
+    def call(*args):
+        buf = _ARGS()
+        at = start = ctypes.addressof(buf)
+        passed = []
+        for a in args[:-1]:
+            if type(a) in _SCALARS:
+                if type(a) is int and not -(1 << 31) <= a < 1 << 31:
+                    raise OverflowError("argument does not fit 32 bits")
+                passed.append(a)
+                continue
+            shape = a.shape
+            n = len(shape)
+            if a.dtype not in _DTYPES:
+                raise TypeError(f"unsupported dtype {a.dtype}")
+            if n > 4:
+                raise ValueError("at most 4 dims")
+            _ARG[n].pack_into(buf, at - start, a.data_ptr(), _DTYPES[a.dtype], n, *shape, *a.stride())
+            passed.append(at)
+            at += 80
+        return fn(*passed, args[-1])
+
+    return call
+
+
+def _args_module():
+    """The CPython module that packs the views in C, or None where it was not built."""
+    from importlib.machinery import ExtensionFileLoader
+    from importlib.util import module_from_spec, spec_from_file_location
+
+    path = os.path.join(_HERE, "_build", "fa8_args.so")
+    if not os.path.exists(path):
+        return None
+    module = module_from_spec(spec_from_file_location("fa8_args", path, loader=ExtensionFileLoader("fa8_args", path)))
+    module.set_dtypes(list(_DTYPES.items()))
+    return module
+
+
+_entries = {}
+
+
+def _entry(name):
+    fn = _entries.get(name)
+    if fn is None:
+        module = _args_module()
+        if module is None:
+            fn = _packed(name)
+        else:
+            import functools
+
+            fn = functools.partial(getattr(module, name), ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value)
+        _entries[name] = fn
+    return fn
 
 
 def _call(name, device, stream, *args):
-    """One library call on ``device``; tensors are passed as views, the stream goes last.  The
-    views are packed into one buffer: a decode step's calls are short, and building a ctypes
-    structure per tensor took longer than the kernels."""
-    fn = _direct.get(name)
-    if fn is None:
-        res, types = SIGNATURES[name]
-        fn = lib()[name]
-        fn.restype, fn.argtypes = res, [ctypes.c_void_p if t is _P else t for t in types]
-        _direct[name] = fn
-    buf = _ARGS()
-    at = start = ctypes.addressof(buf)
-    passed = []
-    for a in args:
-        if type(a) in _SCALARS:
-            passed.append(a)
-            continue
-        shape = a.shape
-        n = len(shape)
-        if a.dtype not in _DTYPES:
-            raise TypeError(f"unsupported dtype {a.dtype}")
-        if n > 4:
-            raise ValueError("at most 4 dims")
-        _ARG[n].pack_into(buf, at - start, a.data_ptr(), _DTYPES[a.dtype], n, *shape, *a.stride())
-        passed.append(at)
-        at += 80
+    """One library call on ``device``; tensors are passed as views, the stream goes last."""
+    fn = _entry(name)
     if device.type != "cuda":
-        status = fn(*passed, None)
+        status = fn(*args, 0)
     else:
-        handle = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
-        if torch.cuda.current_device() == device.index:
-            status = fn(*passed, handle)
+        index = device.index
+        handle = _raw_stream(index) if stream is None else stream.cuda_stream
+        if _current_device() == index:
+            status = fn(*args, handle)
         else:
             with torch.cuda.device(device):
-                status = fn(*passed, handle)
+                status = fn(*args, handle)
     if status:
         _raise(status)
+
+
+def _raw_stream(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)  # no Stream object per call
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def rope_append(q, k, v, inv_freq, *, k_out, v_out, q_out=None, positions=None, interleaved=False,

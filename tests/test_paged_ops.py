@@ -227,3 +227,40 @@ def test_rotation_keeps_lengths_and_relative_angles():
         at = lambda n: ref.rope(x, torch.tensor([n]), w, inter, 0, 1.0).flatten()
         assert abs(float(at(5).norm() / x.norm()) - 1) < 1e-12
         assert abs(float(at(5) @ at(9) - at(100) @ at(104))) < 1e-9
+
+
+# ------------------------------------------------------------------ the binding's two ways to pass views
+@pytest.fixture(params=["c", "python"])
+def entries(request, monkeypatch):
+    """The views packed by the CPython module, and by the binding itself."""
+    monkeypatch.setattr(fa8, "_entries", {})
+    if request.param == "python":
+        monkeypatch.setattr(fa8, "_args_module", lambda: None)
+    elif fa8._args_module() is None:
+        pytest.skip("Python's headers are missing here")
+
+
+def test_views_reach_the_library(entries):
+    assert status(fa8_fwd, FWD, {}) == CUDA
+    assert status(fa8_rope, ROPE, dict(rotary_offset=4)) == UNSUPPORTED
+    assert "rotary_offset" in fa8.lib().fa8_last_error().decode()
+    assert status(fa8_select, SELECT, dict(pages=i32(2, 3, 4, 2).transpose(2, 3))) == BAD
+    assert "contiguous" in fa8.lib().fa8_last_error().decode()
+    assert status(fa8_bounds, BOUNDS, dict(bounds=e8(9, 3, 2, 128))) == BAD
+    assert "Hkv=2, 2, D=128" in fa8.lib().fa8_last_error().decode()
+    # strides of more than 32 bits, zero-d tensors
+    far = torch.empty_strided((2, 2, 8, 128), (0, 2 ** 33 + 8, 128, 1), dtype=torch.bfloat16, device="meta")
+    with pytest.raises((fa8.Fa8Error, RuntimeError)):
+        fa8_rope(far, **{k: v for k, v in ROPE.items() if k != "q"})
+    assert status(fa8_fwd, FWD, dict(descale_q=torch.tensor(1.0))) == CUDA
+
+
+def test_views_refuse_what_is_no_tensor(entries):
+    with pytest.raises(TypeError, match="dtype"):
+        status(fa8_bounds, BOUNDS, dict(cu_seqlens_k=torch.zeros(3, dtype=torch.int64)))
+    with pytest.raises(ValueError, match="4 dims"):
+        status(fa8_bounds, BOUNDS, dict(bounds=e8(1, 9, 2, 2, 128)))
+    with pytest.raises((TypeError, AttributeError)):
+        status(fa8_bounds, BOUNDS, dict(cu_seqlens_k="cu"))
+    with pytest.raises(OverflowError):
+        fa8._entry("fa8_page_bounds")(BOUNDS["k"], BOUNDS["bounds"], None, None, None, 2 ** 70, 0, 0)
