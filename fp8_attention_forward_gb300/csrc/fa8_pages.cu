@@ -331,9 +331,10 @@ __device__ __forceinline__ unsigned long long exact_key(const uint8_t *src, cons
 // shares a token's pages and rank 0 chooses.
 //
 // Exact choice from fp32 scores: E4M3 products are exact, an MMA adds 16 of them to the running
-// sum, and what it drops is below 2^-22 of the largest magnitude passing through, itself at most
-// A = max_h |q_h|_1 * max|bound|.  So a score is off by at most eps = (2 D / 16 + 1) 2^-21 A: the MMA
-// steps and the sum of their two chains, with a factor two to spare.  With t the k-th largest fp32 score, pages above t + 2 eps
+// sum, and what it drops is below 2^-23 of the largest magnitude passing through (fp32's 24 bits; a
+// probe over five kinds of data finds a quarter of that at most), itself at most
+// A = max_h |q_h|_1 * max|bound|.  So a score is off by at most eps = (2 D / 16 + 1) 2^-23 A: the MMA
+// steps and the sum of their two chains.  With t the k-th largest fp32 score, pages above t + 2 eps
 // are in and pages below t - 2 eps out whatever the true scores; the few between are scored again
 // in 64-bit integers (E4M3 is a whole number of 2^-9) and ranked by (score, lower index).
 template <int D, int NT, int TB>
@@ -376,7 +377,7 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
         i0 = blk * TB;
         tok0 += i0;
         ntok = min(TB, Lq - i0);
-        if (ntok <= 0 || tok0 < 0 || (long long)tok0 + ntok > p.T) return;
+        if (blk < 0 || ntok <= 0 || tok0 < 0 || (long long)tok0 + ntok > p.T) return;
     }
     const int Lk = p.tab.cu_k[b + 1] - p.tab.cu_k[b];
     bool bad = Lk < 0 || (long long)Lk > (long long)p.tab.max_pages * ps;
@@ -627,7 +628,7 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
         a_k = fmaxf(a_k, s_kw[w]);
     }
     for (int r = 0; CS > 1 && r < CS; ++r) a_k = fmaxf(a_k, s_kmax[r]);
-    const float eps2 = 2.f * (C::STEPS + 1) * 0x1p-21f * a_l1 * a_k;
+    const float eps2 = 2.f * (C::STEPS + 1) * 0x1p-23f * a_l1 * a_k;
     float t_hi = INFINITY, t_lo = INFINITY;
     if (want > 0) {
         const float t = unorder_f32(team.kth_score(scores + from, last - from, want));

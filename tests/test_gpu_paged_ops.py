@@ -154,6 +154,38 @@ def test_select_pages_ties_and_close_scores(kind, K, four):
         assert torch.equal(run_select(p, b8, K)[0, 0], want)
 
 
+def test_select_pages_widest_table():
+    """16384 columns, most of them used: more scores than a CTA's threads hold in registers."""
+    p = Problem([8 * 15001 - 3], [1], Hq=4, Hkv=1, D=64, DV=64, ps=8, width=16384, seed=40)
+    b = e4m3(torch.randn((p.k.shape[0], 1, 2, 64), generator=p.g))
+    for K in (1, 500, 4096):
+        got = run_select(p, b, K, keep_first=0, keep_last=1)
+        q, lo, hi = val(p.q)[0, 0], val(b)[p.bt[0, :15001].long(), 0, 0], val(b)[p.bt[0, :15001].long(), 0, 1]
+        s = (q.clamp_max(0) @ lo.T + q.clamp_min(0) @ hi.T).amax(0)
+        s[-1] = math.inf
+        want = s.sort(descending=True, stable=True).indices[:K].sort().values
+        assert torch.equal(got[0, 0, 0].long(), want)
+
+
+@pytest.mark.parametrize("Hkv", [2, 40])
+def test_packed_rows_ahead_of_the_first_sequence_stay(Hkv):
+    """cu_seqlens_q that begins past row 0, one token at a time and in blocks of four."""
+    p = Problem([90, 200], [33, 70], Hq=Hkv, Hkv=Hkv, D=64, DV=64, ps=8, packed=True, tail=6, seed=41)
+    shift = 5
+    bnd = e4m3(ref.bounds(p))
+    q = torch.roll(p.q.view(torch.uint8), shift, 0).view(E4M3).cuda()
+    kw = dict(p.index_args(), cu_seqlens_q=(p.cu_q + shift).cuda())
+    lists = torch.full((p.T + p.tail, Hkv, 4), -7, dtype=torch.int32, device="cuda")
+    fa8.select_pages(q, bnd.cuda(), 4, pages=lists, **kw)
+    out = torch.full((p.T + p.tail, Hkv, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((Hkv, p.T + p.tail), 7.0, device="cuda")
+    fa8.fwd_pages(q, p.k.cuda(), p.v.cuda(), lists, out=out, lse=lse, **kw)
+    ok()
+    assert torch.equal(lists[shift:shift + p.T].cpu(), ref.select(p, bnd, 4))
+    for x, keep in ((lists, -7), (out, 7.0), (lse.T, 7.0)):
+        assert (x[:shift] == keep).all() and (x[shift + p.T:] == keep).all() and (x[shift:shift + p.T] != keep).any()
+
+
 def test_select_pages_strided():
     p = Problem([800, 300], [2, 2], Hq=8, Hkv=2, D=64, DV=64, ps=16, seed=6)
     bnd = e4m3(ref.bounds(p))
@@ -241,7 +273,9 @@ ATTEND = [
     dict(keys=[900], new=[1], K=40, Hq=12, Hkv=1, ps=8, descales=False),
     dict(keys=[1200], new=[1], K=64, Hq=8, Hkv=1, ps=16),                 # two CTAs a cluster
     dict(keys=[3000], new=[1], K=256, Hq=8, Hkv=1, ps=8, sink=True),      # four
-    dict(keys=[5000], new=[1], K=300, Hq=16, Hkv=1, ps=16),               # eight
+    dict(keys=[5000], new=[1], K=300, Hq=16, Hkv=1, ps=16),               # eight, of eight warps
+    dict(keys=[5000], new=[2], K=200, Hq=24, Hkv=3, ps=24, D=256, DV=256),
+    dict(keys=[4200], new=[1], K=520, Hq=6, Hkv=2, ps=8, D=96, DV=96),
     dict(keys=[9000], new=[1], K=2, Hq=4, Hkv=1, ps=4096, D=64, DV=64),   # the largest page
     dict(keys=[300], new=[3], K=0),                                        # an empty list
     dict(keys=[400], new=[1], K=20, scale=2.5),                           # sharp softmax
