@@ -11,8 +11,9 @@
 // Bound: HBM, 2 bytes read and 1 written per element; next, the instructions per element.  A thread
 // keeps the same 16 dims of a head over the heads of one token, so its 8 pairs of sines serve all of
 // them, arithmetic goes two values an instruction, and no barrier follows the loads.  Measured, 8192
-// tokens of 32 + 2 x 8 heads of 128 dims (151 MB): 31 us, 4.85 TB/s; sines through shared memory, four
-// tokens a CTA: 57 us; sincospif per pair and heads by select: 46 us; one decode token: 3.2 us.
+// tokens of 32 + 2 x 8 heads of 128 dims (151 MB): 28 us, 5.4 TB/s, 0.79 of the copy rate; sines through
+// shared memory, four tokens a CTA: 57 us; sincospif per pair and heads by select: 46 us; one decode
+// token: 3.0 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -125,9 +126,11 @@ __device__ __forceinline__ uint32_t round4(uint64_t a, uint64_t b) {
     return ptx::prmt_lo16(ptx::cvt_e4m3x2(a1, a0), ptx::cvt_e4m3x2(b1, b0));
 }
 
-// Rotates (ROT), scales and rounds one thread's 16 dims: two groups of 8, `gap` apart.
+// Rotates (ROT: where `on`), scales and rounds one thread's 16 dims: two groups of 8, `gap` apart.  A warp
+// holds rotated dims and others, so both go through the rotation and the others drop it: exactly, also
+// beside an infinity.
 template <typename T, bool INTER, bool ROT>
-__device__ __forceinline__ void rope_store(uint8_t *dst, int gap, const uint4 &ra, const uint4 &rb, float inv,
+__device__ __forceinline__ void rope_store(uint8_t *dst, int gap, const uint4 &ra, const uint4 &rb, float inv, bool on,
                                            const uint64_t (&cc)[INTER ? 8 : 4], const uint64_t (&ss)[INTER ? 8 : 4],
                                            const uint64_t (&ns)[INTER ? 1 : 4]) {
     const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
@@ -140,13 +143,16 @@ __device__ __forceinline__ void rope_store(uint8_t *dst, int gap, const uint4 &r
         if constexpr (ROT && INTER) {  // (x0, x1) {c, c} + (x1, x0) {-s, s}
             float x0, x1;
             ptx::f2unpack(a[e], x0, x1);
-            a[e] = ptx::ffma2(a[e], cc[e], fmul2(ptx::f2pack(x1, x0), ss[e]));
+            const uint64_t y = ptx::ffma2(a[e], cc[e], fmul2(ptx::f2pack(x1, x0), ss[e]));
+            a[e] = on ? y : a[e];
             ptx::f2unpack(c[e], x0, x1);
-            c[e] = ptx::ffma2(c[e], cc[4 + e], fmul2(ptx::f2pack(x1, x0), ss[4 + e]));
+            const uint64_t z = ptx::ffma2(c[e], cc[4 + e], fmul2(ptx::f2pack(x1, x0), ss[4 + e]));
+            c[e] = on ? z : c[e];
         } else if constexpr (ROT) {
             const uint64_t y = ptx::ffma2(a[e], cc[e], fmul2(c[e], ns[e]));
-            c[e] = ptx::ffma2(a[e], ss[e], fmul2(c[e], cc[e]));
-            a[e] = y;
+            const uint64_t z = ptx::ffma2(a[e], ss[e], fmul2(c[e], cc[e]));
+            a[e] = on ? y : a[e];
+            c[e] = on ? z : c[e];
         }
         a[e] = fmul2(a[e], sc);
         c[e] = fmul2(c[e], sc);
@@ -156,9 +162,9 @@ __device__ __forceinline__ void rope_store(uint8_t *dst, int gap, const uint4 &r
 }
 
 // A thread: 16 dims (x) of every blockDim.y-th head of one token.  blockDim = (D / 16, head lanes,
-// tokens).  The loads of its first K and V head and of a batch of NB q-heads go out first; the angles
+// tokens).  ALL: every dim is rotated.  The loads of its first K and V head and of a batch of NB q-heads go out first; the angles
 // of its 8 pairs, shared by all heads, and the cache slot are computed while they are in flight.
-template <typename T, bool INTER, int NB>
+template <typename T, bool INTER, int NB, bool ALL>
 __global__ void __launch_bounds__(kRopeThreads, 5) rope_append_kernel(const __grid_constant__ RopeParams p) {
     __shared__ __align__(16) unsigned long long turn[kRopeMaxPairs];
     const int x = threadIdx.x, Y = blockDim.y * gridDim.y;
@@ -267,15 +273,14 @@ __global__ void __launch_bounds__(kRopeThreads, 5) rope_append_kernel(const __gr
     }
     auto store = [&](uint8_t *dst, const uint4 &a, const uint4 &c, float d) {
         const float inv = __fdividef(1.f, d);
-        if (rotated) rope_store<T, INTER, true>(dst, gap, a, c, inv, cc, ss, ns);
-        else rope_store<T, INTER, false>(dst, gap, a, c, inv, cc, ss, ns);
+        rope_store<T, INTER, true>(dst, gap, a, c, inv, ALL || rotated, cc, ss, ns);
     };
     if (ok) {
         uint8_t *dk = p.ko + outer * p.ko_s[0] + row * p.ko_s[1] + da;
         uint8_t *dv = p.vo + outer * p.vo_s[0] + row * p.vo_s[1] + 16 * x;
         for (int h = y; h < p.Hkv; h += Y) {
             store(dk + h * p.ko_s[2], ka, kb, kd);
-            if (has_v) rope_store<T, INTER, false>(dv + h * p.vo_s[2], 8, va, vb, __fdividef(1.f, vd), cc, ss, ns);
+            if (has_v) rope_store<T, INTER, false>(dv + h * p.vo_s[2], 8, va, vb, __fdividef(1.f, vd), false, cc, ss, ns);
             if (h + Y < p.Hkv) {
                 sk += Y * p.k_s[2];
                 sv += Y * p.v_s[2];
@@ -309,15 +314,19 @@ cudaError_t launch_rope_batch(const RopeParams &p, int lanes, int spread, cudaSt
     const int xs = p.D / 16;
     const int ys = std::max(1, std::min(lanes, kRopeThreads / xs)), zs = kRopeThreads / (xs * ys);
     const dim3 grid((unsigned)(((long long)p.T + zs - 1) / zs), (unsigned)((spread + ys - 1) / ys));
-    rope_append_kernel<T, INTER, NB><<<grid, dim3(xs, ys, zs), 0, s>>>(p);
+    if (p.rot == p.D) rope_append_kernel<T, INTER, NB, true><<<grid, dim3(xs, ys, zs), 0, s>>>(p);
+    else rope_append_kernel<T, INTER, NB, false><<<grid, dim3(xs, ys, zs), 0, s>>>(p);
     return cudaGetLastError();
 }
 
 template <typename T, bool INTER>
 cudaError_t launch_rope(const RopeParams &p, int sm_count, cudaStream_t s) {
-    // Many tokens: as many head lanes as kv-heads (at most eight), so that a thread's q-heads share its
-    // angles.  Few: a lane per q-head, and the heads over several CTAs, to shorten the chain.
-    if (p.T >= sm_count) return launch_rope_batch<T, INTER, 2>(p, std::min(p.Hkv, 8), 1, s);
+    // Enough tokens for two CTAs per SM: half as many head lanes as kv-heads, four at most, so that a
+    // thread's heads share its angles (8192 tokens of 32 + 2 x 8 heads, d = 128: 28 us with four lanes,
+    // 30 with eight, 31 with two).  Fewer: a lane per q-head, and the heads over several CTAs, to shorten
+    // the chain.
+    const int lanes = std::max(1, std::min(p.Hkv / 2, 4));
+    if ((long long)p.T * lanes * (p.D / 16) >= 2LL * sm_count * kRopeThreads) return launch_rope_batch<T, INTER, 2>(p, lanes, 1, s);
     return launch_rope_batch<T, INTER, 1>(p, p.Hq, p.Hq, s);
 }
 
