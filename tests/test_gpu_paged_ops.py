@@ -430,6 +430,15 @@ def test_rope_append_dense_many_tokens():
     check_rope(p, torch.float16, 32, 16, True, layout="dense", descales=False)
 
 
+@pytest.mark.parametrize("D,DV,R,off,Hq,Hkv,T,inter", [
+    (128, 128, 128, 0, 24, 8, 1301, False), (96, 96, 32, 24, 9, 9, 1707, True), (192, 128, 64, 128, 10, 5, 1799, False),
+    (256, 256, 256, 0, 7, 7, 1111, True), (64, 64, 48, 8, 8, 1, 9733, False)])
+def test_rope_append_prefill(D, DV, R, off, Hq, Hkv, T, inter):
+    """Token counts at which a thread walks several heads: odd numbers of them, packed, with a tail."""
+    p = Problem([T - 500 + 16, 500], [T - 500, 500], Hq=Hq, Hkv=Hkv, D=D, DV=DV, packed=True, tail=2, seed=42)
+    check_rope(p, torch.bfloat16, R, off, inter)
+
+
 @pytest.mark.parametrize("freq", [torch.float64, torch.float32])
 def test_rope_append_far_positions(freq):
     """Positions up to 2^29 and negative ones; an attention factor.  The 64-bit reference's own
@@ -445,12 +454,15 @@ def test_rope_append_saturates_and_keeps_nan():
     check_rope(p, torch.bfloat16, 64, 0, False, mult=1e4)
     x = torch.zeros((1, 4, 1, 64), dtype=torch.bfloat16, device="cuda")
     x[0, 0, 0, 0], x[0, 1, 0, 0], x[0, 2, 0, 0] = math.inf, -math.inf, math.nan
-    zero = torch.zeros(1, dtype=torch.float64).expand(32).contiguous().cuda()
     ko, vo = p.k.cuda(), p.v.cuda()
-    fa8.rope_append(x, x, x, zero, k_out=ko, v_out=vo, rotary_offset=0, **p.index_args())
-    ok()
-    got = val(vo.cpu())[int(p.bt[0, 0]), :4, 0, 0]
-    assert got[0] == 448 and got[1] == -448 and got[2].isnan() and got[3] == 0
+    for inter in (False, True):  # dims 16 to 47 rotated; an infinity beside them stays one
+        fa8.rope_append(x, x, x, torch.ones(16, dtype=torch.float64).cuda(), k_out=ko, v_out=vo, rotary_offset=16,
+                        interleaved=inter, **p.index_args())
+        ok()
+        for cache in (ko, vo):
+            got = val(cache.cpu())[int(p.bt[0, 0]), :4, 0]
+            assert got[0, 0] == 448 and got[1, 0] == -448 and got[2, 0].isnan() and got[3, 0] == 0
+            assert (got[:, 1:] == 0).all()
 
 
 def test_rope_inv_freq_on_device_matches_angles():
