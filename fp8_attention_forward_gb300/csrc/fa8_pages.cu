@@ -7,6 +7,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "fa8.h"
 #include "fa8_host.h"
@@ -151,17 +152,17 @@ template <int D, int NT, int TB>
 struct SelCfg {
     static constexpr int GP = 2 * NT;        // TB = 4: rows per token
     static constexpr int ROW = 2 * D;        // bytes of a page's bounds
-    static constexpr int PITCH = ROW + (ROW % 128 == 0 ? 64 : 0);  // two rows' lanes meet different banks
+    // piece ch of row r of a buffer: rows a multiple of 128 bytes long alternate their halves, so that two
+    // rows' lanes meet different banks
+    static __device__ __forceinline__ int at(int r, int ch) { return r * ROW + 16 * (ROW % 128 == 0 ? ch ^ ((r & 1) << 2) : ch); }
     static constexpr int NV = ROW / 64;      // 16-byte vectors of a row per lane
     static constexpr int STEPS = ROW / 16;   // MMA k-steps
-    static constexpr int BUF = 16 * PITCH;   // 16 pages
-    // chunks in a warp's ring: one where four tokens share a pass (more CTAs per SM hide the copies: 49.7
-    // against 55 us for 512 tokens of 512 pages), two else (56 against 58 us for the ragged batch)
-    static constexpr int NBUF = TB == 1 ? 2 : 1;
-    static constexpr int RING = kSelWarps * NBUF * BUF;
+    static constexpr int BUF = 16 * ROW;   // 16 pages
+    static constexpr int RING = kSelWarps * BUF;
     static constexpr int QR = TB == 1 ? 8 * NT : TB * GP;  // query rows of one pass
     static constexpr int Q_BYTES = NT * STEPS * 32 * 8 + QR * D;  // as MMA fragments, and as they are
     static constexpr int W = kSelWarps / TB;  // warps that choose for a token
+    static_assert(W * TB == kSelWarps, "every warp belongs to one team, whose barrier counts its threads");
     // per token after the ring: fp32 scores, list, scratch, two bit masks; the 64-bit keys of undecided
     // pages take the ring's place
     static __host__ __device__ int words(int table) { return (table + 31) / 32; }
@@ -179,6 +180,11 @@ __device__ __forceinline__ unsigned int order_f32(float v) {
 }
 __device__ __forceinline__ float unorder_f32(unsigned int u) {
     return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
 }
 // E4M3 code as a whole number of 2^-9 (NaN not handled)
 __device__ __forceinline__ int fixed_e4m3(unsigned int code) {
@@ -333,12 +339,12 @@ __device__ __forceinline__ unsigned long long exact_key(const uint8_t *src, cons
 // Exact choice from fp32 scores: E4M3 products are exact, an MMA adds 16 of them to the running
 // sum, and what it drops is below 2^-23 of the largest magnitude passing through (fp32's 24 bits; a
 // probe over five kinds of data finds a quarter of that at most), itself at most
-// A = max_h |q_h|_1 * max|bound|.  So a score is off by at most eps = (2 D / 16 + 1) 2^-23 A: the MMA
+// A = max_h |q_h|_1 * max|bound| (of which the kernel takes a bound).  So a score is off by at most eps = (2 D / 16 + 1) 2^-23 A: the MMA
 // steps and the sum of their two chains.  With t the k-th largest fp32 score, pages above t + 2 eps
 // are in and pages below t - 2 eps out whatever the true scores; the few between are scored again
 // in 64-bit integers (E4M3 is a whole number of 2^-9) and ranked by (score, lower index).
 template <int D, int NT, int TB>
-__global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_constant__ SelectParams p) {
+__global__ void __launch_bounds__(kSelThreads, D > 128 ? 4 : (TB == 1 && NT == 1 ? 7 : 5)) select_pages_kernel(const __grid_constant__ SelectParams p) {
     using C = SelCfg<D, NT, TB>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
@@ -379,6 +385,28 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
         ntok = min(TB, Lq - i0);
         if (blk < 0 || ntok <= 0 || tok0 < 0 || (long long)tok0 + ntok > p.T) return;
     }
+    const long long bb = p.cu_q ? 0 : b;
+    const long long t0 = p.cu_q ? tok0 : i0;
+    const int *bt = p.tab.bt + (long long)b * p.tab.bt_stride;
+    const uint8_t *q = p.q + bb * p.q_s[0] + t0 * p.q_s[1] + (long long)kvh * p.G * p.q_s[2];
+    // the loads that the first scores wait for go out together: the query rows, the first pages (as far as
+    // the table goes: the lengths are still on their way), the lengths.  Padding query rows repeat a real
+    // one: the maximum does not see them.
+    constexpr int QN = (C::QR * (D / 16) + kSelThreads - 1) / kSelThreads;
+    uint4 qv[QN];
+    auto load_q = [&](int g0) {
+#pragma unroll
+        for (int k = 0; k < QN; ++k) {
+            const int x = tid + k * kSelThreads, r = x / (D / 16), ch = x - r * (D / 16);
+            const int tk = TB == 1 ? 0 : min(r / C::GP, ntok - 1);
+            const int h = TB == 1 ? (g0 + r < p.G ? g0 + r : g0) : (r % C::GP < p.G ? r % C::GP : 0);
+            if (r < C::QR) qv[k] = __ldg(reinterpret_cast<const uint4 *>(q + tk * p.q_s[1] + h * p.q_s[2] + 16 * ch));
+        }
+    };
+    load_q(0);
+    const int p0 = p.keep_first + 16 * (warp * CS + rank), stride = 16 * kSelWarps * CS;
+    auto id_at = [&](int it) { return lane < 16 && (long long)p0 + it * stride + lane < p.tab.max_pages ? __ldg(bt + p0 + it * stride + lane) : -1; };
+    const int id_0 = id_at(0), id_1 = id_at(1);
     const int Lk = p.tab.cu_k[b + 1] - p.tab.cu_k[b];
     bool bad = Lk < 0 || (long long)Lk > (long long)p.tab.max_pages * ps;
     if (bad && tid == 0) atomicOr(p.status, kStatusBounds);
@@ -387,13 +415,11 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
         const int vis = bad ? 0 : (p.causal ? min(Lk, Lk - Lq + i + 1) : Lk);
         return vis > 0 ? (vis - 1) / ps + 1 : 0;
     };
-    const long long bb = p.cu_q ? 0 : b;
-    const long long t0 = p.cu_q ? tok0 : i0;
     const int n_last = pages_of(i0 + ntok - 1);  // the most of the CTA's tokens
     // ---- this thread's team chooses for one token
     Team<C::W> team;
-    team.id = TB == 1 ? 0 : warp;
-    team.t = TB == 1 ? tid : lane;
+    team.id = tid / (32 * C::W);
+    team.t = tid % (32 * C::W);
     const int words = C::words(p.tab.max_pages);
     uint8_t *mine = smem + C::front(p.tab.max_pages) + team.id * ((C::token_bytes(p.tab.max_pages) + 15) & ~15);
     float *scores = reinterpret_cast<float *>(mine);
@@ -407,61 +433,56 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
     if (n_last <= p.K) return;
     if (CS > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 
-    const int *bt = p.tab.bt + (long long)b * p.tab.bt_stride;
-    const uint8_t *q = p.q + bb * p.q_s[0] + t0 * p.q_s[1] + (long long)kvh * p.G * p.q_s[2];
     const uint8_t *bounds = p.bounds + (long long)kvh * p.b_s[1];
+    const unsigned int b_stride = (unsigned int)p.b_s[0];
     const int from = p.keep_first, to = n_last - p.keep_last;  // pages that go by score
 
     // ---- scores of this CTA's pages: chunk it is pages from + 16 ((warp + 4 it) CS + rank) ..
     uint2 *qf = reinterpret_cast<uint2 *>(smem);
-    const uint32_t ring = ptx::smem_u32(smem + C::Q_BYTES) + warp * C::NBUF * C::BUF;
-    const int p0 = from + 16 * (warp * CS + rank), stride = 16 * kSelWarps * CS;
+    const uint32_t ring = ptx::smem_u32(smem + C::Q_BYTES) + warp * C::BUF;
     const int chunks = to > p0 ? (to - p0 + stride - 1) / stride : 0;
     uint32_t kmax2[4] = {0, 0, 0, 0};
     float l1[TB];
 #pragma unroll
     for (int t = 0; t < TB; ++t) l1[t] = 0.f;
     for (int g0 = 0; g0 < (TB == 1 ? p.G : 1); g0 += 8 * NT) {
+        if (g0) {
+            __syncthreads();  // the last group's rows have been read
+            load_q(g0);
+        }
         // lane i < 16 holds the i-th page of the chunk that is fetched next; eight consecutive lanes copy
         // 128 consecutive bytes
-        auto id_of = [&](int it) { return lane < 16 && it < chunks && p0 + it * stride + lane < to ? bt[p0 + it * stride + lane] : -1; };
-        int id = id_of(0), id2 = id_of(1);
-        unsigned int live = 0;  // bit 16 b + i: page i of buffer b is there
+        auto id_of = [&](int it) { return lane < 16 && it < chunks && p0 + it * stride + lane < to ? __ldg(bt + p0 + it * stride + lane) : -1; };
+        int id = p0 + lane < to ? id_0 : -1, id2 = p0 + stride + lane < to ? id_1 : -1;
+        unsigned int ok = 0;  // bit i: page i of the buffer is there
         constexpr int RP = C::ROW / 16;  // 16-byte pieces of a row
         auto fetch = [&](int it) {
-            const int buf = C::NBUF == 1 ? 0 : it & 1;
-            const bool ok = id >= 0 && id < p.num_pages;
-            if (!ok && lane < 16 && p0 + it * stride + lane < to) atomicOr(p.status, kStatusBounds);
-            const unsigned int m = __ballot_sync(0xffffffffu, ok);
-            const long long off = ok ? id * p.b_s[0] : 0;
+            const bool good = id >= 0 && id < p.num_pages;
+            if (!good && lane < 16 && p0 + it * stride + lane < to) atomicOr(p.status, kStatusBounds);
+            const unsigned int m = __ballot_sync(0xffffffffu, good), page = good ? id : 0;
+            auto copy = [&](auto all) {  // all: no page is missing
 #pragma unroll
-            for (int u = 0; u < RP / 2; ++u) {
-                const int r = 32 % RP == 0 ? (32 / RP) * u + lane / RP : (32 * u + lane) / RP;
-                const int ch = 32 % RP == 0 ? lane % RP : (32 * u + lane) % RP;
-                const uint8_t *src = bounds + 16 * ch + __shfl_sync(0xffffffffu, off, r);
-                const uint32_t dst = ring + buf * C::BUF + r * C::PITCH + 16 * ch;
-                if (m == 0xFFFFu) cp_async16(dst, src, 16);
-                else cp_async16(dst, m >> r & 1u ? src : p.bounds, m >> r & 1u ? 16 : 0);
-            }
-            live = buf ? (live & 0xFFFFu) | m << 16 : (live & 0xFFFF0000u) | m;
+                for (int u = 0; u < RP / 2; ++u) {
+                    const int r = 32 % RP == 0 ? (32 / RP) * u + lane / RP : (32 * u + lane) / RP;
+                    const int ch = 32 % RP == 0 ? lane % RP : (32 * u + lane) % RP;
+                    const uint8_t *src = bounds + 16 * ch + (unsigned long long)__shfl_sync(0xffffffffu, page, r) * b_stride;
+                    const uint32_t dst = ring + C::at(r, ch);
+                    if constexpr (decltype(all)::value) cp_async16(dst, src, 16);
+                    else cp_async16(dst, m >> r & 1u ? src : p.bounds, m >> r & 1u ? 16 : 0);
+                }
+            };
+            if (m == 0xFFFFu) copy(std::true_type());
+            else copy(std::false_type());
+            ok = m;
             id = id2;
             id2 = id_of(it + 2);
         };
-#pragma unroll 1
-        for (int i = 0; i < C::NBUF; ++i) {
-            if (i < chunks) fetch(i);
-            cp_async_commit();
-        }
-        // the query rows, while the first pages arrive; padding rows repeat a real one: the maximum
-        // does not see them
-        if (g0) __syncthreads();
+        if (chunks > 0) fetch(0);
+        cp_async_commit();
         uint8_t *qraw = smem + NT * C::STEPS * 32 * 8;
-        for (int x = tid; x < C::QR * (D / 16); x += kSelThreads) {
-            const int r = x / (D / 16), ch = x - r * (D / 16);
-            const int tk = TB == 1 ? 0 : min(r / C::GP, ntok - 1);
-            const int h = TB == 1 ? (g0 + r < p.G ? g0 + r : g0) : (r % C::GP < p.G ? r % C::GP : 0);
-            *reinterpret_cast<uint4 *>(qraw + 16 * x) = __ldg(reinterpret_cast<const uint4 *>(q + tk * p.q_s[1] + h * p.q_s[2] + 16 * ch));
-        }
+#pragma unroll
+        for (int k = 0; k < QN; ++k)
+            if (tid + k * kSelThreads < C::QR * (D / 16)) *reinterpret_cast<uint4 *>(qraw + 16 * (tid + k * kSelThreads)) = qv[k];
         __syncthreads();
 #pragma unroll 2
         for (int x = tid; x < NT * C::STEPS * 32; x += kSelThreads) {
@@ -499,9 +520,8 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
         __syncthreads();
 #pragma unroll 1
         for (int it = 0; it < chunks; ++it) {
-            cp_async_wait<C::NBUF - 1>();
+            cp_async_wait<0>();
             __syncwarp();
-            const uint32_t buf = ring + (C::NBUF == 1 ? 0 : it & 1) * C::BUF + (lane >> 2) * C::PITCH + 16 * (lane & 3);
             float acc[NT][4], acc2[NT][4];  // two chains of dependent MMAs
 #pragma unroll
             for (int t = 0; t < NT; ++t)
@@ -509,7 +529,7 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
                 for (int e = 0; e < 4; ++e) acc[t][e] = acc2[t][e] = 0.f;
 #pragma unroll
             for (int v = 0; v < C::NV; ++v) {
-                const Bytes<16> x = ld_shared<16>(buf + 64 * v), y = ld_shared<16>(buf + 8 * C::PITCH + 64 * v);
+                const Bytes<16> x = ld_shared<16>(ring + C::at(lane >> 2, 4 * v + (lane & 3))), y = ld_shared<16>(ring + C::at(8 + (lane >> 2), 4 * v + (lane & 3)));
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
                     uint32_t a[4];
@@ -521,9 +541,10 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
                         mma_f16(s & 1 ? acc2[t] : acc[t], a[0], a[1], a[2], a[3], bf.x, bf.y);
                     }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const __half2 z = __hmax2(__habs2(*reinterpret_cast<__half2 *>(&a[e])), *reinterpret_cast<__half2 *>(&kmax2[e]));
-                        kmax2[e] = *reinterpret_cast<const uint32_t *>(&z);
+                    for (int e = 0; e < 2; ++e) {  // |x| + |y| bounds both, and an addition is cheaper than a maximum
+                        const __half2 z = __hadd2(__habs2(*reinterpret_cast<__half2 *>(&a[2 * e])), __habs2(*reinterpret_cast<__half2 *>(&a[2 * e + 1])));
+                        const __half2 m = __hmax2(z, *reinterpret_cast<__half2 *>(&kmax2[2 * (s & 1) + e]));
+                        kmax2[2 * (s & 1) + e] = *reinterpret_cast<const uint32_t *>(&m);
                     }
                 }
             }
@@ -531,9 +552,9 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[t][e] += acc2[t][e];
-            const unsigned int ok = C::NBUF == 1 ? live : live >> (16 * (it & 1));
+            const unsigned int there = ok;
             __syncwarp();  // the buffer has been read
-            if (it + C::NBUF < chunks) fetch(it + C::NBUF);
+            if (it + 1 < chunks) fetch(it + 1);
             cp_async_commit();
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -542,35 +563,32 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
                     float *dst = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(scores) +
                                                            (TB == 1 ? 0 : (token - team.id) * ((C::token_bytes(p.tab.max_pages) + 15) & ~15)));
                     if (pg >= to) return;
-                    if (!(ok >> pl & 1u)) s = -INFINITY;
+                    if (s != s) s = INFINITY;  // a NaN ranks above all
+                    if (!(there >> pl & 1u)) s = -INFINITY;
                     if (TB == 1 && g0) s = fmaxf(s, dst[pg]);
                     dst[pg] = s;
                 };
-                // maximum over two columns; a NaN ranks above all
-                auto top = [&](int t) {
-                    const float x = acc[t][2 * half], y = acc[t][2 * half + 1];
-                    return x != x || y != y ? INFINITY : fmaxf(x, y);
-                };
+                auto top = [&](int t) { return max_nan(acc[t][2 * half], acc[t][2 * half + 1]); };
                 if constexpr (TB == 1) {
                     float s = top(0);
 #pragma unroll
-                    for (int t = 1; t < NT; ++t) s = fmaxf(s, top(t));
-                    s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, 1));
-                    s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, 2));
+                    for (int t = 1; t < NT; ++t) s = max_nan(s, top(t));
+                    s = max_nan(s, __shfl_xor_sync(0xffffffffu, s, 1));
+                    s = max_nan(s, __shfl_xor_sync(0xffffffffu, s, 2));
                     if (c == 0) put(0, s);
                 } else if constexpr (C::GP == 8) {
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
                         float s = top(t);
-                        s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, 1));
-                        s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, 2));
+                        s = max_nan(s, __shfl_xor_sync(0xffffffffu, s, 1));
+                        s = max_nan(s, __shfl_xor_sync(0xffffffffu, s, 2));
                         if (c == t) put(t, s);
                     }
                 } else if constexpr (C::GP == 4) {
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
                         float s = top(t);
-                        s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, 1));
+                        s = max_nan(s, __shfl_xor_sync(0xffffffffu, s, 1));
                         if ((c & 1) == t) put(2 * t + (c >> 1), s);
                     }
                 } else {
@@ -628,7 +646,7 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const __grid_
         a_k = fmaxf(a_k, s_kw[w]);
     }
     for (int r = 0; CS > 1 && r < CS; ++r) a_k = fmaxf(a_k, s_kmax[r]);
-    const float eps2 = 2.f * (C::STEPS + 1) * 0x1p-23f * a_l1 * a_k;
+    const float eps2 = 2.002f * (C::STEPS + 1) * 0x1p-23f * a_l1 * a_k;
     float t_hi = INFINITY, t_lo = INFINITY;
     if (want > 0) {
         const float t = unorder_f32(team.kth_score(scores + from, last - from, want));
@@ -795,6 +813,7 @@ fa8_status check_bounds(const fa8_tensor *t, long long Hkv, long long D) {
     if (t->stride[3] != 1 || t->stride[2] != D) return fail(FA8_ERR_INVALID_ARG, "bounds: the last two dims must be contiguous");
     for (int i = 0; i < 2; ++i)
         if (t->stride[i] < 0 || t->stride[i] % 16 != 0) return fail(FA8_ERR_INVALID_ARG, "bounds: strides must be multiples of 16 bytes");
+    if (t->stride[0] > 0x7fffffffLL) return fail(FA8_ERR_UNSUPPORTED, "bounds: a page's stride must be below 2^31 bytes");
     if (!aligned16(t->data)) return fail(FA8_ERR_INVALID_ARG, "bounds: data must be 16-byte aligned");
     if (t->shape[0] < 0 || t->shape[0] > 0x7fffffffLL) return fail(FA8_ERR_UNSUPPORTED, "too many pages");
     if (t->shape[0] > 0 && !t->data) return fail(FA8_ERR_INVALID_ARG, "bounds has a null data pointer");
@@ -909,14 +928,14 @@ fa8_status fa8_select_pages(const fa8_tensor *q, const fa8_tensor *bounds, fa8_t
     p.status = ds->status;
     // Several tokens per request and enough of them to fill the GPU in blocks of four: one pass over
     // the bounds serves four tokens.  Else a token at a time, and where there are few (token, kv-head)
-    // pairs a cluster of CTAs shares each pair's pages, 128 or more a CTA, up to four CTAs per SM in all
-    // (512 pairs: 51 us without clusters, 53 with two CTAs each, 58 with four).
+    // pairs a cluster of CTAs shares each pair's pages, 128 or more a CTA, up to the seven CTAs that fit an
+    // SM (512 ragged pairs of up to 2048 pages: 46 us in clusters of two, 55 without).
     const long long blocks = p.cu_q ? (long long)qs.T / 4 + qs.B : (long long)qs.B * ((qs.Sq + 3) / 4);
     const bool four = p.G <= 8 && (long long)qs.T >= 4LL * qs.B && blocks * Hkv >= 2LL * ds->sm_count &&
                       p.tab.max_pages <= fa8::kSelMaxTable4;
     p.cluster = 1;
     if (!four)
-        while (p.cluster < fa8::kSelMaxCluster && rows * p.cluster * 2 <= 4LL * ds->sm_count && p.tab.max_pages >= 128 * p.cluster * 2)
+        while (p.cluster < fa8::kSelMaxCluster && rows * p.cluster * 2 <= 7LL * ds->sm_count && p.tab.max_pages >= 128 * p.cluster * 2)
             p.cluster *= 2;
     if (blocks * Hkv > 0x7fffffffLL) return fail(FA8_ERR_UNSUPPORTED, "problem too large for the grid");
     const unsigned grid = (unsigned)(four ? blocks * Hkv : rows);
