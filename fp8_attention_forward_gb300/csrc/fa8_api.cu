@@ -125,6 +125,7 @@ fa8_status device_state(DeviceState **out) {
         e = cudaGetSymbolAddress(&ptr, g_fa8_status_word);
         if (e != cudaSuccess) return cuda_fail(e, "cudaGetSymbolAddress(status)");
         d.status = static_cast<unsigned int *>(ptr);
+        d.ordinal = dev;
         d.ready = true;
     }
     *out = &d;

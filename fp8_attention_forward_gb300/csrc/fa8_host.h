@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "fa8.h"
 
 namespace fa8 {
@@ -18,11 +20,26 @@ void clear_error();
 
 struct DeviceState {
     bool ready = false;
+    int ordinal = 0;
     int sm_count = 0;
     unsigned int *status = nullptr;
 };
 // State of the current device, looked up on the first call for it.
 fa8_status device_state(DeviceState **out);
+
+// Opts a kernel in to `bytes` of dynamic shared memory on a device, once per size: what each device has
+// been given for this kernel so far.
+struct SmemOptIn {
+    std::atomic<int> given[64] = {};
+    template <typename K>
+    cudaError_t operator()(K *kernel, int bytes, int ordinal) {
+        if (given[ordinal].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        int had = given[ordinal].load(std::memory_order_relaxed);
+        while (e == cudaSuccess && had < bytes && !given[ordinal].compare_exchange_weak(had, bytes)) {}
+        return e;
+    }
+};
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool supported_dims(int d, int dv);

@@ -343,6 +343,12 @@ __device__ __forceinline__ unsigned long long exact_key(const uint8_t *src, cons
 // steps and the sum of their two chains.  With t the k-th largest fp32 score, pages above t + 2 eps
 // are in and pages below t - 2 eps out whatever the true scores; the few between are scored again
 // in 64-bit integers (E4M3 is a whole number of 2^-9) and ranked by (score, lower index).
+//
+// Bound: for many pages HBM (2 D bytes per page and kv-head) and the ALU pipe that widens them; else the
+// chain of a CTA: 4 us to its first score, 5 us to choose.  Measured, d = 128: 64 x 8 pairs of 64 .. 2048
+// pages (140 MB): 47 us, 3.0 TB/s, 0.44 of the copy rate (a token's pages in one CTA with two buffers:
+// 51; per-lane bulk copies: 65; fragments straight to registers: 73); 512 tokens x 8 heads over 512 pages:
+// 40 us (a token at a time: 164); one pair of 2048 pages, d = 256, a cluster of eight CTAs: 14 us (22).
 template <int D, int NT, int TB>
 __global__ void __launch_bounds__(kSelThreads, D > 128 ? 4 : (TB == 1 && NT == 1 ? 7 : 5)) select_pages_kernel(const __grid_constant__ SelectParams p) {
     using C = SelCfg<D, NT, TB>;
@@ -775,9 +781,10 @@ __global__ void __launch_bounds__(kSelThreads, D > 128 ? 4 : (TB == 1 && NT == 1
 }
 
 template <int D, int NT, int TB>
-cudaError_t launch_select(const SelectParams &p, unsigned int rows, cudaStream_t s) {
+cudaError_t launch_select(const SelectParams &p, unsigned int rows, int dev, cudaStream_t s) {
+    static host::SmemOptIn opt_in;
     const int smem = SelCfg<D, NT, TB>::smem(p.tab.max_pages);
-    cudaError_t e = cudaFuncSetAttribute(select_pages_kernel<D, NT, TB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = opt_in(select_pages_kernel<D, NT, TB>, smem, dev);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(rows * p.cluster);
@@ -794,9 +801,9 @@ cudaError_t launch_select(const SelectParams &p, unsigned int rows, cudaStream_t
 }
 
 template <int D>
-cudaError_t launch_select_dim(const SelectParams &p, unsigned int rows, bool four, cudaStream_t s) {
-    if (four) return p.G <= 2 ? launch_select<D, 1, 4>(p, rows, s) : (p.G <= 4 ? launch_select<D, 2, 4>(p, rows, s) : launch_select<D, 4, 4>(p, rows, s));
-    return p.G <= 8 ? launch_select<D, 1, 1>(p, rows, s) : launch_select<D, 2, 1>(p, rows, s);
+cudaError_t launch_select_dim(const SelectParams &p, unsigned int rows, bool four, int dev, cudaStream_t s) {
+    if (four) return p.G <= 2 ? launch_select<D, 1, 4>(p, rows, dev, s) : (p.G <= 4 ? launch_select<D, 2, 4>(p, rows, dev, s) : launch_select<D, 4, 4>(p, rows, dev, s));
+    return p.G <= 8 ? launch_select<D, 1, 1>(p, rows, dev, s) : launch_select<D, 2, 1>(p, rows, dev, s);
 }
 
 }  // namespace fa8
@@ -942,11 +949,11 @@ fa8_status fa8_select_pages(const fa8_tensor *q, const fa8_tensor *bounds, fa8_t
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaErrorInvalidValue;
     switch (qs.D) {
-        case 64: e = fa8::launch_select_dim<64>(p, grid, four, s); break;
-        case 96: e = fa8::launch_select_dim<96>(p, grid, four, s); break;
-        case 128: e = fa8::launch_select_dim<128>(p, grid, four, s); break;
-        case 192: e = fa8::launch_select_dim<192>(p, grid, four, s); break;
-        case 256: e = fa8::launch_select_dim<256>(p, grid, four, s); break;
+        case 64: e = fa8::launch_select_dim<64>(p, grid, four, ds->ordinal, s); break;
+        case 96: e = fa8::launch_select_dim<96>(p, grid, four, ds->ordinal, s); break;
+        case 128: e = fa8::launch_select_dim<128>(p, grid, four, ds->ordinal, s); break;
+        case 192: e = fa8::launch_select_dim<192>(p, grid, four, ds->ordinal, s); break;
+        case 256: e = fa8::launch_select_dim<256>(p, grid, four, ds->ordinal, s); break;
     }
     if (e != cudaSuccess) return cuda_fail(e, "page selection kernel launch");
     return FA8_SUCCESS;

@@ -511,7 +511,8 @@ __global__ void __launch_bounds__(32 * PW, D + DV <= 256 && NT == 1 ? 16 / PW : 
 }
 
 template <int D, int DV, int NT, int PW>
-fa8_status launch_pages(PagesParams &p, const fa8_tensor *k, const fa8_tensor *v, unsigned int tiles, cudaStream_t s) {
+fa8_status launch_pages(PagesParams &p, const fa8_tensor *k, const fa8_tensor *v, unsigned int tiles, int dev, cudaStream_t s) {
+    static host::SmemOptIn opt_in;
     using C = PgCfg<D, DV, NT, PW>;
     const int ps = p.tab.page_size;
     p.box = std::gcd(ps, C::KC);
@@ -525,7 +526,7 @@ fa8_status launch_pages(PagesParams &p, const fa8_tensor *k, const fa8_tensor *v
         if ((st = host::encode_kv(&tk, k, C::CW, p.box)) || (st = host::encode_kv(&tv, v, C::CWV, p.box))) return st;
     }
     const int smem = C::smem(p.K);
-    cudaError_t e = cudaFuncSetAttribute(fwd_pages_kernel<D, DV, NT, PW>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = opt_in(fwd_pages_kernel<D, DV, NT, PW>, smem, dev);
     if (e != cudaSuccess) return host::cuda_fail(e, "page attention shared memory");
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(tiles * p.cluster);
@@ -659,10 +660,10 @@ extern "C" fa8_status fa8_fwd_pages(const fa8_tensor *q, const fa8_tensor *k, co
     cudaStream_t s = static_cast<cudaStream_t>(stream);
 #define FA8_PAGES(D_, DV_)                                                                               \
     case D_ * 1000 + DV_:                                                                                \
-        return nt == 1 ? (wide ? fa8::launch_pages<D_, DV_, 1, 8>(p, k, v, (unsigned)tiles, s)           \
-                               : fa8::launch_pages<D_, DV_, 1, 4>(p, k, v, (unsigned)tiles, s))          \
-                       : (wide ? fa8::launch_pages<D_, DV_, 2, 8>(p, k, v, (unsigned)tiles, s)           \
-                               : fa8::launch_pages<D_, DV_, 2, 4>(p, k, v, (unsigned)tiles, s));
+        return nt == 1 ? (wide ? fa8::launch_pages<D_, DV_, 1, 8>(p, k, v, (unsigned)tiles, ds->ordinal, s)           \
+                               : fa8::launch_pages<D_, DV_, 1, 4>(p, k, v, (unsigned)tiles, ds->ordinal, s))          \
+                       : (wide ? fa8::launch_pages<D_, DV_, 2, 8>(p, k, v, (unsigned)tiles, ds->ordinal, s)           \
+                               : fa8::launch_pages<D_, DV_, 2, 4>(p, k, v, (unsigned)tiles, ds->ordinal, s));
     switch (qs.D * 1000 + DV) {
         FA8_PAGES(64, 64)
         FA8_PAGES(96, 96)
