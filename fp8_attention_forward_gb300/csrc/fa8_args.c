@@ -1,7 +1,7 @@
 /* fa8_args.c -- CPython module that turns torch tensors into fa8_tensor views and calls an entry point
  * of libfa8.so.  Argument marshalling only, as the ctypes binding does it, for the calls of a decode
  * step: their kernels run for a few microseconds, less than the views took to build in Python.
- * Uses tensors through their Python attributes only (data_ptr, dtype, shape, stride).
+ * Uses tensors through their Python attributes only (data_ptr, dtype, shape, stride, get_device).
  *
  * Every function takes the entry point's address, then its arguments in the C order (tensor or None,
  * number), the stream handle last, and returns the status.
@@ -11,12 +11,13 @@
 
 #include "fa8.h"
 
-static PyObject *s_data_ptr, *s_dtype, *s_shape, *s_stride;
+static PyObject *s_data_ptr, *s_dtype, *s_shape, *s_stride, *s_get_device;
 static PyObject *g_dtypes[16];
 static int g_codes[16], g_ndtypes;
 
-/* Fills *v from tensor `t` and points *out at it; None gives a null pointer. */
-static int view(PyObject *t, fa8_tensor *v, fa8_tensor **out) {
+/* Fills *v from tensor `t` and points *out at it; None gives a null pointer.  Every tensor has to be on
+ * the first one's device, *device (-2: not known yet). */
+static int view(PyObject *t, fa8_tensor *v, fa8_tensor **out, long *device) {
     PyObject *x, *y;
     Py_ssize_t n, i;
     *out = NULL;
@@ -29,6 +30,14 @@ static int view(PyObject *t, fa8_tensor *v, fa8_tensor **out) {
         return -1;
     }
     v->dtype = g_codes[i];
+    if (!(x = PyObject_CallMethodNoArgs(t, s_get_device))) return -1;
+    const long dev = PyLong_AsLong(x);
+    Py_DECREF(x);
+    if (*device == -2) *device = dev;
+    if (dev != *device) {
+        PyErr_SetString(PyExc_ValueError, "all tensors must be on one device");
+        return -1;
+    }
     if (!(x = PyObject_CallMethodNoArgs(t, s_data_ptr))) return -1;
     v->data = PyLong_AsVoidPtr(x);
     Py_DECREF(x);
@@ -64,6 +73,7 @@ typedef struct {
  * point's address. */
 static int take(PyObject *const *a, Py_ssize_t n, const char *form, views *w, int *ints, float *f, void **fn, void **stream) {
     int nt = 0, ni = 0;
+    long device = -2;
     const Py_ssize_t len = (Py_ssize_t)strlen(form);
     if (n != len + 2) {
         PyErr_Format(PyExc_TypeError, "%zd arguments, %zd expected", n, len + 2);
@@ -73,7 +83,7 @@ static int take(PyObject *const *a, Py_ssize_t n, const char *form, views *w, in
     for (Py_ssize_t k = 0; k < len; ++k) {
         PyObject *x = a[k + 1];
         if (form[k] == 't') {
-            if (view(x, &w->v[nt], &w->p[nt])) return -1;
+            if (view(x, &w->v[nt], &w->p[nt], &device)) return -1;
             ++nt;
         } else if (form[k] == 'i') {
             const long long v = PyLong_AsLongLong(x);
@@ -149,6 +159,7 @@ PyMODINIT_FUNC PyInit_fa8_args(void) {
     s_dtype = PyUnicode_InternFromString("dtype");
     s_shape = PyUnicode_InternFromString("shape");
     s_stride = PyUnicode_InternFromString("stride");
-    if (!s_data_ptr || !s_dtype || !s_shape || !s_stride) return NULL;
+    s_get_device = PyUnicode_InternFromString("get_device");
+    if (!s_data_ptr || !s_dtype || !s_shape || !s_stride || !s_get_device) return NULL;
     return PyModule_Create(&module);
 }

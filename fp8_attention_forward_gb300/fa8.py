@@ -255,6 +255,7 @@ def _packed(name):
         buf = _ARGS()
         at = start = ctypes.addressof(buf)
         passed = []
+        device = None
         for a in args[:-1]:
             if type(a) in _SCALARS:
                 if type(a) is int and not -(1 << 31) <= a < 1 << 31:
@@ -267,6 +268,9 @@ def _packed(name):
                 raise TypeError(f"unsupported dtype {a.dtype}")
             if n > 4:
                 raise ValueError("at most 4 dims")
+            if a.get_device() != (a.get_device() if device is None else device):
+                raise ValueError("all tensors must be on one device")
+            device = a.get_device()
             _ARG[n].pack_into(buf, at - start, a.data_ptr(), _DTYPES[a.dtype], n, *shape, *a.stride())
             passed.append(at)
             at += 80
@@ -309,7 +313,9 @@ def _call(name, device, stream, *args):
     """One library call on ``device``; tensors are passed as views, the stream goes last."""
     fn = _entry(name)
     if device.type != "cuda":
-        status = fn(*args, 0)
+        if torch.cuda.is_available():
+            raise ValueError("the tensors must be on a CUDA device")
+        status = fn(*args, 0)  # refuses what it would refuse, else says that there is no device
     else:
         index = device.index
         handle = _raw_stream(index) if stream is None else stream.cuda_stream

@@ -512,6 +512,27 @@ def test_bad_table_entries_are_reported():
     assert fa8.check() == fa8.FA8_ERR_DEVICE_BOUNDS
 
 
+@pytest.mark.parametrize("python", [False, True])
+def test_host_tensors_are_refused(python, monkeypatch):
+    monkeypatch.setattr(fa8, "_entries", {})
+    if python:
+        monkeypatch.setattr(fa8, "_args_module", lambda: None)
+    p = Problem([64], [1], Hq=2, Hkv=1, ps=16, seed=18)
+    lists = torch.zeros((1, 1, 1, 2), dtype=torch.int32)
+    args = (p.q.cuda(), p.k.cuda(), p.v.cuda(), lists.cuda())
+    for i in range(4):
+        mixed = list(args)
+        mixed[i] = mixed[i].cpu()
+        with pytest.raises(ValueError, match="device"):
+            fa8.fwd_pages(*mixed, **p.index_args())
+    with pytest.raises(ValueError, match="device"):
+        fa8.fwd_pages(*args, **dict(p.index_args(), block_table=p.bt))
+    with pytest.raises(ValueError, match="device"):
+        fa8.page_bounds(p.k, **{n: t for n, t in p.index_args("cpu").items() if n != "cu_seqlens_q"})
+    fa8.fwd_pages(*args, **p.index_args())
+    ok()
+
+
 # ------------------------------------------------------------------ together
 def chain(q, k, v, inv, p, kc, vc, bnd, K, dev_args, ds, **kw):
     q8 = fa8.rope_append(q, k, v, inv, k_out=kc, v_out=vc, descale_q=ds, descale_k=ds, descale_v=ds, **dev_args)
