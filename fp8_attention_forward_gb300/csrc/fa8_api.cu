@@ -304,8 +304,10 @@ EncodeTiledFn get_encode(fa8_status *st) {
 }
 
 CUtensorMapSwizzle swizzle_for(int chunk_bytes) {
-    return chunk_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
-                              : (chunk_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B);
+    return chunk_bytes == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+           : chunk_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+           : chunk_bytes == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
+                               : CU_TENSOR_MAP_SWIZZLE_NONE;
 }
 
 // 4-D byte tensor {inner, d1, d2, d3} with byte strides {s1, s2, s3}, box {b0, b1, b2, 1}.

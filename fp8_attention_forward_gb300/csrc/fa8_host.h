@@ -62,7 +62,7 @@ struct Table {
 fa8_status check_table(const fa8_tensor *cu_k, const fa8_tensor *bt, int page_size, int B, Table *out);
 
 // TMA map of a paged K or V pool {d, head, row, page} whose boxes are `width` bytes of one head by
-// `rows` rows, with the swizzle of that width.
+// `rows` rows, with the swizzle of that width (128, 64 or 32; none for others).
 fa8_status encode_kv(CUtensorMap *m, const fa8_tensor *t, int width, int rows);
 // The bound on every in-kernel wait (fa8_set_wait_timeout_ns).
 unsigned long long wait_timeout_ns();

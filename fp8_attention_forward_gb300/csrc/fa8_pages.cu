@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const __gri
     const uint8_t *src = p.k + (long long)page * p.k_s[0] + (long long)h * p.k_s[2] + 16 * c;
     uint32_t lo[8], hi[8];
     {  // every part starts from row 0: a part may have no row of its own
-        const Bytes<16> v = ld_stream<16>(src);
+        const Bytes<16> v = ld_stream(src);
 #pragma unroll
         for (int i = 0; i < 4; ++i) e4m3x4_to_h2(v.w[i], lo[2 * i], lo[2 * i + 1]);
 #pragma unroll
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const __gri
     for (int r = part; r < rows; r += 32) {  // eight loads in flight
         Bytes<16> v[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) v[u] = ld_stream<16>(src + (long long)min(r + 4 * u, rows - 1) * p.k_s[1]);
+        for (int u = 0; u < 8; ++u) v[u] = ld_stream(src + (long long)min(r + 4 * u, rows - 1) * p.k_s[1]);
 #pragma unroll
         for (int u = 0; u < 8; ++u)
             if (r + 4 * u < rows) take(v[u]);

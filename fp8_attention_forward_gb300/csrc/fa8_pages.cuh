@@ -69,34 +69,30 @@ __device__ __forceinline__ uint32_t zip_hi(uint32_t x, uint32_t y) {
     return d;
 }
 
-// read-once global loads of N = 4, 8 or 16 bytes (no L1 allocation)
 template <int N>
 struct Bytes {
     uint32_t w[N / 4];
 };
-template <int N>
-__device__ __forceinline__ Bytes<N> ld_stream(const uint8_t *p) {
-    Bytes<N> r;
-    if constexpr (N == 16)
-        asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3])
-                     : "l"(p));
-    else if constexpr (N == 8)
-        asm volatile("ld.global.nc.L1::no_allocate.v2.b32 {%0, %1}, [%2];" : "=r"(r.w[0]), "=r"(r.w[1]) : "l"(p));
-    else
-        asm volatile("ld.global.nc.L1::no_allocate.b32 %0, [%1];" : "=r"(r.w[0]) : "l"(p));
+// read-once global load of 16 bytes (no L1 allocation)
+__device__ __forceinline__ Bytes<16> ld_stream(const uint8_t *p) {
+    Bytes<16> r;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3])
+                 : "l"(p));
     return r;
 }
-
+// N bytes of shared memory, aligned to N (12: to 4)
 template <int N>
 __device__ __forceinline__ Bytes<N> ld_shared(uint32_t addr) {
     Bytes<N> r;
-    if constexpr (N == 16)
+    if constexpr (N == 16) {
         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]) : "r"(addr) : "memory");
-    else if constexpr (N == 8)
+    } else if constexpr (N == 8) {
         asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.w[0]), "=r"(r.w[1]) : "r"(addr) : "memory");
-    else
-        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r.w[0]) : "r"(addr) : "memory");
+    } else {
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r.w[i]) : "r"(addr + 4 * i) : "memory");
+    }
     return r;
 }
 

@@ -69,10 +69,12 @@ struct PgCfg {
     static constexpr int MT = D + DV <= 256 ? 2 : 1;  // 16-key tiles per chunk
     static constexpr int KC = 16 * MT;                // keys per chunk
     static constexpr int NG = 2 * MT;                 // 8-key groups per chunk
-    // rows arrive as blocks of CW bytes, each block KC rows deep with the swizzle of its width
-    static constexpr int CW = D % 128 == 0 ? 128 : (D % 64 == 0 ? 64 : 32), NCK = D / CW;
-    static constexpr int CWV = DV % 128 == 0 ? 128 : (DV % 64 == 0 ? 64 : 32), NCV = DV / CWV;
-    static constexpr int VK = CW >= 64 ? 16 : 8;      // bytes of one K fragment load
+    // rows arrive as blocks of CW bytes, each block KC rows deep with the swizzle of its width (rows of
+    // 96 bytes in one block without one: four of them cover all banks once)
+    static constexpr int CW = D % 128 == 0 ? 128 : (D % 64 == 0 ? 64 : 96), NCK = D / CW;
+    static constexpr int CWV = DV % 128 == 0 ? 128 : (DV % 64 == 0 ? 64 : 96), NCV = DV / CWV;
+    static_assert(NCK * CW == D && NCV * CWV == DV, "head dims");
+    static constexpr int VK = CW == 96 ? 8 : 16;      // bytes of one K fragment load
     static constexpr int NKV = D / (4 * VK);          // K fragment loads per key and lane
     static constexpr int VB = CWV / 8;                // bytes of one V fragment load
     static constexpr int STEPS = D / 16;
@@ -83,6 +85,10 @@ struct PgCfg {
     static constexpr int MERGE_BYTES = PW * ROWS * (OPITCH + 2) * 4;
     static constexpr int OFF_Q = PW * STAGE, OFF_ENT = OFF_Q + Q_BYTES;
     static int smem(int K) { return 1024 + std::max(OFF_ENT + ((K * 8 + 15) & ~15), MERGE_BYTES); }
+    // CTAs per SM that registers are cut to: four of four warps, but where 16 rows of wide heads would
+    // spill (d = dv = 192, 60 lists of 960 keys x 8 heads: 37.6 us against 54.7 uncut; 16 rows, d = dv =
+    // 128: 24.8 against 31.7; 16 rows, d = dv = 256: 52.9 cut against 32)
+    static constexpr int CTAS = PW > 4 ? 1 : (NT == 2 && D + DV > 256 ? 2 : 4);
     // first of the VK channels that lane column c takes with fragment load v (rows of 128 bytes: the
     // pieces 2c and 2c + 1 of a block, so that two rows' lanes meet different banks)
     static __device__ __forceinline__ int k_dim(int v, int c) {
@@ -91,7 +97,7 @@ struct PgCfg {
     // byte offset in a stage of byte x of a row of width-W blocks (TMA swizzle of W bytes)
     template <int W>
     static __device__ __forceinline__ int at(int row, int x) {
-        const int piece = (x % W) >> 4, sw = W == 128 ? row & 7 : (W == 64 ? (row >> 1) & 3 : (row >> 2) & 1);
+        const int piece = (x % W) >> 4, sw = W == 128 ? row & 7 : (W == 64 ? (row >> 1) & 3 : 0);
         return (x / W) * KC * W + row * W + 16 * (piece ^ sw) + (x & 15);
     }
     // dv index of slot s (0 .. DV / 8 - 1) of the lane with row r
@@ -99,7 +105,7 @@ struct PgCfg {
 };
 
 template <int D, int DV, int NT, int PW>
-__global__ void __launch_bounds__(32 * PW, D + DV <= 256 && NT == 1 ? 16 / PW : 1) fwd_pages_kernel(
+__global__ void __launch_bounds__(32 * PW, PgCfg<D, DV, NT, PW>::CTAS) fwd_pages_kernel(
     const __grid_constant__ PagesParams p, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
     using C = PgCfg<D, DV, NT, PW>;
     constexpr int kThreads = 32 * PW;
@@ -647,14 +653,14 @@ extern "C" fa8_status fa8_fwd_pages(const fa8_tensor *q, const fa8_tensor *k, co
     p.num_pages = (int)k->shape[0];
     p.status = ds->status;
     p.timeout_ns = wait_timeout_ns();
-    // Clusters split a list over CTAs while the grid is below 16 warps per SM and every warp keeps at
-    // least two chunks; where clusters of eight still leave SMs empty, CTAs of eight warps split it once
+    // Clusters split a list over CTAs while all of them run at once and every warp keeps at least two
+    // chunks; where clusters of eight still leave SMs empty, CTAs of eight warps split it once
     // more (8 lists of 4096 keys, d = dv = 256: 12.4 us against 15.2 with four warps; 512 lists of 2048
     // keys, d = dv = 128: 53 against 48.5).
     const long long keys = (long long)p.K * page_size;
-    const int kc = qs.D + DV <= 256 ? 32 : 16;
+    const int kc = qs.D + DV <= 256 ? 32 : 16, per_sm = nt == 2 && qs.D + DV > 256 ? 2 : 4;
     p.cluster = 1;
-    while (p.cluster < fa8::kPgMaxCluster && tiles * p.cluster * 2 <= 4LL * ds->sm_count && keys >= 2LL * kc * 4 * p.cluster * 2)
+    while (p.cluster < fa8::kPgMaxCluster && tiles * p.cluster * 2 <= (long long)per_sm * ds->sm_count && keys >= 2LL * kc * 4 * p.cluster * 2)
         p.cluster *= 2;
     const bool wide = p.cluster == fa8::kPgMaxCluster && tiles * p.cluster <= ds->sm_count && keys >= 2LL * kc * 8 * p.cluster;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
