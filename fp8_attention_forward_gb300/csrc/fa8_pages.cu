@@ -163,12 +163,13 @@ struct SelCfg {
     static constexpr int Q_BYTES = NT * STEPS * 32 * 8 + QR * D;  // as MMA fragments, and as they are
     static constexpr int W = kSelWarps / TB;  // warps that choose for a token
     static_assert(W * TB == kSelWarps, "every warp belongs to one team, whose barrier counts its threads");
-    // per token after the ring: fp32 scores, list, scratch, two bit masks; the 64-bit keys of undecided
-    // pages take the ring's place
+    // per token after the ring: fp32 scores, list, scratch, two bit masks; the keys of undecided pages take
+    // the ring's place: 64 bits each of kSelList, or the upper 16 bits of every page's 48
     static __host__ __device__ int words(int table) { return (table + 31) / 32; }
     static __host__ __device__ int token_bytes(int table) { return words(table) * (32 * 4 + 8) + kSelList * 4 + 64; }
+    static __host__ __device__ int key_bytes(int table) { return words(table) * 64 > kSelList * 8 ? words(table) * 64 : kSelList * 8; }
     static __host__ __device__ int front(int table) {
-        const int keys = TB * words(table) * 32 * 8;
+        const int keys = TB * key_bytes(table);
         return Q_BYTES + (keys > RING ? keys : RING);
     }
     static int smem(int table) { return 128 + front(table) + TB * ((token_bytes(table) + 15) & ~15); }
@@ -224,25 +225,37 @@ struct Team {
         return v;
     }
     // The rank-th largest (rank >= 1) of scores [0, n), as ordered integers: bisection by counting, done
-    // when exactly `rank` scores lie in the upper part (after about as many steps as n has bits).
+    // when exactly `rank` scores lie in the upper part (after about as many steps as n has bits).  A thread
+    // keeps HELD scores in registers; one warp takes twice as many of a longer list (1024 pages: 70 us
+    // for 512 tokens x 8 heads against 80; 2048: 175 against 183), four warps gain nothing by it.
+    template <int HELD>
     __device__ __forceinline__ unsigned int kth_score(const float *scores, int n, unsigned int rank) const {
-        unsigned int v[kSelHeld], hi = 0, nlo = 0;
+        unsigned int v[HELD], hi = 0, nlo = 0;
 #pragma unroll
-        for (int j = 0; j < kSelHeld; ++j) {
+        for (int j = 0; j < HELD; ++j) {
             const int i = t + 32 * W * j;
             v[j] = i < n ? order_f32(scores[i]) : 0u;  // no score is 0: that is a NaN's place
         }
 #pragma unroll
-        for (int j = 0; j < kSelHeld; ++j) {
+        for (int j = 0; j < HELD; ++j) {
             hi = max(hi, v[j]);
             if (v[j]) nlo = max(nlo, ~v[j]);
         }
+        // the scores behind them, eight loads at once
+        auto rest = [&](auto f) {
 #pragma unroll 1
-        for (int i = t + 32 * W * kSelHeld; i < n; i += 32 * W) {
-            const unsigned int u = order_f32(scores[i]);
+            for (int i = t + 32 * W * HELD; i < n; i += 8 * 32 * W) {
+                unsigned int u[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) u[k] = i + 32 * W * k < n ? order_f32(scores[i + 32 * W * k]) : 0u;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) f(u[k]);
+            }
+        };
+        rest([&](unsigned int u) {
             hi = max(hi, u);
-            nlo = max(nlo, ~u);
-        }
+            if (u) nlo = max(nlo, ~u);
+        });
         hi = reduce<true>(hi);
         unsigned int lo = ~reduce<true>(nlo);
 #pragma unroll 1
@@ -250,9 +263,8 @@ struct Team {
             const unsigned int mid = lo + (hi - lo + 1) / 2;
             unsigned int c = 0, low = 0;  // scores from mid up: how many, and the complement of the least
 #pragma unroll
-            for (int j = 0; j < kSelHeld; ++j) c += v[j] >= mid;
-#pragma unroll 1
-            for (int i = t + 32 * W * kSelHeld; i < n; i += 32 * W) c += order_f32(scores[i]) >= mid;
+            for (int j = 0; j < HELD; ++j) c += v[j] >= mid;
+            rest([&](unsigned int u) { c += u >= mid; });
             c = reduce<false>(c);
             if (c < rank) {
                 hi = mid - 1;
@@ -261,25 +273,24 @@ struct Team {
             lo = mid;
             if (c > rank) continue;
 #pragma unroll
-            for (int j = 0; j < kSelHeld; ++j)
+            for (int j = 0; j < HELD; ++j)
                 if (v[j] >= mid) low = max(low, ~v[j]);
-#pragma unroll 1
-            for (int i = t + 32 * W * kSelHeld; i < n; i += 32 * W) {
-                const unsigned int u = order_f32(scores[i]);
+            rest([&](unsigned int u) {
                 if (u >= mid) low = max(low, ~u);
-            }
+            });
             return ~reduce<true>(low);
         }
         return lo;
     }
-    // The largest key that at least `rank` (>= 1) of keys [0, n) reach.  Keys of 0 are none.
-    __device__ __forceinline__ unsigned long long kth_key(const unsigned long long *keys, int n, unsigned int rank) const {
-        unsigned long long lo = 0, hi = ~0ull;
+    // The largest 48-bit key that at least `rank` (>= 1) of key(0 .. n - 1) reach.  Keys of 0 are none.
+    template <typename F>
+    __device__ __forceinline__ unsigned long long kth_key(F key, int n, unsigned int rank) const {
+        unsigned long long lo = 0, hi = (1ull << 48) - 1;
 #pragma unroll 1
         while (lo < hi) {
             const unsigned long long mid = lo + (hi - lo) / 2 + 1;
             unsigned int c = 0;
-            each(n, [&](int i) { c += keys[i] >= mid; });
+            each(n, [&](int i) { c += key(i) >= mid; });
             if (reduce<false>(c) >= rank) lo = mid;
             else hi = mid - 1;
         }
@@ -288,7 +299,8 @@ struct Team {
 };
 
 // Exact score of one page for q-heads [first, end) of a token, by a warp: sum_c max(q_c lo_c, q_c hi_c) in
-// units of 2^-18, the largest of the heads; a NaN ranks above all.  Order-preserving unsigned key.
+// units of 2^-18, the largest of the heads; a NaN ranks above all.  Order-preserving key of 48 bits:
+// 2^45 + score, which is below 2^44 in magnitude ((448 2^9)^2 times 256 channels), or 2^48 - 1; never 0.
 template <int D>
 __device__ __forceinline__ unsigned long long exact_key(const uint8_t *src, const uint8_t *q, long long q_sh, int first, int end, int lane) {
     constexpr int NW = (D / 4 + 31) / 32;  // words of four channels per lane
@@ -322,13 +334,13 @@ __device__ __forceinline__ unsigned long long exact_key(const uint8_t *src, cons
                 s += (long long)x * (x < 0 ? lo[i][e] : hi[i][e]);
             }
         }
-        // |s| < 2^40: 20 low bits and the rest are summed apart
+        // |s| < 2^40 in a lane: 20 low bits and the rest are summed apart
         const unsigned int low = __reduce_add_sync(0xffffffffu, (unsigned int)s & 0xFFFFFu);
         const int high = __reduce_add_sync(0xffffffffu, (int)(s >> 20));
         const long long sum = ((long long)high << 20) + low;
         best = max(best, __any_sync(0xffffffffu, bad) ? LLONG_MAX : sum);
     }
-    return (unsigned long long)best ^ 0x8000000000000000ull;
+    return best == LLONG_MAX ? (1ull << 48) - 1 : (unsigned long long)(best + (1ll << 45));
 }
 
 // Every CTA scores its pages with f16 MMAs (pages on M, query rows on N; the contraction runs over
@@ -348,7 +360,9 @@ __device__ __forceinline__ unsigned long long exact_key(const uint8_t *src, cons
 // chain of a CTA: 4 us to its first score, 5 us to choose.  Measured, d = 128: 64 x 8 pairs of 64 .. 2048
 // pages (140 MB): 47 us, 3.0 TB/s, 0.44 of the copy rate (a token's pages in one CTA with two buffers:
 // 51; per-lane bulk copies: 65; fragments straight to registers: 73); 512 tokens x 8 heads over 512 pages:
-// 40 us (a token at a time: 164); one pair of 2048 pages, d = 256, a cluster of eight CTAs: 14 us (22).
+// 40 us (a token at a time: 164), over 1024 and 2048 pages 70 and 175 us (106 and 282 with 64-bit keys of
+// every page in shared memory and one load at a time behind the held scores); one pair of 2048 pages,
+// d = 256, a cluster of eight CTAs: 14 us (22); one of 16384, d = 128: 87 us, most of it the choice.
 template <int D, int NT, int TB>
 __global__ void __launch_bounds__(kSelThreads, D > 128 ? 4 : (TB == 1 && NT == 1 ? 7 : 5)) select_pages_kernel(const __grid_constant__ SelectParams p) {
     using C = SelCfg<D, NT, TB>;
@@ -432,7 +446,7 @@ __global__ void __launch_bounds__(kSelThreads, D > 128 ? 4 : (TB == 1 && NT == 1
     int *list = reinterpret_cast<int *>(mine + words * 128);
     team.words = reinterpret_cast<unsigned int *>(list + kSelList);
     unsigned int *sel = team.words + 16, *amb = sel + words;
-    unsigned long long *keys = reinterpret_cast<unsigned long long *>(smem + C::Q_BYTES) + (size_t)team.id * words * 32;
+    uint8_t *key_mem = smem + C::Q_BYTES + team.id * C::key_bytes(p.tab.max_pages);
     const int n = team.id < ntok ? pages_of(i0 + team.id) : 0;
     int *out = p.pages + bb * p.o_s[0] + (t0 + team.id) * p.o_s[1] + kvh * p.o_s[2];
     if (team.id < ntok && n <= p.K && rank == 0) team.each(p.K, [&](int j) { out[j] = j < n ? j : -1; });
@@ -655,7 +669,10 @@ __global__ void __launch_bounds__(kSelThreads, D > 128 ? 4 : (TB == 1 && NT == 1
     const float eps2 = 2.002f * (C::STEPS + 1) * 0x1p-23f * a_l1 * a_k;
     float t_hi = INFINITY, t_lo = INFINITY;
     if (want > 0) {
-        const float t = unorder_f32(team.kth_score(scores + from, last - from, want));
+        unsigned int kth;
+        if (C::W > 1 || last - from <= 32 * kSelHeld) kth = team.template kth_score<kSelHeld>(scores + from, last - from, want);
+        else kth = team.template kth_score<2 * kSelHeld>(scores + from, last - from, want);
+        const float t = unorder_f32(kth);
         t_hi = __fadd_ru(t, eps2);
         t_lo = __fsub_rd(t, eps2);
     }
@@ -708,6 +725,7 @@ __global__ void __launch_bounds__(kSelThreads, D > 128 ? 4 : (TB == 1 && NT == 1
             return exact_key<D>(bounds + (long long)id * p.b_s[0], q + (TB == 1 ? 0 : team.id) * p.q_s[1], p.q_s[2], hs, he, lane);
         };
         if (n_amb <= kSelList) {
+            unsigned long long *keys = reinterpret_cast<unsigned long long *>(key_mem);
             // by rank among the undecided; every warp scores a part of each page's heads
             team.each(n_amb, [&](int i) { keys[i] = 0; });
             team.sync();
@@ -726,26 +744,31 @@ __global__ void __launch_bounds__(kSelThreads, D > 128 ? 4 : (TB == 1 && NT == 1
                 if (ahead < places) atomicOr(&sel[pg >> 5], 1u << (pg & 31));
             });
         } else {
-            // many (equal or nearly equal pages): a warp per page, then bisection over the keys
-            team.each(n, [&](int i) { keys[i] = 0; });
-            team.sync();
+            // many (equal or nearly equal pages): a warp per page, then bisection over the keys, whose lower
+            // 32 bits take the scores' place
+            unsigned int *key_lo = reinterpret_cast<unsigned int *>(scores);
+            unsigned short *key_hi = reinterpret_cast<unsigned short *>(key_mem);
+            auto key_at = [&](int i) { return (unsigned long long)key_hi[i] << 32 | key_lo[i]; };
 #pragma unroll 1
-            for (int w = tw; w < nw; w += C::W)
+            for (int w = tw; w < nw; w += C::W) {
+                if (!(amb[w] >> lane & 1u)) key_lo[32 * w + lane] = 0, key_hi[32 * w + lane] = 0;
 #pragma unroll 1
                 for (unsigned int bits = amb[w]; bits; bits &= bits - 1) {
                     const int pg = 32 * w + __ffs(bits) - 1;
                     const unsigned long long key = key_of(pg, 0, p.G);
-                    if (lane == 0) keys[pg] = key;
+                    __syncwarp();  // the page's score has been read
+                    if (lane == 0) key_lo[pg] = (unsigned int)key, key_hi[pg] = (unsigned short)(key >> 32);
                 }
+            }
             team.sync();
-            const unsigned long long t = team.kth_key(keys, n, places);
+            const unsigned long long t = team.kth_key(key_at, n, places);
             unsigned int c = 0;
-            team.each(n, [&](int i) { c += keys[i] > t; });
+            team.each(n, [&](int i) { c += key_at(i) > t; });
             int left = places - (int)team.template reduce<false>(c);  // of the keys equal to t
             if (tw == 0) {  // ties at the threshold in index order
                 for (int w = 0; w < nw; ++w) {
                     const bool on = amb[w] >> lane & 1u;
-                    const unsigned long long key = on ? keys[32 * w + lane] : 0;
+                    const unsigned long long key = on ? key_at(32 * w + lane) : 0;
                     unsigned int take = __ballot_sync(0xffffffffu, on && key > t);
                     unsigned int tie = __ballot_sync(0xffffffffu, on && key == t);
                     while (tie && left > 0) {

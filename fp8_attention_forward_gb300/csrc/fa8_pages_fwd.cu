@@ -655,7 +655,7 @@ extern "C" fa8_status fa8_fwd_pages(const fa8_tensor *q, const fa8_tensor *k, co
     p.timeout_ns = wait_timeout_ns();
     // Clusters split a list over CTAs while all of them run at once and every warp keeps at least two
     // chunks; where clusters of eight still leave SMs empty, CTAs of eight warps split it once
-    // more (8 lists of 4096 keys, d = dv = 256: 12.4 us against 15.2 with four warps; 512 lists of 2048
+    // more (8 lists of 4096 keys, d = dv = 256: 12.4 us against 16.8 with four warps; 512 lists of 2048
     // keys, d = dv = 128: 53 against 48.5).
     const long long keys = (long long)p.K * page_size;
     const int kc = qs.D + DV <= 256 ? 32 : 16, per_sm = nt == 2 && qs.D + DV > 256 ? 2 : 4;

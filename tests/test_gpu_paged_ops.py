@@ -167,6 +167,37 @@ def test_select_pages_widest_table():
         assert torch.equal(got[0, 0, 0].long(), want)
 
 
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("four", [False, True], ids=["one", "four"])
+def test_select_pages_keys_of_the_largest_scores(sign, four):
+    """Products of the largest values over 256 channels, apart by the smallest ones, more undecided pages
+    than are ranked directly: the exact scores reach their full width on either side of zero."""
+    n, K = 700, 150
+    p = Problem([8 * n], [1], Hq=2, Hkv=1, D=256, ps=8, seed=43)
+    bnd = torch.full(p.k.shape[:1] + (1, 2, 256), 448.0 * sign, dtype=torch.float64)
+    q = torch.full((1, 1, 2, 256), 448.0, dtype=torch.float64)
+    q[..., 3] = 2.0 ** -9
+    bnd[p.bt[0].long(), 0, :, 3] = (torch.randperm(n, generator=p.g) % 8).double()[:, None] * 2.0 ** -9
+    p.q, b8 = q.float().to(E4M3), bnd.float().to(E4M3)
+    want = ref.select(p, b8, K)[0]
+    if four:
+        m = 1301
+        p.q = p.q.view(torch.uint8).expand(1, m, -1, -1).contiguous().view(E4M3)
+        p.new, p.T = [m], m
+        assert (run_select(p, b8, K, causal=False) == want).all()
+    else:
+        assert torch.equal(run_select(p, b8, K)[0, 0], want)
+
+
+@pytest.mark.parametrize("n", [600, 1025, 2047])
+def test_select_pages_long_lists_by_one_warp(n):
+    """Blocks of four tokens over more pages than a warp holds in registers."""
+    p = Problem([8 * n - 3], [60], Hq=42, Hkv=21, D=64, DV=64, ps=8, seed=44)
+    bnd = e4m3(ref.bounds(p))
+    got = run_select(p, bnd, 77, keep_first=0, keep_last=1)
+    assert torch.equal(p.flat(got), ref.select(p, bnd, 77, True, 0, 1))
+
+
 @pytest.mark.parametrize("Hkv", [2, 40])
 def test_packed_rows_ahead_of_the_first_sequence_stay(Hkv):
     """cu_seqlens_q that begins past row 0, one token at a time and in blocks of four."""
