@@ -19,7 +19,8 @@
 // Many tokens of one request (512 x 8 lists of 2048 keys, 2.1 GB through L2): 211 us; the ALU pipe,
 // which widens E4M3 to f16, is at 62 %.  The same with fragments loaded straight to registers: 63 and
 // 303 us; by 16-byte asynchronous copies: 61 and 258 us (L2 is asked for every sector twice); QK by the
-// E4M3 warp MMA: 48.5 and 218 us (it widens too); three buffers and fewer CTAs per SM: slower.
+// E4M3 warp MMA: 48.5 and 218 us (it widens too); a second K or V buffer: 217 to 220 us,
+// both: 245.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -266,7 +267,8 @@ __global__ void __launch_bounds__(32 * PW, PgCfg<D, DV, NT, PW>::CTAS) fwd_pages
             for (int e = 0; e < 4; ++e) o[d][t][e] = 0.f;
 
     for (int it = 0; it < chunks; ++it) {
-        if (!W.wait_warp(bar_k, it & 1)) {
+        if (!W.wait_warp(bar_k, it & 1)) {  // another warp may have given up: this one's copies are still on their way
+            W.drain(bar_k, it & 1);
             W.drain(bar_v, it & 1);
             break;
         }
@@ -380,6 +382,7 @@ __global__ void __launch_bounds__(32 * PW, PgCfg<D, DV, NT, PW>::CTAS) fwd_pages
         }
         // ---- O^T
         if (!W.wait_warp(bar_v, it & 1)) {
+            W.drain(bar_v, it & 1);
             if (more) W.drain(bar_k, (it + 1) & 1);
             break;
         }
