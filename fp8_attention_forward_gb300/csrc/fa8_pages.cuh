@@ -57,16 +57,16 @@ __device__ __forceinline__ void e4m3x4_to_h2(uint32_t w, uint32_t &lo, uint32_t 
     lo = ptx::e4m3x2_to_h2(w);
     hi = ptx::e4m3x2_to_h2(w >> 16);
 }
-// byte pairs of two words: (x0, y0, x1, y1) and (x2, y2, x3, y3)
-__device__ __forceinline__ uint32_t zip_lo(uint32_t x, uint32_t y) {
-    uint32_t d;
-    asm("prmt.b32 %0, %1, %2, 0x5140;" : "=r"(d) : "r"(x), "r"(y));
-    return d;
+// two 16 x 16 byte tiles transposed, rows at the addresses of lanes 0 .. 15 and 16 .. 31: lane (r, c) gets
+// column r of rows 4c .. 4c + 3 and column r + 8 of them, of either tile
+__device__ __forceinline__ void ld_trans_b8(uint32_t (&d)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+                 : "r"(addr)
+                 : "memory");
 }
-__device__ __forceinline__ uint32_t zip_hi(uint32_t x, uint32_t y) {
-    uint32_t d;
-    asm("prmt.b32 %0, %1, %2, 0x7362;" : "=r"(d) : "r"(x), "r"(y));
-    return d;
+__device__ __forceinline__ void st_shared_zero16(uint32_t addr) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0) : "memory");
 }
 
 template <int N>

@@ -63,6 +63,7 @@ struct PagesParams {
 };
 
 constexpr int kPgMaxCluster = 8;
+constexpr float kPgSlack = 8.f;
 
 template <int D, int DV, int NT, int PW>
 struct PgCfg {
@@ -77,7 +78,6 @@ struct PgCfg {
     static_assert(NCK * CW == D && NCV * CWV == DV, "head dims");
     static constexpr int VK = CW == 96 ? 8 : 16;      // bytes of one K fragment load
     static constexpr int NKV = D / (4 * VK);          // K fragment loads per key and lane
-    static constexpr int VB = CWV / 8;                // bytes of one V fragment load
     static constexpr int STEPS = D / 16;
     static constexpr int DT = DV / 16;                // 16-row tiles of O^T
     static constexpr int OPITCH = DV + 4;             // floats per row of a merge buffer
@@ -101,8 +101,6 @@ struct PgCfg {
         const int piece = (x % W) >> 4, sw = W == 128 ? row & 7 : (W == 64 ? (row >> 1) & 3 : 0);
         return (x / W) * KC * W + row * W + 16 * (piece ^ sw) + (x & 15);
     }
-    // dv index of slot s (0 .. DV / 8 - 1) of the lane with row r
-    static __device__ __forceinline__ int slot_dv(int s, int r) { return (s / VB) * CWV + VB * r + s % VB; }
 };
 
 template <int D, int DV, int NT, int PW>
@@ -204,6 +202,9 @@ __global__ void __launch_bounds__(32 * PW, PgCfg<D, DV, NT, PW>::CTAS) fwd_pages
     // box_shift ..; K is fetched while the chunk before goes through softmax and PV, V during PV and S^T
     const int first = warp * CS + rank, stride = CS * PW;
     const uint32_t ks = ptx::smem_u32(smem) + warp * C::STAGE, vs = ks + C::K_STAGE;
+    // the row of V's 16 x 16 byte tiles that this lane addresses: a lane of the transpose receives keys 2c,
+    // 2c + 1, 2c + 8 and 2c + 9, as P^T's fragments have them
+    const int vrow = 2 * ((lane >> 2) & 3) + (lane & 1) + 8 * ((lane >> 1) & 1);
     const int nb = 1 << p.box_shift, mine = lane & (nb - 1), part = lane >> p.box_shift;
     // this lane's box of the chunk: page, first row, and how many of its keys are visible
     int page, prow, lim;
@@ -226,8 +227,8 @@ __global__ void __launch_bounds__(32 * PW, PgCfg<D, DV, NT, PW>::CTAS) fwd_pages
     };
     // visible keys of 8-key group i (of all lanes)
     auto group_lim = [&](int i) {
-        const int b0 = i * 8 / p.box;
-        return __shfl_sync(0xffffffffu, lim, b0) - (i * 8 - b0 * p.box);
+        const int sh = (C::MT == 2 ? 5 : 4) - p.box_shift, b0 = i * 8 >> sh;  // a box is 2^sh keys
+        return __shfl_sync(0xffffffffu, lim, b0) - (i * 8 - (b0 << sh));
     };
     auto fetch_k = [&]() {
         if (lane == 0) ptx::mbar_arrive_expect_tx(bar_k, (uint32_t)C::K_STAGE);
@@ -323,13 +324,8 @@ __global__ void __launch_bounds__(32 * PW, PgCfg<D, DV, NT, PW>::CTAS) fwd_pages
                             if (off) s[x][t][2 * h + e] = -INFINITY;
                 }
         }
-        // V rows that are not visible may hold anything: their words become zeros below
         const bool partial = !full;
-        int vlim[C::NG];
-        if (partial) {
-#pragma unroll
-            for (int i = 0; i < C::NG; ++i) vlim[i] = group_lim(i);
-        }
+        const int vlim = partial ? group_lim(lane >> 3) - (lane & 7) : 1;  // visible: above 0 for row `lane`
         const bool more = it + 1 < chunks;
         __syncwarp();  // every lane has read the K buffer
         if (more) {
@@ -337,6 +333,8 @@ __global__ void __launch_bounds__(32 * PW, PgCfg<D, DV, NT, PW>::CTAS) fwd_pages
             fetch_k();
         }
         uint32_t pb[C::MT][NT][2];
+        // The maximum that P is taken against moves only when some score is 2^kPgSlack above it (p stays below
+        // f16's range, sums are fp32 anyway): most chunks need no maximum over lanes and no rescaling.
         float mx[NT][2];
         bool moved = false;
 #pragma unroll
@@ -346,17 +344,18 @@ __global__ void __launch_bounds__(32 * PW, PgCfg<D, DV, NT, PW>::CTAS) fwd_pages
                 float y = -INFINITY;
 #pragma unroll
                 for (int x = 0; x < C::MT; ++x) y = fmaxf(y, fmaxf(s[x][t][e], s[x][t][2 + e]));
-#pragma unroll
-                for (int sh = 4; sh < 32; sh <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, sh));
                 mx[t][e] = y * cs;
-                moved |= mx[t][e] > m[t][e];
+                moved |= mx[t][e] > m[t][e] + kPgSlack;
             }
         if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float mn = fmaxf(m[t][e], mx[t][e]);
+                    float mn = mx[t][e];
+#pragma unroll
+                    for (int sh = 4; sh < 32; sh <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, sh));
+                    mn = fmaxf(m[t][e], mn);
                     const float alpha = mn == -INFINITY ? 1.f : ptx::ex2(m[t][e] - mn);  // 0 while nothing has been seen
                     m[t][e] = mn;
                     l[t][e] *= alpha;
@@ -386,34 +385,25 @@ __global__ void __launch_bounds__(32 * PW, PgCfg<D, DV, NT, PW>::CTAS) fwd_pages
             if (more) W.drain(bar_k, (it + 1) & 1);
             break;
         }
+        if (partial) {  // rows that are not visible may hold anything: they become zeros
+            if (lane < C::KC && vlim <= 0)
+#pragma unroll
+                for (int d = 0; d < DV; d += 16) st_shared_zero16(vs + C::template at<C::CWV>(lane, d));
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+        }
 #pragma unroll
         for (int x = 0; x < C::MT; ++x) {
-            uint32_t vr[4][DV / 32];  // keys 2c, 2c + 1 of the tile's two groups
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                const int row = 16 * x + 8 * (y >> 1) + 2 * c + (y & 1);
-#pragma unroll
-                for (int j = 0; j < C::NCV; ++j) {
-                    const Bytes<C::VB> z = ld_shared<C::VB>(vs + C::template at<C::CWV>(row, C::CWV * j + C::VB * r));
-#pragma unroll
-                    for (int w = 0; w < C::VB / 4; ++w) vr[y][C::VB / 4 * j + w] = z.w[w];
-                }
-                if (partial && 2 * c + (y & 1) >= vlim[2 * x + (y >> 1)]) {
-#pragma unroll
-                    for (int w = 0; w < DV / 32; ++w) vr[y][w] = 0u;
-                }
-            }
 #pragma unroll
             for (int w = 0; w < DV / 32; ++w) {
-                uint32_t a[8];
-                e4m3x4_to_h2(zip_lo(vr[0][w], vr[1][w]), a[0], a[1]);
-                e4m3x4_to_h2(zip_hi(vr[0][w], vr[1][w]), a[2], a[3]);
-                e4m3x4_to_h2(zip_lo(vr[2][w], vr[3][w]), a[4], a[5]);
-                e4m3x4_to_h2(zip_hi(vr[2][w], vr[3][w]), a[6], a[7]);
+                uint32_t z[4], a0, a1, a2, a3;
+                ld_trans_b8(z, vs + C::template at<C::CWV>(16 * x + vrow, 32 * w + 16 * (lane >> 4)));
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    mma_f16(o[2 * w][t], a[0], a[1], a[4], a[5], pb[x][t][0], pb[x][t][1]);
-                    mma_f16(o[2 * w + 1][t], a[2], a[3], a[6], a[7], pb[x][t][0], pb[x][t][1]);
+                for (int h = 0; h < 2; ++h) {
+                    e4m3x4_to_h2(z[2 * h], a0, a2);
+                    e4m3x4_to_h2(z[2 * h + 1], a1, a3);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) mma_f16(o[2 * w + h][t], a0, a1, a2, a3, pb[x][t][0], pb[x][t][1]);
                 }
             }
         }
@@ -441,7 +431,7 @@ __global__ void __launch_bounds__(32 * PW, PgCfg<D, DV, NT, PW>::CTAS) fwd_pages
             for (int d = 0; d < C::DT; ++d)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    wo[(warp * C::ROWS + rw) * C::OPITCH + C::slot_dv(2 * d + h, r)] = o[d][t][2 * h + e];
+                    wo[(warp * C::ROWS + rw) * C::OPITCH + 16 * d + 8 * h + r] = o[d][t][2 * h + e];
         }
     __syncthreads();
     // warp buffers -> buffer of warp 0 (relative to the CTA's maximum), and the CTA's m and l
