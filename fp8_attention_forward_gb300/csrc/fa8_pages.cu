@@ -351,9 +351,8 @@ __device__ __forceinline__ unsigned long long exact_key(const uint8_t *src, cons
 // Exact choice from fp32 scores: E4M3 products are exact, an MMA adds 16 of them to the running
 // sum, and what it drops is below 2^-23 of the largest magnitude passing through (fp32's 24 bits; a
 // probe over five kinds of data finds a quarter of that at most), itself at most
-// A = max_h |q_h|_1 * max|bound| (of which the kernel takes a bound).  So a score is off by at most eps = (2 D / 16 + 1) 2^-23 A: the MMA
-// steps and the sum of their two chains.  With t the k-th largest fp32 score, pages above t + 2 eps
-// are in and pages below t - 2 eps out whatever the true scores; the few between are scored again
+// A = max_h |q_h|_1 * max|bound| (of which the kernel takes a bound).  So a score is off by at most
+// eps = (2 D / 16) 2^-23 A over its MMA steps.  With t the k-th largest fp32 score, pages above t + 2 eps are in and pages below t - 2 eps out whatever the true scores; the few between are scored again
 // in 64-bit integers (E4M3 is a whole number of 2^-9) and ranked by (score, lower index).
 //
 // Bound: for many pages HBM (2 D bytes per page and kv-head) and the ALU pipe that widens them; else the
@@ -542,11 +541,11 @@ __global__ void __launch_bounds__(kSelThreads, D > 128 ? 4 : (TB == 1 && NT == 1
         for (int it = 0; it < chunks; ++it) {
             cp_async_wait<0>();
             __syncwarp();
-            float acc[NT][4], acc2[NT][4];  // two chains of dependent MMAs
+            float acc[NT][4];
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[t][e] = acc2[t][e] = 0.f;
+                for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
 #pragma unroll
             for (int v = 0; v < C::NV; ++v) {
                 const Bytes<16> x = ld_shared<16>(ring + C::at(lane >> 2, 4 * v + (lane & 3))), y = ld_shared<16>(ring + C::at(8 + (lane >> 2), 4 * v + (lane & 3)));
@@ -558,7 +557,7 @@ __global__ void __launch_bounds__(kSelThreads, D > 128 ? 4 : (TB == 1 && NT == 1
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
                         const uint2 bf = qf[(t * C::STEPS + 4 * v + s) * 32 + lane];
-                        mma_f16(s & 1 ? acc2[t] : acc[t], a[0], a[1], a[2], a[3], bf.x, bf.y);
+                        mma_f16(acc[t], a[0], a[1], a[2], a[3], bf.x, bf.y);
                     }
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {  // |x| + |y| bounds both, and an addition is cheaper than a maximum
@@ -568,10 +567,6 @@ __global__ void __launch_bounds__(kSelThreads, D > 128 ? 4 : (TB == 1 && NT == 1
                     }
                 }
             }
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[t][e] += acc2[t][e];
             const unsigned int there = ok;
             __syncwarp();  // the buffer has been read
             if (it + 1 < chunks) fetch(it + 1);
@@ -666,7 +661,7 @@ __global__ void __launch_bounds__(kSelThreads, D > 128 ? 4 : (TB == 1 && NT == 1
         a_k = fmaxf(a_k, s_kw[w]);
     }
     for (int r = 0; CS > 1 && r < CS; ++r) a_k = fmaxf(a_k, s_kmax[r]);
-    const float eps2 = 2.002f * (C::STEPS + 1) * 0x1p-23f * a_l1 * a_k;
+    const float eps2 = 2.002f * C::STEPS * 0x1p-23f * a_l1 * a_k;  // 2 eps; 0.002 for A's own roundings
     float t_hi = INFINITY, t_lo = INFINITY;
     if (want > 0) {
         unsigned int kth;

@@ -274,13 +274,13 @@ __global__ void __launch_bounds__(32 * PW, PgCfg<D, DV, NT, PW>::CTAS) fwd_pages
             break;
         }
         // ---- S^T
-        float s[C::MT][NT][4], s2[C::MT][NT][4];  // two sums each: shorter chains of dependent MMAs
+        float s[C::MT][NT][4];
 #pragma unroll
         for (int x = 0; x < C::MT; ++x)
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[x][t][e] = s2[x][t][e] = 0.f;
+                for (int e = 0; e < 4; ++e) s[x][t][e] = 0.f;
 #pragma unroll
         for (int j = 0; j < C::NKV; ++j) {
             Bytes<C::VK> kr[C::NG];
@@ -299,16 +299,10 @@ __global__ void __launch_bounds__(32 * PW, PgCfg<D, DV, NT, PW>::CTAS) fwd_pages
                     e4m3x4_to_h2(kr[2 * x].w[w], a0, a2);
                     e4m3x4_to_h2(kr[2 * x + 1].w[w], a1, a3);
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) mma_f16(w & 1 ? s2[x][t] : s[x][t], a0, a1, a2, a3, bf[t].x, bf[t].y);
+                    for (int t = 0; t < NT; ++t) mma_f16(s[x][t], a0, a1, a2, a3, bf[t].x, bf[t].y);
                 }
             }
         }
-#pragma unroll
-        for (int x = 0; x < C::MT; ++x)
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[x][t][e] += s2[x][t][e];
         // ---- softmax in log2 units of the scaled score: mask, running maximum per row (over the
         // lanes of equal c), and O^T rescaled only when some row's maximum moved
         if (!full) {
