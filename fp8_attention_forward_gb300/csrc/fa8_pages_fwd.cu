@@ -10,17 +10,19 @@
 // A warp works alone: it takes every (warps x cluster)-th chunk of 16 or 32 keys of the list, keeps
 // its own running maximum, sum and O^T in registers, and has one K and one V buffer that TMA fills
 // (boxes of one head's rows of a page, swizzled): the next K while this chunk goes through softmax and
-// PV, the next V during PV and the next S^T.  V's fragments pair the bytes of two keys with one byte
-// permute.  P is rounded to f16 (2^-11 relative; p <= 1 and the running maximum is exact, so nothing
+// PV, the next V during PV and the next S^T.  V's 16 x 16 byte tiles are transposed as they are loaded.  P is
+// rounded to f16 (2^-11 relative; p <= 2^8, as the maximum it is taken against trails by no more, so nothing
 // saturates), not to E4M3 as in fa8_fwd: V widens to f16 anyway.  The warps, then the CTAs of the
 // cluster through distributed shared memory, merge by their maxima: no workspace, no second kernel.
 //
-// Measured (d = dv = 128, 64 x 8 lists of 2048 keys, 267 MB): 48.5 us, 5.5 TB/s, 0.81 of the copy rate.
-// Many tokens of one request (512 x 8 lists of 2048 keys, 2.1 GB through L2): 211 us; the ALU pipe,
-// which widens E4M3 to f16, is at 62 %.  The same with fragments loaded straight to registers: 63 and
-// 303 us; by 16-byte asynchronous copies: 61 and 258 us (L2 is asked for every sector twice); QK by the
-// E4M3 warp MMA: 48.5 and 218 us (it widens too); a second K or V buffer: 217 to 220 us,
-// both: 245.
+// Measured (d = dv = 128, 64 x 8 lists of 2048 keys, 267 MB): 48 us, 5.6 TB/s, 0.82 of the copy rate.
+// Many tokens of one request (512 x 8 lists of 2048 keys, 2.1 GB through L2): 168 us, 12.8 TB/s; shared
+// memory is at 70 %, the ALU pipe, which widens E4M3 to f16, at 54 %, issue slots at 56 %.  The copies and the
+// softmax without the products: 122 us.  Tried: V's fragments by 16-byte loads whose bytes are paired by
+// permutes, 52 and 210 us; both operands straight to registers, 63 and 303; by 16-byte asynchronous copies,
+// 61 and 258 (L2 is asked for every sector twice); QK by the E4M3 warp MMA, 3 % slower (it widens too); a
+// second K or V buffer, 3 to 5 % slower; chunks of 64 keys with three CTAs per SM, 61 and 162 where 32 keys
+// took 51 and 172.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -79,6 +81,9 @@ struct PgCfg {
     static constexpr int VK = CW == 96 ? 8 : 16;      // bytes of one K fragment load
     static constexpr int NKV = D / (4 * VK);          // K fragment loads per key and lane
     static constexpr int STEPS = D / 16;
+    // Q's fragments stay in registers while they take 16 (chunk of tokens, d = 128: 168 us against 171; with
+    // 32, 16 rows of d = 128: 23.2 against 21.6)
+    static constexpr bool HELD = NT * STEPS <= 8;
     static constexpr int DT = DV / 16;                // 16-row tiles of O^T
     static constexpr int OPITCH = DV + 4;             // floats per row of a merge buffer
     static constexpr int K_STAGE = KC * D, V_STAGE = KC * DV, STAGE = K_STAGE + V_STAGE;
@@ -267,6 +272,12 @@ __global__ void __launch_bounds__(32 * PW, PgCfg<D, DV, NT, PW>::CTAS) fwd_pages
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[d][t][e] = 0.f;
 
+    uint2 qh[C::HELD ? NT * C::STEPS : 1];
+    if constexpr (C::HELD) {
+#pragma unroll
+        for (int i = 0; i < NT * C::STEPS; ++i) qh[i] = qf[i * 32 + lane];
+    }
+
     for (int it = 0; it < chunks; ++it) {
         if (!W.wait_warp(bar_k, it & 1)) {  // another warp may have given up: this one's copies are still on their way
             W.drain(bar_k, it & 1);
@@ -292,7 +303,11 @@ __global__ void __launch_bounds__(32 * PW, PgCfg<D, DV, NT, PW>::CTAS) fwd_pages
             for (int w = 0; w < C::VK / 4; ++w) {
                 uint2 bf[NT];
 #pragma unroll
-                for (int t = 0; t < NT; ++t) bf[t] = qf[(t * C::STEPS + j * (C::VK / 4) + w) * 32 + lane];
+                for (int t = 0; t < NT; ++t) {
+                    const int i = t * C::STEPS + j * (C::VK / 4) + w;
+                    if constexpr (C::HELD) bf[t] = qh[i];
+                    else bf[t] = qf[i * 32 + lane];
+                }
 #pragma unroll
                 for (int x = 0; x < C::MT; ++x) {
                     uint32_t a0, a1, a2, a3;
