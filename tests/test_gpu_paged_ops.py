@@ -325,6 +325,26 @@ def test_fwd_pages(c):
     check_attend(p, random_lists(p, K, causal=causal), causal, s, scale, out, descales)
 
 
+@pytest.mark.parametrize("order", ["up", "down", "saw"])
+@pytest.mark.parametrize("span", [3.0, 8.0, 40.0, 400.0])
+@pytest.mark.parametrize("Hq,D", [(4, 128), (12, 64), (8, 256)])
+def test_fwd_pages_scores_that_climb(Hq, D, span, order):
+    """One row's scores run through `span` binary orders over the list, chunk after chunk, up, down and in
+    a saw: the maximum that P is taken against moves in small and in large steps, for some rows only."""
+    n, ps = 900, 16
+    p = Problem([n], [1], Hq=Hq, Hkv=1, D=D, DV=D, ps=ps, seed=45)
+    levels = torch.arange(1, 127).to(torch.uint8).view(E4M3).double()  # the positive values
+    j = torch.arange(n)
+    at = {"up": j * 126 // n, "down": 125 - j * 126 // n, "saw": (j * 5) % n * 126 // n}[order]
+    k = torch.zeros((p.k.shape[0], ps, 1, D), dtype=torch.float64)
+    k[p.bt[0].long()[j // ps], j % ps, 0, 1] = levels[at]
+    q = torch.zeros((1, 1, Hq, D), dtype=torch.float64)
+    q[0, 0, :, 1] = torch.tensor([1.0, 0.5, -1.0, 0.125] * 4)[:Hq].double()
+    p.q, p.k = q.float().to(E4M3), k.float().to(E4M3)
+    lists = torch.arange(-(-n // ps), dtype=torch.int32).reshape(1, 1, -1)
+    check_attend(p, lists, scale=span * math.log(2) / 448, descales=False)
+
+
 def test_fwd_pages_duplicates_order_and_invisible():
     """A page listed twice counts twice; order does not matter; pages past the token add nothing."""
     p = Problem([200], [3], Hq=8, Hkv=2, ps=16, seed=9)
