@@ -18,7 +18,6 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libfa8.so")
-ARGS = os.path.join(BUILD, "fa8_args.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -53,24 +52,38 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(f) <= t for f in _sources() + _headers() + [__file__])
 
 
+def args_path() -> str:
+    """Where the argument module for the running torch lies."""
+    import torch
+
+    return os.path.join(BUILD, f"fa8_args-{torch.__version__}.so")
+
+
 def build_args():
-    """Compiles csrc/fa8_args.c, the CPython module that packs tensor views (needs Python's headers:
-    without them the binding packs the views itself)."""
-    src = os.path.join(CSRC, "fa8_args.c")
-    inc = sysconfig.get_paths()["include"]
-    if not os.path.exists(os.path.join(inc, "Python.h")):
+    """Compiles csrc/fa8_args.cpp, the Python module that packs tensor views (needs Python's and torch's
+    headers: without them the binding packs the views itself)."""
+    import torch
+
+    out, src = args_path(), os.path.join(CSRC, "fa8_args.cpp")
+    py, pt = sysconfig.get_paths()["include"], os.path.dirname(torch.__file__)
+    inc = os.path.join(pt, "include")
+    if not os.path.exists(os.path.join(py, "Python.h")) or not os.path.exists(os.path.join(inc, "ATen", "ATen.h")):
         return None
     deps = [src, os.path.join(ROOT, "include", "fa8.h"), __file__]
-    if os.path.exists(ARGS) and all(os.path.getmtime(f) <= os.path.getmtime(ARGS) for f in deps):
-        return ARGS
+    if os.path.exists(out) and all(os.path.getmtime(f) <= os.path.getmtime(out) for f in deps):
+        return out
     os.makedirs(BUILD, exist_ok=True)
-    tmp = ARGS + f".tmp{os.getpid()}"
-    r = subprocess.run(["gcc", "-O2", "-Wall", "-fPIC", "-shared", "-fvisibility=hidden", "-I", inc, "-I",
-                        os.path.join(ROOT, "include"), src, "-o", tmp], capture_output=True, text=True)
+    tmp = out + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"]
+    cmd += [x for d in (py, inc, os.path.join(inc, "torch", "csrc", "api", "include")) for x in ("-isystem", d)]
+    cmd += ["-I", os.path.join(ROOT, "include"), src, "-o", tmp, "-L", os.path.join(pt, "lib"), "-ltorch_python",
+            "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError("gcc failed on fa8_args.c:\n" + r.stdout + r.stderr)
-    os.replace(tmp, ARGS)
-    return ARGS
+        raise RuntimeError("g++ failed on fa8_args.cpp:\n" + r.stdout + r.stderr)
+    os.replace(tmp, out)
+    return out
 
 
 def build(force: bool = False, ptxas_verbose: bool = False, jobs: int | None = None,
@@ -79,9 +92,9 @@ def build(force: bool = False, ptxas_verbose: bool = False, jobs: int | None = N
     _build/); ``defines`` are extra -D macros (e.g. FA8_TRACE for the pipeline trace);
     ``src_dir`` compiles another copy of the sources instead of csrc/."""
     build_dir = out_dir or BUILD
-    build_args()
     lib = os.path.join(build_dir, "libfa8.so")
     if not force and not ptxas_verbose and not defines and out_dir is None and src_dir is None and up_to_date():
+        build_args()
         return LIB
     os.makedirs(build_dir, exist_ok=True)
     cc = nvcc()
@@ -96,11 +109,13 @@ def build(force: bool = False, ptxas_verbose: bool = False, jobs: int | None = N
 
     jobs = jobs or min(len(srcs), os.cpu_count() or 4)
     logs = []
-    with cf.ThreadPoolExecutor(jobs) as ex:
+    with cf.ThreadPoolExecutor(jobs + 1) as ex:
+        args = ex.submit(build_args)
         for src, rc, out in ex.map(one, zip(srcs, objs)):
             logs.append(f"== {os.path.basename(src)}\n{out}")
             if rc != 0:
                 raise RuntimeError(f"nvcc failed on {src}:\n{out}")
+        args.result()
     with open(os.path.join(build_dir, "ptxas.log"), "w") as f:
         f.write("\n".join(logs))
     tmp = lib + f".tmp{os.getpid()}"

@@ -280,25 +280,29 @@ def _packed(name):
 
 
 def _args_module():
-    """The CPython module that packs the views in C, or None where it was not built."""
+    """The module that packs the views in C++, or None where it was not built for this torch."""
     from importlib.machinery import ExtensionFileLoader
     from importlib.util import module_from_spec, spec_from_file_location
 
-    path = os.path.join(_HERE, "_build", "fa8_args.so")
+    path = os.path.join(_HERE, "_build", f"fa8_args-{torch.__version__}.so")
     if not os.path.exists(path):
         return None
-    module = module_from_spec(spec_from_file_location("fa8_args", path, loader=ExtensionFileLoader("fa8_args", path)))
-    module.set_dtypes(list(_DTYPES.items()))
-    return module
+    return module_from_spec(spec_from_file_location("fa8_args", path, loader=ExtensionFileLoader("fa8_args", path)))
 
 
-_entries = {}
+_entries = {}  # what the calls below use, by name; "": the module
+
+
+def _module():
+    if "" not in _entries:
+        _entries[""] = _args_module()
+    return _entries[""]
 
 
 def _entry(name):
     fn = _entries.get(name)
     if fn is None:
-        module = _args_module()
+        module = _module()
         if module is None:
             fn = _packed(name)
         else:
@@ -307,6 +311,22 @@ def _entry(name):
             fn = functools.partial(getattr(module, name), ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value)
         _entries[name] = fn
     return fn
+
+
+def _empty(q, dtype, drop, *dims):
+    """A new tensor beside q, of its shape with the last ``drop`` dims replaced."""
+    module = _module()
+    if module is None or dtype not in _DTYPES:
+        return torch.empty((*q.shape[:-drop], *dims), dtype=dtype, device=q.device)
+    return module.empty(q, _DTYPES[dtype], drop, *dims)
+
+
+def _empty_lse(q):
+    module = _module()
+    if module is not None:
+        return module.empty_lse(q)
+    shape = (q.shape[0], q.shape[2], q.shape[1]) if q.dim() == 4 else (q.shape[1], q.shape[0])
+    return torch.empty(shape, dtype=torch.float32, device=q.device)
 
 
 def _call(name, device, stream, *args):
@@ -342,7 +362,7 @@ def rope_append(q, k, v, inv_freq, *, k_out, v_out, q_out=None, positions=None, 
     """Rotates Q and K, rounds Q, K and V to E4M3, appends K and V to k_out / v_out (dense,
     varlen or paged, as in ``fwd``) and returns E4M3 Q."""
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=torch.float8_e4m3fn, device=q.device)
+        q_out = _empty(q, torch.float8_e4m3fn, 1, q.shape[-1])
     _call("fa8_rope_append", q.device, stream, q, k, v, inv_freq, positions, int(bool(interleaved)),
           int(rotary_offset), float(rot_scale), descale_q, descale_k, descale_v, q_out, k_out, v_out, cu_seqlens_q,
           cu_seqlens_k, block_table, int(page_size))
@@ -367,7 +387,7 @@ def select_pages(q, bounds, top_k, *, cu_seqlens_k, block_table, page_size, cu_s
     """For every token and kv-head the top_k pages by bounded score: int32 (.., Hkv, top_k),
     ascending, -1 behind the last."""
     if pages is None:
-        pages = torch.empty((*q.shape[:-2], bounds.shape[1], int(top_k)), dtype=torch.int32, device=q.device)
+        pages = _empty(q, torch.int32, 2, bounds.shape[1], int(top_k))
     elif pages.shape[-1] != top_k:
         raise ValueError("pages must hold top_k entries")
     _call("fa8_select_pages", q.device, stream, q, bounds, pages, cu_seqlens_q, cu_seqlens_k, block_table,
@@ -380,10 +400,9 @@ def fwd_pages(q, k, v, pages, *, cu_seqlens_k, block_table, page_size, descale_q
               out_dtype=torch.bfloat16, return_lse=True, stream=None):
     """Attention over the listed pages of a paged cache; returns (out, lse) as ``fwd`` does."""
     if out is None:
-        out = torch.empty((*q.shape[:-1], v.shape[-1]), dtype=out_dtype, device=q.device)
+        out = _empty(q, out_dtype, 1, v.shape[-1])
     if lse is None and return_lse:
-        shape = (q.shape[0], q.shape[2], q.shape[1]) if q.dim() == 4 else (q.shape[1], q.shape[0])
-        lse = torch.empty(shape, dtype=torch.float32, device=q.device)
+        lse = _empty_lse(q)
     _call("fa8_fwd_pages", q.device, stream, q, k, v, pages, descale_q, descale_k, descale_v, out, lse, cu_seqlens_q,
           cu_seqlens_k, block_table, int(page_size), int(bool(causal)), sink, float(softmax_scale))
     return out, lse
