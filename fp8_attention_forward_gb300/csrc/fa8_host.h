@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <mutex>
 
 #include "fa8.h"
 
@@ -28,15 +29,17 @@ struct DeviceState {
 fa8_status device_state(DeviceState **out);
 
 // Opts a kernel in to `bytes` of dynamic shared memory on a device, once per size: what each device has
-// been given for this kernel so far.
+// been given for this kernel so far.  Setting is under a lock: a smaller size must not land after a larger.
 struct SmemOptIn {
     std::atomic<int> given[64] = {};
+    std::mutex mu;
     template <typename K>
     cudaError_t operator()(K *kernel, int bytes, int ordinal) {
+        if (given[ordinal].load(std::memory_order_acquire) >= bytes) return cudaSuccess;
+        std::lock_guard<std::mutex> lock(mu);
         if (given[ordinal].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        int had = given[ordinal].load(std::memory_order_relaxed);
-        while (e == cudaSuccess && had < bytes && !given[ordinal].compare_exchange_weak(had, bytes)) {}
+        if (e == cudaSuccess) given[ordinal].store(bytes, std::memory_order_release);
         return e;
     }
 };

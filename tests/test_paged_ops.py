@@ -2,6 +2,8 @@
 nothing to do, the rotary frequencies, and the 64-bit forms that the GPU tests hold the kernels
 to."""
 import math
+import os
+import subprocess
 
 import pytest
 import torch
@@ -264,3 +266,39 @@ def test_views_refuse_what_is_no_tensor(entries):
         status(fa8_bounds, BOUNDS, dict(cu_seqlens_k="cu"))
     with pytest.raises(OverflowError):
         fa8._entry("fa8_page_bounds")(BOUNDS["k"], BOUNDS["bounds"], None, None, None, 2 ** 70, 0, 0)
+
+
+OPT_IN = r"""
+#include <cstdio>
+#include <thread>
+#include <chrono>
+#include <unistd.h>
+#include "fa8_host.h"
+static std::atomic<int> limit{0};
+extern "C" cudaError_t cudaFuncSetAttribute(const void *, cudaFuncAttribute, int bytes) {
+    usleep(bytes < 1000 ? 60000 : 10000);  // the smaller size takes longer
+    limit = bytes;
+    return cudaSuccess;
+}
+static void kernel() {}
+int main() {
+    static fa8::host::SmemOptIn opt_in;
+    std::thread small([] { opt_in(kernel, 500, 0); });
+    usleep(20000);
+    std::thread large([] { opt_in(kernel, 90000, 0); });
+    small.join(), large.join();
+    opt_in(kernel, 80000, 0);
+    printf("%d", limit.load());
+}
+"""
+
+
+def test_two_threads_opt_in_to_the_larger_shared_memory(tmp_path):
+    """A smaller size that is set late must not take back a larger one."""
+    src, exe = tmp_path / "opt_in.cpp", tmp_path / "opt_in"
+    src.write_text(OPT_IN)
+    cuda = os.path.join(os.path.dirname(os.path.realpath(build.nvcc())), "..", "include")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-pthread", "-I", cuda, "-I", build.CSRC, "-I",
+                    os.path.join(build.ROOT, "include"), str(src), "-o", str(exe)], check=True, capture_output=True)
+    out = subprocess.run([str(exe)], check=True, capture_output=True, text=True, timeout=60).stdout
+    assert int(out) == 90000
