@@ -280,14 +280,14 @@ extern "C" cudaError_t cudaFuncSetAttribute(const void *, cudaFuncAttribute, int
     limit = bytes;
     return cudaSuccess;
 }
-static void kernel() {}
+static int kernel;
 int main() {
     static fa8::host::SmemOptIn opt_in;
-    std::thread small([] { opt_in(kernel, 500, 0); });
+    std::thread small([] { opt_in(&kernel, 500, 0); });
     usleep(20000);
-    std::thread large([] { opt_in(kernel, 90000, 0); });
+    std::thread large([] { opt_in(&kernel, 90000, 0); });
     small.join(), large.join();
-    opt_in(kernel, 80000, 0);
+    opt_in(&kernel, 80000, 0);
     printf("%d", limit.load());
 }
 """
