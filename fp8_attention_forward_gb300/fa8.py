@@ -313,6 +313,15 @@ def _entry(name):
     return fn
 
 
+def _beside(stream, make, *args):
+    """make(*args), on ``stream`` where one is given: memory that work queued on the current stream may
+    still use must not reach a kernel that does not wait for that work."""
+    if stream is None:
+        return make(*args)
+    with torch.cuda.stream(stream):
+        return make(*args)
+
+
 def _empty(q, dtype, drop, *dims):
     """A new tensor beside q, of its shape with the last ``drop`` dims replaced."""
     module = _module()
@@ -327,6 +336,11 @@ def _empty_lse(q):
         return module.empty_lse(q)
     shape = (q.shape[0], q.shape[2], q.shape[1]) if q.dim() == 4 else (q.shape[1], q.shape[0])
     return torch.empty(shape, dtype=torch.float32, device=q.device)
+
+
+def _zero_bounds(k):
+    return torch.zeros((k.shape[0], k.shape[2], 2, k.shape[3]), dtype=torch.uint8,
+                       device=k.device).view(torch.float8_e4m3fn)
 
 
 def _call(name, device, stream, *args):
@@ -362,7 +376,7 @@ def rope_append(q, k, v, inv_freq, *, k_out, v_out, q_out=None, positions=None, 
     """Rotates Q and K, rounds Q, K and V to E4M3, appends K and V to k_out / v_out (dense,
     varlen or paged, as in ``fwd``) and returns E4M3 Q."""
     if q_out is None:
-        q_out = _empty(q, torch.float8_e4m3fn, 1, q.shape[-1])
+        q_out = _beside(stream, _empty, q, torch.float8_e4m3fn, 1, q.shape[-1])
     _call("fa8_rope_append", q.device, stream, q, k, v, inv_freq, positions, int(bool(interleaved)),
           int(rotary_offset), float(rot_scale), descale_q, descale_k, descale_v, q_out, k_out, v_out, cu_seqlens_q,
           cu_seqlens_k, block_table, int(page_size))
@@ -375,8 +389,7 @@ def page_bounds(k, bounds=None, *, cu_seqlens_k, block_table, page_size, cu_seql
     request (cu_seqlens_q: its new tokens; neither: all pages).  Without ``bounds`` a zeroed
     (num_pages, Hkv, 2, D) tensor is made."""
     if bounds is None:
-        bounds = torch.zeros((k.shape[0], k.shape[2], 2, k.shape[3]), dtype=torch.uint8,
-                             device=k.device).view(torch.float8_e4m3fn)
+        bounds = _beside(stream, _zero_bounds, k)
     _call("fa8_page_bounds", k.device, stream, k, bounds, cu_seqlens_q, cu_seqlens_k, block_table, int(page_size),
           int(new_tokens))
     return bounds
@@ -387,7 +400,7 @@ def select_pages(q, bounds, top_k, *, cu_seqlens_k, block_table, page_size, cu_s
     """For every token and kv-head the top_k pages by bounded score: int32 (.., Hkv, top_k),
     ascending, -1 behind the last."""
     if pages is None:
-        pages = _empty(q, torch.int32, 2, bounds.shape[1], int(top_k))
+        pages = _beside(stream, _empty, q, torch.int32, 2, bounds.shape[1], int(top_k))
     elif pages.shape[-1] != top_k:
         raise ValueError("pages must hold top_k entries")
     _call("fa8_select_pages", q.device, stream, q, bounds, pages, cu_seqlens_q, cu_seqlens_k, block_table,
@@ -400,9 +413,9 @@ def fwd_pages(q, k, v, pages, *, cu_seqlens_k, block_table, page_size, descale_q
               out_dtype=torch.bfloat16, return_lse=True, stream=None):
     """Attention over the listed pages of a paged cache; returns (out, lse) as ``fwd`` does."""
     if out is None:
-        out = _empty(q, out_dtype, 1, v.shape[-1])
+        out = _beside(stream, _empty, q, out_dtype, 1, v.shape[-1])
     if lse is None and return_lse:
-        lse = _empty_lse(q)
+        lse = _beside(stream, _empty_lse, q)
     _call("fa8_fwd_pages", q.device, stream, q, k, v, pages, descale_q, descale_k, descale_v, out, lse, cu_seqlens_q,
           cu_seqlens_k, block_table, int(page_size), int(bool(causal)), sink, float(softmax_scale))
     return out, lse

@@ -564,6 +564,41 @@ def test_bad_table_entries_are_reported():
 
 
 @pytest.mark.parametrize("python", [False, True])
+def test_outputs_made_for_another_stream(python, monkeypatch):
+    """With stream= the outputs that a call makes must not share memory with work that the current stream
+    has still to run, and page_bounds' zeros must come before its kernel."""
+    monkeypatch.setattr(fa8, "_entries", {})
+    if python:
+        monkeypatch.setattr(fa8, "_args_module", lambda: None)
+    p = Problem([640], [2], Hq=8, Hkv=2, D=128, ps=16, seed=46)
+    q, k, v = p.q.cuda(), p.k.cuda(), p.v.cuda()
+    w = fa8.rope_inv_freq(128, device="cuda")
+    x = [torch.randn((1, 2, h, 128), generator=p.g).cuda().bfloat16() for h in (8, 2, 2)]
+    kw = p.index_args()
+    caches = [[t.clone() for t in (k, v)] for _ in range(2)]
+    side = torch.cuda.Stream()
+
+    def calls(cache, stream):
+        b = fa8.page_bounds(k, stream=stream, **{n: t for n, t in kw.items() if n != "cu_seqlens_q"})
+        lists = fa8.select_pages(q, b, 5, stream=stream, **kw)
+        return (b.view(torch.uint8), lists, *fa8.fwd_pages(q, k, v, lists, stream=stream, **kw),
+                fa8.rope_append(*x, w, k_out=cache[0], v_out=cache[1], stream=stream, **kw).view(torch.uint8))
+
+    want = [t.clone() for t in calls(caches[0], None)]
+    sizes = [t.nbytes for t in want]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)
+    for n in sizes:  # freed blocks that the current stream writes later
+        torch.empty(n, dtype=torch.uint8, device="cuda").fill_(0x55)
+    got = calls(caches[1], side)
+    side.synchronize()
+    kept = [t.clone() for t in got]
+    ok()
+    for a, b, c in zip(got, want, kept):
+        assert torch.equal(a, b) and torch.equal(c, b)
+
+
+@pytest.mark.parametrize("python", [False, True])
 def test_host_tensors_are_refused(python, monkeypatch):
     monkeypatch.setattr(fa8, "_entries", {})
     if python:
