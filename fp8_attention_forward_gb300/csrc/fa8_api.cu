@@ -161,6 +161,12 @@ fa8_status check_payload(const fa8_tensor *t, const char *name) {
     return FA8_SUCCESS;
 }
 
+fa8_status check_written(const fa8_tensor *t, const char *name) {
+    for (int i = 0; i < t->ndim; ++i)
+        if (t->shape[i] > 1 && t->stride[i] == 0) return fail(FA8_ERR_INVALID_ARG, "%s: dim %d is expanded, it is written", name, i);
+    return FA8_SUCCESS;
+}
+
 fa8_status check_descale(const fa8_tensor *t, const char *name, int B, int Hkv, const float **ptr, long long *sb,
                          long long *sh) {
     *ptr = nullptr;

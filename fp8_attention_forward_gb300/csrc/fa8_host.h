@@ -50,6 +50,8 @@ bool supported_dims(int d, int dv);
 fa8_status check_int_vec(const fa8_tensor *t, const char *name, long long n);
 // E4M3 payload: last dim contiguous, other strides positive multiples of 16 bytes, 16-byte base.
 fa8_status check_payload(const fa8_tensor *t, const char *name);
+// A tensor that a call writes: refuses one whose entries share memory (an expanded dim).
+fa8_status check_written(const fa8_tensor *t, const char *name);
 // fp32, 0-d or (B, Hkv); NULL gives a null pointer (1.0).
 fa8_status check_descale(const fa8_tensor *t, const char *name, int B, int Hkv, const float **ptr, long long *sb,
                          long long *sh);

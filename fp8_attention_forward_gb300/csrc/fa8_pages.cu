@@ -862,6 +862,7 @@ fa8_status fa8_page_bounds(const fa8_tensor *k, fa8_tensor *bounds, const fa8_te
     if (D < 16 || D > 256 || D % 16 != 0) return fail(FA8_ERR_UNSUPPORTED, "d = %lld is not a multiple of 16 up to 256", D);
     if (Hkv <= 0 || Hkv > 65536) return fail(FA8_ERR_INVALID_ARG, "k needs kv heads");
     if ((st = check_bounds(bounds, Hkv, D))) return st;
+    if ((st = check_written(bounds, "bounds"))) return st;
     if (bounds->shape[0] != k->shape[0]) return fail(FA8_ERR_INVALID_ARG, "bounds and k must have the same pages");
     if (k->shape[0] > 0 && !k->data) return fail(FA8_ERR_INVALID_ARG, "k has a null data pointer");
     if (!block_table || block_table->ndim != 2) return fail(FA8_ERR_INVALID_ARG, "block_table must be a 2-D int32 tensor");
@@ -925,6 +926,7 @@ fa8_status fa8_select_pages(const fa8_tensor *q, const fa8_tensor *bounds, fa8_t
     if (p.tab.max_pages > fa8::kSelMaxTable)
         return fail(FA8_ERR_UNSUPPORTED, "block_table has %d columns, at most %d are supported", p.tab.max_pages, fa8::kSelMaxTable);
     if ((st = check_page_lists(pages, qs, (int)Hkv, p.o_s, &p.K))) return st;
+    if ((st = check_written(pages, "pages"))) return st;
     if (p.K < 1) return fail(FA8_ERR_INVALID_ARG, "top_k must be at least 1");
     if (causal != 0 && causal != 1) return fail(FA8_ERR_INVALID_ARG, "causal must be 0 or 1");
     if (keep_first < 0 || keep_last < 0 || (long long)keep_first + keep_last > p.K)

@@ -596,6 +596,7 @@ extern "C" fa8_status fa8_fwd_pages(const fa8_tensor *q, const fa8_tensor *k, co
     if (out->shape[nd - 1] != DV) return fail(FA8_ERR_INVALID_ARG, "out last dim must be dv=%d", DV);
     if (out->stride[nd - 1] != 1) return fail(FA8_ERR_INVALID_ARG, "out: last dim must be contiguous");
     if (!aligned16(out->data)) return fail(FA8_ERR_INVALID_ARG, "out must be 16-byte aligned");
+    if ((st = check_written(out, "out"))) return st;
     if (lse) {
         if (lse->dtype != FA8_DTYPE_F32) return fail(FA8_ERR_INVALID_ARG, "lse must be fp32");
         if (qs.cu_q) {
@@ -611,6 +612,7 @@ extern "C" fa8_status fa8_fwd_pages(const fa8_tensor *q, const fa8_tensor *k, co
             p.lse_s[2] = lse->stride[1];
         }
     }
+    if (lse && (st = check_written(lse, "lse"))) return st;
     if ((st = check_descale(descale_q, "descale_q", qs.B, (int)Hkv, &p.dq, &p.dq_s[0], &p.dq_s[1])) ||
         (st = check_descale(descale_k, "descale_k", qs.B, (int)Hkv, &p.dk, &p.dk_s[0], &p.dk_s[1])) ||
         (st = check_descale(descale_v, "descale_v", qs.B, (int)Hkv, &p.dv, &p.dv_s[0], &p.dv_s[1])))

@@ -231,6 +231,17 @@ def test_rotation_keeps_lengths_and_relative_angles():
         assert abs(float(at(5) @ at(9) - at(100) @ at(104))) < 1e-9
 
 
+def test_expanded_outputs_are_refused():
+    """A tensor that a call writes must not have entries that share memory; one that it reads may."""
+    assert status(fa8_bounds, BOUNDS, dict(bounds=e8(1, 2, 2, 128).expand(9, 2, 2, 128))) == BAD
+    assert status(fa8_select, SELECT, dict(bounds=e8(1, 2, 2, 128).expand(9, 2, 2, 128))) == CUDA
+    assert status(fa8_select, SELECT, dict(pages=i32(2, 1, 2, 4).expand(2, 3, 2, 4))) == BAD
+    assert status(fa8_fwd, FWD, dict(pages=i32(2, 1, 2, 4).expand(2, 3, 2, 4))) == CUDA
+    assert status(fa8_fwd, FWD, dict(out=torch.zeros((2, 3, 1, 128), dtype=torch.bfloat16).expand(2, 3, 8, 128))) == BAD
+    assert status(fa8_fwd, FWD, dict(lse=f32(2, 8, 1).expand(2, 8, 3))) == BAD
+    assert "lse" in fa8.lib().fa8_last_error().decode()
+
+
 # ------------------------------------------------------------------ the binding's two ways to pass views
 @pytest.fixture(params=["c", "python"])
 def entries(request, monkeypatch):
