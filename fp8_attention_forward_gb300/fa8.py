@@ -343,20 +343,20 @@ def _zero_bounds(k):
                        device=k.device).view(torch.float8_e4m3fn)
 
 
-def _call(name, device, stream, *args):
-    """One library call on ``device``; tensors are passed as views, the stream goes last."""
-    fn = _entry(name)
-    if device.type != "cuda":
+def _call(name, index, stream, *args):
+    """One library call on CUDA device ``index`` (-1: host tensors); tensors are passed as views, the
+    stream goes last."""
+    fn = _entries.get(name) or _entry(name)
+    if index < 0:
         if torch.cuda.is_available():
             raise ValueError("the tensors must be on a CUDA device")
         status = fn(*args, 0)  # refuses what it would refuse, else says that there is no device
     else:
-        index = device.index
         handle = _raw_stream(index) if stream is None else stream.cuda_stream
         if _current_device() == index:
             status = fn(*args, handle)
         else:
-            with torch.cuda.device(device):
+            with torch.cuda.device(index):
                 status = fn(*args, handle)
     if status:
         _raise(status)
@@ -377,7 +377,7 @@ def rope_append(q, k, v, inv_freq, *, k_out, v_out, q_out=None, positions=None, 
     varlen or paged, as in ``fwd``) and returns E4M3 Q."""
     if q_out is None:
         q_out = _beside(stream, _empty, q, torch.float8_e4m3fn, 1, q.shape[-1])
-    _call("fa8_rope_append", q.device, stream, q, k, v, inv_freq, positions, int(bool(interleaved)),
+    _call("fa8_rope_append", q.get_device(), stream, q, k, v, inv_freq, positions, int(bool(interleaved)),
           int(rotary_offset), float(rot_scale), descale_q, descale_k, descale_v, q_out, k_out, v_out, cu_seqlens_q,
           cu_seqlens_k, block_table, int(page_size))
     return q_out
@@ -390,7 +390,7 @@ def page_bounds(k, bounds=None, *, cu_seqlens_k, block_table, page_size, cu_seql
     (num_pages, Hkv, 2, D) tensor is made."""
     if bounds is None:
         bounds = _beside(stream, _zero_bounds, k)
-    _call("fa8_page_bounds", k.device, stream, k, bounds, cu_seqlens_q, cu_seqlens_k, block_table, int(page_size),
+    _call("fa8_page_bounds", k.get_device(), stream, k, bounds, cu_seqlens_q, cu_seqlens_k, block_table, int(page_size),
           int(new_tokens))
     return bounds
 
@@ -403,7 +403,7 @@ def select_pages(q, bounds, top_k, *, cu_seqlens_k, block_table, page_size, cu_s
         pages = _beside(stream, _empty, q, torch.int32, 2, bounds.shape[1], int(top_k))
     elif pages.shape[-1] != top_k:
         raise ValueError("pages must hold top_k entries")
-    _call("fa8_select_pages", q.device, stream, q, bounds, pages, cu_seqlens_q, cu_seqlens_k, block_table,
+    _call("fa8_select_pages", q.get_device(), stream, q, bounds, pages, cu_seqlens_q, cu_seqlens_k, block_table,
           int(page_size), int(bool(causal)), int(keep_first), int(keep_last))
     return pages
 
@@ -416,7 +416,7 @@ def fwd_pages(q, k, v, pages, *, cu_seqlens_k, block_table, page_size, descale_q
         out = _beside(stream, _empty, q, out_dtype, 1, v.shape[-1])
     if lse is None and return_lse:
         lse = _beside(stream, _empty_lse, q)
-    _call("fa8_fwd_pages", q.device, stream, q, k, v, pages, descale_q, descale_k, descale_v, out, lse, cu_seqlens_q,
+    _call("fa8_fwd_pages", q.get_device(), stream, q, k, v, pages, descale_q, descale_k, descale_v, out, lse, cu_seqlens_q,
           cu_seqlens_k, block_table, int(page_size), int(bool(causal)), sink, float(softmax_scale))
     return out, lse
 
