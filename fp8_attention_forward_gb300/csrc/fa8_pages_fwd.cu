@@ -658,15 +658,15 @@ extern "C" fa8_status fa8_fwd_pages(const fa8_tensor *q, const fa8_tensor *k, co
     p.status = ds->status;
     p.timeout_ns = wait_timeout_ns();
     // Clusters split a list over CTAs while all of them run at once and every warp keeps at least two
-    // chunks; where clusters of eight still leave SMs empty, CTAs of eight warps split it once
-    // more (8 lists of 4096 keys, d = dv = 256: 12.4 us against 16.8 with four warps; 512 lists of 2048
-    // keys, d = dv = 128: 53 against 48.5).
+    // chunks; where clusters of eight still leave a quarter of the SMs empty, CTAs of eight warps, one per
+    // SM, split it once more (8 lists of 4096 keys, d = dv = 256: 12.0 us against 15.5 with four warps; 14
+    // lists 13.0 against 16.9; 16 lists, whose clusters no longer fit at once, 23.8 against 17.9).
     const long long keys = (long long)p.K * page_size;
     const int kc = qs.D + DV <= 256 ? 32 : 16, per_sm = nt == 2 && qs.D + DV > 256 ? 2 : 4;
     p.cluster = 1;
     while (p.cluster < fa8::kPgMaxCluster && tiles * p.cluster * 2 <= (long long)per_sm * ds->sm_count && keys >= 2LL * kc * 4 * p.cluster * 2)
         p.cluster *= 2;
-    const bool wide = p.cluster == fa8::kPgMaxCluster && tiles * p.cluster <= ds->sm_count && keys >= 2LL * kc * 8 * p.cluster;
+    const bool wide = p.cluster == fa8::kPgMaxCluster && tiles * p.cluster * 4 <= 3LL * ds->sm_count && keys >= 2LL * kc * 8 * p.cluster;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
 #define FA8_PAGES(D_, DV_)                                                                               \
     case D_ * 1000 + DV_:                                                                                \
