@@ -44,6 +44,24 @@ struct SmemOptIn {
     }
 };
 
+// Whether a launch in clusters of 16, past the portable 8, fits the device: asked once per kernel, device
+// and shared-memory size.
+struct Cluster16 {
+    std::atomic<int> fits[64] = {}, not_from[64] = {};  // bytes + 1 up to which it fits, from which it does not
+    template <typename K>
+    bool operator()(K *kernel, const cudaLaunchConfig_t &cfg, int ordinal) {
+        const int bytes = (int)cfg.dynamicSmemBytes + 1, no = not_from[ordinal].load(std::memory_order_relaxed);
+        if (fits[ordinal].load(std::memory_order_relaxed) >= bytes) return true;
+        if (no && bytes >= no) return false;
+        int n = 0;
+        const bool ok = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0;
+        if (!ok) cudaGetLastError();  // a refusal is an answer
+        (ok ? fits : not_from)[ordinal].store(bytes, std::memory_order_relaxed);
+        return ok;
+    }
+};
+
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool supported_dims(int d, int dv);
 // A contiguous 1-D int32 tensor of n entries.

@@ -141,7 +141,7 @@ struct SelectParams {
 constexpr int kSelWarps = 4, kSelThreads = kSelWarps * 32;
 constexpr int kSelMaxTable = 16384;  // block_table columns
 constexpr int kSelMaxTable4 = 2048;  // of the kernel that takes four tokens at once
-constexpr int kSelMaxCluster = 8;
+constexpr int kSelMaxCluster = 16;
 constexpr int kSelList = 256;  // undecided pages that are ranked directly
 constexpr int kSelHeld = 16;   // scores that a thread keeps in registers while it chooses
 
@@ -361,7 +361,8 @@ __device__ __forceinline__ unsigned long long exact_key(const uint8_t *src, cons
 // 51; per-lane bulk copies: 65; fragments straight to registers: 73); 512 tokens x 8 heads over 512 pages:
 // 40 us (a token at a time: 164), over 1024 and 2048 pages 70 and 175 us (106 and 282 with 64-bit keys of
 // every page in shared memory and one load at a time behind the held scores); one pair of 2048 pages,
-// d = 256, a cluster of eight CTAs: 14 us (22); one of 16384, d = 128: 87 us, most of it the choice.
+// d = 256, a cluster of 16 CTAs: 12 us (eight: 14, one CTA: 22); 8 of 16384, d = 128: 75 us, most of it
+// the choice.
 template <int D, int NT, int TB>
 __global__ void __launch_bounds__(kSelThreads, D > 128 ? 4 : (TB == 1 && NT == 1 ? 7 : 5)) select_pages_kernel(const __grid_constant__ SelectParams p) {
     using C = SelCfg<D, NT, TB>;
@@ -799,8 +800,9 @@ __global__ void __launch_bounds__(kSelThreads, D > 128 ? 4 : (TB == 1 && NT == 1
 }
 
 template <int D, int NT, int TB>
-cudaError_t launch_select(const SelectParams &p, unsigned int rows, int dev, cudaStream_t s) {
+cudaError_t launch_select(SelectParams &p, unsigned int rows, int dev, cudaStream_t s) {
     static host::SmemOptIn opt_in;
+    static host::Cluster16 cluster16;
     const int smem = SelCfg<D, NT, TB>::smem(p.tab.max_pages);
     const cudaError_t e = opt_in(select_pages_kernel<D, NT, TB>, smem, dev);
     if (e != cudaSuccess) return e;
@@ -815,11 +817,15 @@ cudaError_t launch_select(const SelectParams &p, unsigned int rows, int dev, cud
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = p.cluster > 1 ? 1 : 0;
+    if (p.cluster > 8 && !cluster16(select_pages_kernel<D, NT, TB>, cfg, dev)) {
+        p.cluster = attr[0].val.clusterDim.x = 8;
+        cfg.gridDim = dim3(rows * 8);
+    }
     return cudaLaunchKernelEx(&cfg, select_pages_kernel<D, NT, TB>, p);
 }
 
 template <int D>
-cudaError_t launch_select_dim(const SelectParams &p, unsigned int rows, bool four, int dev, cudaStream_t s) {
+cudaError_t launch_select_dim(SelectParams &p, unsigned int rows, bool four, int dev, cudaStream_t s) {
     if (four) return p.G <= 2 ? launch_select<D, 1, 4>(p, rows, dev, s) : (p.G <= 4 ? launch_select<D, 2, 4>(p, rows, dev, s) : launch_select<D, 4, 4>(p, rows, dev, s));
     return p.G <= 8 ? launch_select<D, 1, 1>(p, rows, dev, s) : launch_select<D, 2, 1>(p, rows, dev, s);
 }
@@ -956,13 +962,15 @@ fa8_status fa8_select_pages(const fa8_tensor *q, const fa8_tensor *bounds, fa8_t
     // Several tokens per request and enough of them to fill the GPU in blocks of four: one pass over
     // the bounds serves four tokens.  Else a token at a time, and where there are few (token, kv-head)
     // pairs a cluster of CTAs shares each pair's pages, 128 or more a CTA, up to the seven CTAs that fit an
-    // SM (512 ragged pairs of up to 2048 pages: 46 us in clusters of two, 55 without).
+    // SM (512 ragged pairs of up to 2048 pages: 46 us in clusters of two, 55 without).  Clusters of 16 only
+    // while every CTA may have an SM (one pair of 2048 pages, d = 256: 12.1 us against 14.3; 64 pairs: 27.7
+    // against 24.2).
     const long long blocks = p.cu_q ? (long long)qs.T / 4 + qs.B : (long long)qs.B * ((qs.Sq + 3) / 4);
     const bool four = p.G <= 8 && (long long)qs.T >= 4LL * qs.B && blocks * Hkv >= 2LL * ds->sm_count &&
                       p.tab.max_pages <= fa8::kSelMaxTable4;
     p.cluster = 1;
     if (!four)
-        while (p.cluster < fa8::kSelMaxCluster && rows * p.cluster * 2 <= 7LL * ds->sm_count && p.tab.max_pages >= 128 * p.cluster * 2)
+        while (p.cluster < fa8::kSelMaxCluster && rows * p.cluster * 2 <= (p.cluster < 8 ? 7LL : 1LL) * ds->sm_count && p.tab.max_pages >= 128 * p.cluster * 2)
             p.cluster *= 2;
     if (blocks * Hkv > 0x7fffffffLL) return fail(FA8_ERR_UNSUPPORTED, "problem too large for the grid");
     const unsigned grid = (unsigned)(four ? blocks * Hkv : rows);
