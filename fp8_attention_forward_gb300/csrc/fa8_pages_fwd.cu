@@ -7,7 +7,7 @@
 //   S^T (16 keys x 8 rows)  = K (M = keys, k = d) . Q^T        f16 MMAs on exactly widened E4M3
 //   O^T (16 dv x 8 rows)   += V^T (M = dv, k = keys) . P^T
 //
-// A warp works alone: it takes every (warps x cluster)-th chunk of 16 or 32 keys of the list, keeps
+// A warp works alone: it takes every (warps x cluster)-th chunk of 16, 32 or 64 keys of the list, keeps
 // its own running maximum, sum and O^T in registers, and has one K and one V buffer that TMA fills
 // (boxes of one head's rows of a page, swizzled): the next K while this chunk goes through softmax and
 // PV, the next V during PV and the next S^T.  V's 16 x 16 byte tiles are transposed as they are loaded.  P is
@@ -70,7 +70,10 @@ constexpr float kPgSlack = 8.f;
 template <int D, int DV, int NT, int PW>
 struct PgCfg {
     static constexpr int ROWS = 8 * NT;
-    static constexpr int MT = D + DV <= 256 ? 2 : 1;  // 16-key tiles per chunk
+    // 16-key tiles per chunk (d = dv = 64, 512 tokens x 8 lists of 2048 keys: 97 us with four, 124 with two;
+    // d = dv = 96: 124 and 146)
+    static constexpr int MT = D + DV <= 192 && NT == 1 ? 4 : (D + DV <= 256 ? 2 : 1);
+    static constexpr int KC_LOG = MT == 4 ? 6 : (MT == 2 ? 5 : 4);
     static constexpr int KC = 16 * MT;                // keys per chunk
     static constexpr int NG = 2 * MT;                 // 8-key groups per chunk
     // rows arrive as blocks of CW bytes, each block KC rows deep with the swizzle of its width (rows of
@@ -232,7 +235,7 @@ __global__ void __launch_bounds__(32 * PW, PgCfg<D, DV, NT, PW>::CTAS) fwd_pages
     };
     // visible keys of 8-key group i (of all lanes)
     auto group_lim = [&](int i) {
-        const int sh = (C::MT == 2 ? 5 : 4) - p.box_shift, b0 = i * 8 >> sh;  // a box is 2^sh keys
+        const int sh = C::KC_LOG - p.box_shift, b0 = i * 8 >> sh;  // a box is 2^sh keys
         return __shfl_sync(0xffffffffu, lim, b0) - (i * 8 - (b0 << sh));
     };
     auto fetch_k = [&]() {
@@ -334,7 +337,9 @@ __global__ void __launch_bounds__(32 * PW, PgCfg<D, DV, NT, PW>::CTAS) fwd_pages
                 }
         }
         const bool partial = !full;
-        const int vlim = partial ? group_lim(lane >> 3) - (lane & 7) : 1;  // visible: above 0 for row `lane`
+        int vlim[(C::KC + 31) / 32];  // above 0 where row 32 i + lane is visible
+#pragma unroll
+        for (int i = 0; i < (C::KC + 31) / 32; ++i) vlim[i] = partial ? group_lim((lane >> 3) + 4 * i) - (lane & 7) : 1;
         const bool more = it + 1 < chunks;
         __syncwarp();  // every lane has read the K buffer
         if (more) {
@@ -395,9 +400,11 @@ __global__ void __launch_bounds__(32 * PW, PgCfg<D, DV, NT, PW>::CTAS) fwd_pages
             break;
         }
         if (partial) {  // rows that are not visible may hold anything: they become zeros
-            if (lane < C::KC && vlim <= 0)
 #pragma unroll
-                for (int d = 0; d < DV; d += 16) st_shared_zero16(vs + C::template at<C::CWV>(lane, d));
+            for (int i = 0; i < (C::KC + 31) / 32; ++i)
+                if (lane + 32 * i < C::KC && vlim[i] <= 0)
+#pragma unroll
+                    for (int d = 0; d < DV; d += 16) st_shared_zero16(vs + C::template at<C::CWV>(lane + 32 * i, d));
             ptx::fence_proxy_async_smem();
             __syncwarp();
         }
@@ -524,7 +531,8 @@ fa8_status launch_pages(PagesParams &p, const fa8_tensor *k, const fa8_tensor *v
     using C = PgCfg<D, DV, NT, PW>;
     const int ps = p.tab.page_size;
     p.box = std::gcd(ps, C::KC);
-    p.box_shift = C::KC / p.box == 1 ? 0 : (C::KC / p.box == 2 ? 1 : 2);
+    p.box_shift = 0;
+    while (p.box << p.box_shift < C::KC) ++p.box_shift;
     p.box_magic = ps > p.box ? (unsigned)((0x100000000ull + ps / p.box - 1) / (ps / p.box)) : 0u;
     CUtensorMap tk, tv;
     memset(&tk, 0, sizeof(tk));
@@ -658,7 +666,7 @@ extern "C" fa8_status fa8_fwd_pages(const fa8_tensor *q, const fa8_tensor *k, co
     p.status = ds->status;
     p.timeout_ns = wait_timeout_ns();
     // Clusters split a list over CTAs while all of them run at once and every warp keeps at least two
-    // chunks; where clusters of eight still leave a quarter of the SMs empty, CTAs of eight warps, one per
+    // chunks (one of 64 keys); where clusters of eight still leave a quarter of the SMs empty, CTAs of eight warps, one per
     // SM, split it once more (8 lists of 4096 keys, d = dv = 256: 12.0 us against 15.5 with four warps; 14
     // lists 13.0 against 16.9; 16 lists, whose clusters no longer fit at once, 23.8 against 17.9).
     const long long keys = (long long)p.K * page_size;
