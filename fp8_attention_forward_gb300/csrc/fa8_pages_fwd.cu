@@ -16,13 +16,12 @@
 // cluster through distributed shared memory, merge by their maxima: no workspace, no second kernel.
 //
 // Measured (d = dv = 128, 64 x 8 lists of 2048 keys, 267 MB): 48 us, 5.6 TB/s, 0.82 of the copy rate.
-// Many tokens of one request (512 x 8 lists of 2048 keys, 2.1 GB through L2): 168 us, 12.8 TB/s; shared
-// memory is at 70 %, the ALU pipe, which widens E4M3 to f16, at 54 %, issue slots at 56 %.  The copies and the
-// softmax without the products: 122 us.  Tried: V's fragments by 16-byte loads whose bytes are paired by
+// Many tokens of one request (512 x 8 lists of 2048 keys, 2.1 GB through L2): 157 us, 13.6 TB/s; in chunks
+// of 32 keys 168 us, with shared memory at 70 %, the ALU pipe, which widens E4M3 to f16, at 54 % and issue
+// slots at 56 %; the copies and the softmax without the products, 122 us.  Tried: V's fragments by 16-byte loads whose bytes are paired by
 // permutes, 52 and 210 us; both operands straight to registers, 63 and 303; by 16-byte asynchronous copies,
 // 61 and 258 (L2 is asked for every sector twice); QK by the E4M3 warp MMA, 3 % slower (it widens too); a
-// second K or V buffer, 3 to 5 % slower; chunks of 64 keys with three CTAs per SM, 61 and 162 where 32 keys
-// took 51 and 172.
+// second K or V buffer, 3 to 5 % slower.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -67,12 +66,13 @@ struct PagesParams {
 constexpr int kPgMaxCluster = 8;
 constexpr float kPgSlack = 8.f;
 
-template <int D, int DV, int NT, int PW>
+// MANY: many tokens per request, whose lists L2 serves: longer chunks, fewer CTAs.
+template <int D, int DV, int NT, int PW, bool MANY>
 struct PgCfg {
     static constexpr int ROWS = 8 * NT;
     // 16-key tiles per chunk (d = dv = 64, 512 tokens x 8 lists of 2048 keys: 97 us with four, 124 with two;
     // d = dv = 96: 124 and 146)
-    static constexpr int MT = D + DV <= 192 && NT == 1 ? 4 : (D + DV <= 256 ? 2 : 1);
+    static constexpr int MT = (D + DV <= 192 && NT == 1) || MANY ? 4 : (D + DV <= 256 ? 2 : 1);
     static constexpr int KC_LOG = MT == 4 ? 6 : (MT == 2 ? 5 : 4);
     static constexpr int KC = 16 * MT;                // keys per chunk
     static constexpr int NG = 2 * MT;                 // 8-key groups per chunk
@@ -97,7 +97,7 @@ struct PgCfg {
     // CTAs per SM that registers are cut to: four of four warps, but where 16 rows of wide heads would
     // spill (d = dv = 192, 60 lists of 960 keys x 8 heads: 37.6 us against 54.7 uncut; 16 rows, d = dv =
     // 128: 24.8 against 31.7; 16 rows, d = dv = 256: 52.9 cut against 32)
-    static constexpr int CTAS = PW > 4 ? 1 : (NT == 2 && D + DV > 256 ? 2 : 4);
+    static constexpr int CTAS = PW > 4 ? 1 : (NT == 2 && D + DV > 256 ? 2 : (MANY ? 3 : 4));
     // first of the VK channels that lane column c takes with fragment load v (rows of 128 bytes: the
     // pieces 2c and 2c + 1 of a block, so that two rows' lanes meet different banks)
     static __device__ __forceinline__ int k_dim(int v, int c) {
@@ -111,10 +111,10 @@ struct PgCfg {
     }
 };
 
-template <int D, int DV, int NT, int PW>
-__global__ void __launch_bounds__(32 * PW, PgCfg<D, DV, NT, PW>::CTAS) fwd_pages_kernel(
+template <int D, int DV, int NT, int PW, bool MANY>
+__global__ void __launch_bounds__(32 * PW, PgCfg<D, DV, NT, PW, MANY>::CTAS) fwd_pages_kernel(
     const __grid_constant__ PagesParams p, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
-    using C = PgCfg<D, DV, NT, PW>;
+    using C = PgCfg<D, DV, NT, PW, MANY>;
     constexpr int kThreads = 32 * PW;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -525,10 +525,10 @@ __global__ void __launch_bounds__(32 * PW, PgCfg<D, DV, NT, PW>::CTAS) fwd_pages
     if (CS > 1) cluster_sync();  // no CTA leaves while its shared memory is still read
 }
 
-template <int D, int DV, int NT, int PW>
+template <int D, int DV, int NT, int PW, bool MANY = false>
 fa8_status launch_pages(PagesParams &p, const fa8_tensor *k, const fa8_tensor *v, unsigned int tiles, int dev, cudaStream_t s) {
     static host::SmemOptIn opt_in;
-    using C = PgCfg<D, DV, NT, PW>;
+    using C = PgCfg<D, DV, NT, PW, MANY>;
     const int ps = p.tab.page_size;
     p.box = std::gcd(ps, C::KC);
     p.box_shift = 0;
@@ -542,7 +542,7 @@ fa8_status launch_pages(PagesParams &p, const fa8_tensor *k, const fa8_tensor *v
         if ((st = host::encode_kv(&tk, k, C::CW, p.box)) || (st = host::encode_kv(&tv, v, C::CWV, p.box))) return st;
     }
     const int smem = C::smem(p.K);
-    cudaError_t e = opt_in(fwd_pages_kernel<D, DV, NT, PW>, smem, dev);
+    cudaError_t e = opt_in(fwd_pages_kernel<D, DV, NT, PW, MANY>, smem, dev);
     if (e != cudaSuccess) return host::cuda_fail(e, "page attention shared memory");
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(tiles * p.cluster);
@@ -555,7 +555,7 @@ fa8_status launch_pages(PagesParams &p, const fa8_tensor *k, const fa8_tensor *v
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, fwd_pages_kernel<D, DV, NT, PW>, p, tk, tv);
+    e = cudaLaunchKernelEx(&cfg, fwd_pages_kernel<D, DV, NT, PW, MANY>, p, tk, tv);
     return e == cudaSuccess ? FA8_SUCCESS : host::cuda_fail(e, "page attention kernel launch");
 }
 
@@ -682,6 +682,11 @@ extern "C" fa8_status fa8_fwd_pages(const fa8_tensor *q, const fa8_tensor *k, co
                                : fa8::launch_pages<D_, DV_, 1, 4>(p, k, v, (unsigned)tiles, ds->ordinal, s))          \
                        : (wide ? fa8::launch_pages<D_, DV_, 2, 8>(p, k, v, (unsigned)tiles, ds->ordinal, s)           \
                                : fa8::launch_pages<D_, DV_, 2, 4>(p, k, v, (unsigned)tiles, ds->ordinal, s));
+    // Chunks of 64 keys for d = dv = 128 where L2 serves the lists of many tokens of a request (512 tokens x 8
+    // lists of 2048 keys: 157 us against 168), not where HBM does (64 x 8 lists of one token each: 61
+    // against 51: fewer copies in flight).
+    if (qs.D == 128 && DV == 128 && nt == 1 && p.cluster == 1 && (long long)qs.T >= 16LL * qs.B)
+        return fa8::launch_pages<128, 128, 1, 4, true>(p, k, v, (unsigned)tiles, ds->ordinal, s);
     switch (qs.D * 1000 + DV) {
         FA8_PAGES(64, 64)
         FA8_PAGES(96, 96)
