@@ -18,10 +18,10 @@
 // Measured (d = dv = 128, 64 x 8 lists of 2048 keys, 267 MB): 48 us, 5.6 TB/s, 0.82 of the copy rate.
 // Many tokens of one request (512 x 8 lists of 2048 keys, 2.1 GB through L2): 157 us, 13.6 TB/s; in chunks
 // of 32 keys 168 us, with shared memory at 70 %, the ALU pipe, which widens E4M3 to f16, at 54 % and issue
-// slots at 56 %; the copies and the softmax without the products, 122 us.  Tried: V's fragments by 16-byte loads whose bytes are paired by
-// permutes, 52 and 210 us; both operands straight to registers, 63 and 303; by 16-byte asynchronous copies,
-// 61 and 258 (L2 is asked for every sector twice); QK by the E4M3 warp MMA, 3 % slower (it widens too); a
-// second K or V buffer, 3 to 5 % slower.
+// slots at 56 %; the copies and the softmax without the products, 122 us.  Tried: V's fragments by 16-byte
+// loads whose bytes are paired by permutes, 52 and 210 us; both operands straight to registers, 63 and 303;
+// by 16-byte asynchronous copies, 61 and 258 (L2 is asked for every sector twice); QK by the E4M3 warp MMA,
+// 3 % slower (it widens too); a second K or V buffer, 3 to 5 % slower.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
