@@ -45,9 +45,11 @@ __device__ __forceinline__ uint32_t hmax2_nan(uint32_t a, uint32_t b) {
 // A warp takes 128 bytes (eight 16-channel pieces, a whole line of every row) of one page: lane l holds
 // piece l mod 8 of rows l / 8, l / 8 + 4, ..; then the four row parts meet by shuffles.  E4M3 -> f16 is
 // exact, so the packed f16 minimum and maximum (NaN-propagating) are, and so is the way back.
-// Bound: HBM, one read of the pages' K.  Measured, 2048 pages of 64 keys x 8 heads of 128 (137 MB): 26 us,
-// 5.2 TB/s, 0.77 of the copy rate (a thread per 16 channels walking all rows: 32 us); the one new page of
-// 64 requests: 3.0 us (4.6).
+// Bound: HBM, one read of the pages' K.  Measured, 2048 pages of 64 keys x 8 heads of 128 (137 MB): 25 us,
+// 5.4 TB/s, 0.80 of the copy rate (a thread per 16 channels walking all rows: 32 us); as many keys in pages
+// of 16 and 8, where joining the row parts weighs more: 41 and 58 us (eight loads a lane whatever the page:
+// 45 and 80); the one new page of 64 requests: 2.9 us (4.6).
+template <int U>
 __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const __grid_constant__ BoundsParams p) {
     const int b = blockIdx.x / p.blocks_per_req;
     const int lane = threadIdx.x & 31;
@@ -82,12 +84,10 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const __gri
     const int per = p.D >> 4, h = on ? chunk / per : 0, c = on ? chunk - h * per : 0;
     const uint8_t *src = p.k + (long long)page * p.k_s[0] + (long long)h * p.k_s[2] + 16 * c;
     uint32_t lo[8], hi[8];
-    {  // every part starts from row 0: a part may have no row of its own
-        const Bytes<16> v = ld_stream(src);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) e4m3x4_to_h2(v.w[i], lo[2 * i], lo[2 * i + 1]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) hi[i] = lo[i];
+    for (int i = 0; i < 8; ++i) {  // infinities: a part may have no row of its own
+        lo[i] = 0x7C007C00u;
+        hi[i] = 0xFC00FC00u;
     }
     auto take = [&](const Bytes<16> &v) {
 #pragma unroll
@@ -100,12 +100,12 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const __gri
             hi[2 * i + 1] = hmax2_nan(hi[2 * i + 1], d);
         }
     };
-    for (int r = part; r < rows; r += 32) {  // eight loads in flight
-        Bytes<16> v[8];
+    for (int r = part; r < rows; r += 4 * U) {  // U loads in flight
+        Bytes<16> v[U];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) v[u] = ld_stream(src + (long long)min(r + 4 * u, rows - 1) * p.k_s[1]);
+        for (int u = 0; u < U; ++u) v[u] = ld_stream(src + (long long)min(r + 4 * u, rows - 1) * p.k_s[1]);
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
+        for (int u = 0; u < U; ++u)
             if (r + 4 * u < rows) take(v[u]);
     }
 #pragma unroll
@@ -904,7 +904,9 @@ fa8_status fa8_page_bounds(const fa8_tensor *k, fa8_tensor *bounds, const fa8_te
     DeviceState *ds = nullptr;
     if ((st = device_state(&ds))) return st;
     p.status = ds->status;
-    fa8::page_bounds_kernel<<<(unsigned)(per_req * B), fa8::kBoundsThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    // as many loads in flight as a lane group has rows of a page, eight at most
+    auto kernel = page_size <= 8 ? fa8::page_bounds_kernel<2> : (page_size <= 16 ? fa8::page_bounds_kernel<4> : fa8::page_bounds_kernel<8>);
+    kernel<<<(unsigned)(per_req * B), fa8::kBoundsThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "page bounds kernel launch");
     return FA8_SUCCESS;
