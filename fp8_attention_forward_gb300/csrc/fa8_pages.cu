@@ -47,7 +47,7 @@ __device__ __forceinline__ uint32_t hmax2_nan(uint32_t a, uint32_t b) {
 // exact, so the packed f16 minimum and maximum (NaN-propagating) are, and so is the way back.
 // Bound: HBM, one read of the pages' K.  Measured, 2048 pages of 64 keys x 8 heads of 128 (137 MB): 25 us,
 // 5.4 TB/s, 0.80 of the copy rate (a thread per 16 channels walking all rows: 32 us); as many keys in pages
-// of 16 and 8, where joining the row parts weighs more: 41 and 58 us (eight loads a lane whatever the page:
+// of 16 and 8, where joining the row parts weighs more: 41 and 57 us (eight loads a lane whatever the page:
 // 45 and 80); the one new page of 64 requests: 2.9 us (4.6).
 template <int U>
 __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const __grid_constant__ BoundsParams p) {
@@ -108,20 +108,23 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const __gri
         for (int u = 0; u < U; ++u)
             if (r + 4 * u < rows) take(v[u]);
     }
+    // the four parts meet and divide the result: parts 0 and 1 keep the minima, 2 and 3 the maxima (as minima
+    // of the negatives), then even parts the lower half of the channels, odd ones the upper
+    uint32_t m[8], x[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t neg = hi[i] ^ 0x80008000u;
+        m[i] = hmin2_nan(part & 2 ? neg : lo[i], __shfl_xor_sync(0xffffffffu, part & 2 ? lo[i] : neg, 16));
+    }
 #pragma unroll
-        for (int o = 8; o < 32; o <<= 1) {
-            lo[i] = hmin2_nan(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o));
-            hi[i] = hmax2_nan(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o));
-        }
-    if (part > 1 || !on) return;
-    uint32_t w[4];  // part 0 writes the minima, part 1 the maxima
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w[i] = ptx::prmt_lo16(ptx::cvt_e4m3x2_h2(part ? hi[2 * i] : lo[2 * i]), ptx::cvt_e4m3x2_h2(part ? hi[2 * i + 1] : lo[2 * i + 1]));
-    uint8_t *dst = p.bounds + (long long)page * p.b_s[0] + (long long)h * p.b_s[1] + 16 * c + part * p.D;
-    *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int i = 0; i < 4; ++i) {
+        x[i] = hmin2_nan(part & 1 ? m[4 + i] : m[i], __shfl_xor_sync(0xffffffffu, part & 1 ? m[i] : m[4 + i], 8));
+        if (part & 2) x[i] ^= 0x80008000u;
+    }
+    if (!on) return;
+    uint8_t *dst = p.bounds + (long long)page * p.b_s[0] + (long long)h * p.b_s[1] + 16 * c + (part >> 1) * p.D + 8 * (part & 1);
+    *reinterpret_cast<uint2 *>(dst) = make_uint2(ptx::prmt_lo16(ptx::cvt_e4m3x2_h2(x[0]), ptx::cvt_e4m3x2_h2(x[1])),
+                                                 ptx::prmt_lo16(ptx::cvt_e4m3x2_h2(x[2]), ptx::cvt_e4m3x2_h2(x[3])));
 }
 
 // ------------------------------------------------------------------------------ page selection
