@@ -566,8 +566,7 @@ __global__ void __launch_bounds__(kSelThreads, D > 128 ? 4 : (TB == 1 && NT == 1
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {  // |x| + |y| bounds both, and an addition is cheaper than a maximum
                         const __half2 z = __hadd2(__habs2(*reinterpret_cast<__half2 *>(&a[2 * e])), __habs2(*reinterpret_cast<__half2 *>(&a[2 * e + 1])));
-                        const __half2 m = __hmax2(z, *reinterpret_cast<__half2 *>(&kmax2[2 * (s & 1) + e]));
-                        kmax2[2 * (s & 1) + e] = *reinterpret_cast<const uint32_t *>(&m);
+                        kmax2[2 * (s & 1) + e] = hmax2_nan(*reinterpret_cast<const uint32_t *>(&z), kmax2[2 * (s & 1) + e]);
                     }
                 }
             }
@@ -622,8 +621,9 @@ __global__ void __launch_bounds__(kSelThreads, D > 128 ? 4 : (TB == 1 && NT == 1
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const __half2 x = *reinterpret_cast<__half2 *>(&kmax2[e]);
-            k = fmaxf(k, fmaxf(__low2float(x), __high2float(x)));
+            k = max_nan(k, max_nan(__low2float(x), __high2float(x)));
         }
+        if (k != k) k = 448.f;  // a NaN may have hidden the page beside it: the largest E4M3 value
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) k = fmaxf(k, __shfl_xor_sync(0xffffffffu, k, o));
 #pragma unroll
