@@ -351,21 +351,24 @@ __device__ __forceinline__ unsigned long long exact_key(const uint8_t *src, cons
 // arrive by asynchronous copies, 16 pages a buffer.  With few rows a cluster of CTAs
 // shares a token's pages and rank 0 chooses.
 //
-// Exact choice from fp32 scores: E4M3 products are exact, an MMA adds 16 of them to the running
-// sum, and what it drops is below 2^-23 of the largest magnitude passing through (fp32's 24 bits; a
-// probe over five kinds of data finds a quarter of that at most), itself at most
-// A = max_h |q_h|_1 * max|bound| (of which the kernel takes a bound).  So a score is off by at most
-// eps = (2 D / 16) 2^-23 A over its MMA steps.  With t the k-th largest fp32 score, pages above t + 2 eps are in and pages below t - 2 eps out whatever the true scores; the few between are scored again
-// in 64-bit integers (E4M3 is a whole number of 2^-9) and ranked by (score, lower index).
+// Exact choice from fp32 scores: E4M3 products are exact, and an MMA adds 16 of them to the running sum.  It cuts
+// each of these 17 addends below 2^-25 of the largest one's leading bit and the result to fp32's 24 bits (what
+// this GPU does, held by a probe: at most half of the bound over 87 kinds of data, among them equal products of
+// one sign behind a large one, whose cut parts add up).  No magnitude that passes through is above
+// A = max_h |q_h|_1 * max|bound|, and of a page's 2 D products at most D are not zero, as a q_c has one sign.  So
+// with 2 D / 16 MMAs a score is off by at most eps = (D + 5 * 2 D / 16) 2^-25 A.  With t the k-th largest fp32
+// score, pages above t + 2 eps are in and pages below t - 2 eps out whatever the true scores; the few between
+// are scored again in 64-bit integers (E4M3 is a whole number of 2^-9) and ranked by (score, lower index).
 //
 // Bound: for many pages HBM (2 D bytes per page and kv-head) and the ALU pipe that widens them; else the
 // chain of a CTA: 4 us to its first score, 5 us to choose.  Measured, d = 128: 64 x 8 pairs of 64 .. 2048
-// pages (140 MB): 47 us, 3.0 TB/s, 0.44 of the copy rate (a token's pages in one CTA with two buffers:
+// pages (140 MB): 48 us, 2.9 TB/s, 0.43 of the copy rate (a token's pages in one CTA with two buffers:
 // 51; per-lane bulk copies: 65; fragments straight to registers: 73); 512 tokens x 8 heads over 512 pages:
-// 40 us (a token at a time: 164), over 1024 and 2048 pages 70 and 175 us (106 and 282 with 64-bit keys of
-// every page in shared memory and one load at a time behind the held scores); one pair of 2048 pages,
-// d = 256, a cluster of 16 CTAs: 12 us (eight: 14, one CTA: 22); 8 of 16384, d = 128: 75 us, most of it
-// the choice.
+// 43 us (a token at a time: 164), over 2048 pages 174 us (282 with 64-bit keys of every page in shared memory
+// and one load at a time behind the held scores); one pair of 2048 pages, d = 256, a cluster of 16 CTAs: 13 us
+// (one CTA: 22); 8 of 16384, d = 128: 76 us, most of it the choice.  With an eps that counts on fp32's 24 bits
+// alone, (D + 2 * 2 D / 16) 2^-23 A: 52, 47, 183, 16 and 79 us, for the pages that are scored again; with |x| + |y| of
+// two pages as their maximum, an instruction less: 48, 45, 177, 13 and 76 us.
 template <int D, int NT, int TB>
 __global__ void __launch_bounds__(kSelThreads, D > 128 ? 4 : (TB == 1 && NT == 1 ? 7 : 5)) select_pages_kernel(const __grid_constant__ SelectParams p) {
     using C = SelCfg<D, NT, TB>;
@@ -564,9 +567,10 @@ __global__ void __launch_bounds__(kSelThreads, D > 128 ? 4 : (TB == 1 && NT == 1
                         mma_f16(acc[t], a[0], a[1], a[2], a[3], bf.x, bf.y);
                     }
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {  // |x| + |y| bounds both, and an addition is cheaper than a maximum
-                        const __half2 z = __hadd2(__habs2(*reinterpret_cast<__half2 *>(&a[2 * e])), __habs2(*reinterpret_cast<__half2 *>(&a[2 * e + 1])));
-                        kmax2[2 * (s & 1) + e] = hmax2_nan(*reinterpret_cast<const uint32_t *>(&z), kmax2[2 * (s & 1) + e]);
+                    for (int e = 0; e < 2; ++e) {
+                        const __half2 x = __habs2(*reinterpret_cast<__half2 *>(&a[2 * e])), y = __habs2(*reinterpret_cast<__half2 *>(&a[2 * e + 1]));
+                        const uint32_t z = hmax2_nan(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
+                        kmax2[2 * (s & 1) + e] = hmax2_nan(z, kmax2[2 * (s & 1) + e]);
                     }
                 }
             }
@@ -665,7 +669,7 @@ __global__ void __launch_bounds__(kSelThreads, D > 128 ? 4 : (TB == 1 && NT == 1
         a_k = fmaxf(a_k, s_kw[w]);
     }
     for (int r = 0; CS > 1 && r < CS; ++r) a_k = fmaxf(a_k, s_kmax[r]);
-    const float eps2 = 2.002f * C::STEPS * 0x1p-23f * a_l1 * a_k;  // 2 eps; 0.002 for A's own roundings
+    const float eps2 = 2.002f * (D + 5 * C::STEPS) * 0x1p-25f * a_l1 * a_k;  // 2 eps; 0.002 for A's own roundings
     float t_hi = INFINITY, t_lo = INFINITY;
     if (want > 0) {
         unsigned int kth;

@@ -1,4 +1,5 @@
-"""Corners of the paged-cache operators on the GPU: exact choices beside NaN pages."""
+"""Corners of the paged-cache operators on the GPU: exact choices beside NaN pages and where an MMA's dropped
+bits add up."""
 import math
 
 import pytest
@@ -49,3 +50,28 @@ def test_nan_pages_hide_no_other_page(nan_pages, four):
     bnd[phys[list(nan_pages)]] = math.nan
     check_choice(p, q, bnd, len(nan_pages) + 1, four)
 
+
+@pytest.mark.parametrize("four", [False, True], ids=["one", "four"])
+@pytest.mark.parametrize("large", [448.0, -448.0])
+def test_choice_where_dropped_bits_add_up(large, four):
+    """One product of 448 x 448 first, then 254 equal ones just below 2^-f of it: of its sign on pages 0 to 3,
+    of the other on 4 to 7, which a last product g lifts.  An MMA that drops the small products ranks 4 to 7
+    first, while the real scores may have it the other way round."""
+    for f in range(20, 30):
+        ea = int((16 - f) / 2)
+        eb = 16 - f - ea
+        small = 254 * 1.125 * 2.0 ** ea * 1.75 * 2.0 ** eb
+        steps = [m / 8 * 2.0 ** e for e in range(-6, 9) for m in range(8, 16)]
+        for g in [s for s in steps if s < 2 * small][-3:] + [s for s in steps if s > 2 * small][:1]:
+            p = Problem([8 * 16], [1], Hq=1, Hkv=1, D=256, DV=256, ps=8, seed=51)
+            q = torch.full((1, 1, 1, 256), 1.75 * 2.0 ** eb, dtype=torch.float64)
+            q[..., 0], q[..., 255] = 448.0, 1.0
+            page = torch.zeros((16, 256), dtype=torch.float64)
+            page[:8, 0] = large
+            page[:4, 1:255], page[4:8, 1:255] = 1.125 * 2.0 ** ea, -1.125 * 2.0 ** ea
+            page[4:8, 255] = g
+            if large < 0:  # the pages beside them, of higher scores
+                page[8:, 0] = -16.0
+            bnd = torch.zeros((p.k.shape[0], 1, 2, 256), dtype=torch.float64)
+            bnd[p.bt[0].long(), 0] = page[:, None]
+            check_choice(p, q, bnd, 4 if large > 0 else 12, four)
