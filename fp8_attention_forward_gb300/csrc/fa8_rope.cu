@@ -10,10 +10,11 @@
 //
 // Bound: HBM, 2 bytes read and 1 written per element; next, the instructions per element.  A thread
 // keeps the same 16 dims of a head over the heads of one token, so its 8 pairs of sines serve all of
-// them, arithmetic goes two values an instruction, and no barrier follows the loads.  Measured, 8192
-// tokens of 32 + 2 x 8 heads of 128 dims (151 MB): 28 us, 5.4 TB/s, 0.79 of the copy rate; sines through
+// them, arithmetic goes two values an instruction, and no barrier follows the loads.  Measured from a graph's
+// replays, 8192 tokens of 32 + 2 x 8 heads of 128 dims (151 MB): 29 us, 5.2 TB/s, 0.77 of the copy rate (28 with a
+// quotient by the rounded reciprocal alone, which moves values halfway between two); sines through
 // shared memory, four tokens a CTA: 57 us; sincospif per pair and heads by select: 46 us; one decode
-// token: 3.0 us.
+// token: 3.1 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -118,6 +119,19 @@ __device__ __forceinline__ uint64_t widen2(uint32_t x, __half) {
     ptx::h2_to_f32(x, lo, hi);
     return ptx::f2pack(lo, hi);
 }
+// Division by one descale, as x hi + x lo with one rounding: hi + lo is 1 / d to 2^-40 (while d is below 2^100 and
+// lo not subnormal), so that a quotient halfway between two E4M3 values stays there.  hi is below 1 / d, so lo is
+// positive and an infinity meets one of its own sign.
+struct Divisor {
+    uint64_t hi, lo;
+    __device__ __forceinline__ explicit Divisor(float d) {
+        const float h = 0.25f * __fdividef(1.f - 0x1p-21f, 0.25f * d);  // defined up to 2^126
+        const float l = fmaxf(h * fmaf(-h, d, 1.f), 0x1p-149f);
+        hi = ptx::f2pack(h, h);
+        lo = ptx::f2pack(l, l);
+    }
+    __device__ __forceinline__ uint64_t operator()(uint64_t x) const { return ptx::ffma2(x, hi, fmul2(x, lo)); }
+};
 // four fp32 (two pairs) -> four E4M3 bytes
 __device__ __forceinline__ uint32_t round4(uint64_t a, uint64_t b) {
     float a0, a1, b0, b1;
@@ -126,15 +140,14 @@ __device__ __forceinline__ uint32_t round4(uint64_t a, uint64_t b) {
     return ptx::prmt_lo16(ptx::cvt_e4m3x2(a1, a0), ptx::cvt_e4m3x2(b1, b0));
 }
 
-// Rotates (ROT: where `on`), scales and rounds one thread's 16 dims: two groups of 8, `gap` apart.  A warp
+// Rotates (ROT: where `on`), divides and rounds one thread's 16 dims: two groups of 8, `gap` apart.  A warp
 // holds rotated dims and others, so both go through the rotation and the others drop it: exactly, also
 // beside an infinity.
 template <typename T, bool INTER, bool ROT>
-__device__ __forceinline__ void rope_store(uint8_t *dst, int gap, const uint4 &ra, const uint4 &rb, float inv, bool on,
+__device__ __forceinline__ void rope_store(uint8_t *dst, int gap, const uint4 &ra, const uint4 &rb, const Divisor &div, bool on,
                                            const uint64_t (&cc)[INTER ? 8 : 4], const uint64_t (&ss)[INTER ? 8 : 4],
                                            const uint64_t (&ns)[INTER ? 1 : 4]) {
     const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
-    const uint64_t sc = ptx::f2pack(inv, inv);
     uint64_t a[4], c[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -154,8 +167,8 @@ __device__ __forceinline__ void rope_store(uint8_t *dst, int gap, const uint4 &r
             a[e] = on ? y : a[e];
             c[e] = on ? z : c[e];
         }
-        a[e] = fmul2(a[e], sc);
-        c[e] = fmul2(c[e], sc);
+        a[e] = div(a[e]);
+        c[e] = div(c[e]);
     }
     *reinterpret_cast<uint2 *>(dst) = make_uint2(round4(a[0], a[1]), round4(a[2], a[3]));
     *reinterpret_cast<uint2 *>(dst + gap) = make_uint2(round4(c[0], c[1]), round4(c[2], c[3]));
@@ -272,15 +285,14 @@ __global__ void __launch_bounds__(kRopeThreads, 5) rope_append_kernel(const __gr
         }
     }
     auto store = [&](uint8_t *dst, const uint4 &a, const uint4 &c, float d) {
-        const float inv = __fdividef(1.f, d);
-        rope_store<T, INTER, true>(dst, gap, a, c, inv, ALL || rotated, cc, ss, ns);
+        rope_store<T, INTER, true>(dst, gap, a, c, Divisor(d), ALL || rotated, cc, ss, ns);
     };
     if (ok) {
         uint8_t *dk = p.ko + outer * p.ko_s[0] + row * p.ko_s[1] + da;
         uint8_t *dv = p.vo + outer * p.vo_s[0] + row * p.vo_s[1] + 16 * x;
         for (int h = y; h < p.Hkv; h += Y) {
             store(dk + h * p.ko_s[2], ka, kb, kd);
-            if (has_v) rope_store<T, INTER, false>(dv + h * p.vo_s[2], 8, va, vb, __fdividef(1.f, vd), false, cc, ss, ns);
+            if (has_v) rope_store<T, INTER, false>(dv + h * p.vo_s[2], 8, va, vb, Divisor(vd), false, cc, ss, ns);
             if (h + Y < p.Hkv) {
                 sk += Y * p.k_s[2];
                 sv += Y * p.v_s[2];

@@ -241,8 +241,9 @@ FA8_API fa8_status fa8_rope_inv_freq(int rotary_dim, double base, int scaling, d
  *   positions: int32, one per token, any strides; NULL = the token's key index.  The angle
  *     of pair i is position * inv_freq[i], reduced exactly at every position.
  *   rot_scale multiplies the rotated dims (YaRN's attention factor; 1 otherwise).
- *   descale_q/k/v: as in fa8_fwd; out = e4m3(x / descale), round to nearest even,
- *     saturating at +-448 (infinities too); NaN stays NaN.
+ *   descale_q/k/v: as in fa8_fwd, 2^-126 or more; out = e4m3(x / descale), round to nearest
+ *     even (of the fp32 quotient, which keeps what is halfway between two values while the
+ *     descale is below 2^100), saturating at +-448 (infinities too); NaN stays NaN.
  * The outputs must not overlap the inputs, and no two tokens may share a cache slot.
  */
 FA8_API fa8_status fa8_rope_append(const fa8_tensor *q, const fa8_tensor *k, const fa8_tensor *v,

@@ -1,5 +1,5 @@
 """Corners of the paged-cache operators on the GPU: exact choices beside NaN pages and where an MMA's dropped
-bits add up."""
+bits add up, and quotients halfway between two E4M3 values."""
 import math
 
 import pytest
@@ -75,3 +75,66 @@ def test_choice_where_dropped_bits_add_up(large, four):
             bnd = torch.zeros((p.k.shape[0], 1, 2, 256), dtype=torch.float64)
             bnd[p.bt[0].long(), 0] = page[:, None]
             check_choice(p, q, bnd, 4 if large > 0 else 12, four)
+
+
+# ------------------------------------------------------------------ rotary append
+def append(x, ds, dev="cuda", **kw):
+    """E4M3 (Q, K, V) of the same rows x (tokens, D) divided by ds; D = DV = 64, dims 0 to 15 rotated at position 0."""
+    T = x.shape[0]
+    p = Problem([T], [T], Hq=1, Hkv=1, D=64, DV=64, ps=16, seed=52)
+    rows = x.to(dev)[None, :, None]
+    d = torch.as_tensor(ds, dtype=torch.float32).reshape(1, 1).to(dev)
+    ko, vo = p.k.to(dev), p.v.to(dev)
+    q8 = fa8.rope_append(rows, rows, rows, torch.ones(8, dtype=torch.float64, device=dev), k_out=ko, v_out=vo, descale_q=d,
+                         descale_k=d, descale_v=d, positions=torch.zeros((1, T), dtype=torch.int32, device=dev),
+                         **p.index_args(dev), **kw)
+    ok()
+    page, row = p.bt[0].long()[torch.arange(T) // 16], torch.arange(T) % 16
+    return val(q8.cpu())[0, :, 0], val(ko.cpu())[page, row, 0], val(vo.cpu())[page, row, 0]
+
+
+def check_append(x, d, **kw):
+    """Q and K are rotated first: by cos 0 = 1 and sin 0 = 0, which leaves what is finite, and makes a NaN of an
+    infinity's partner."""
+    x, d = x.cpu(), torch.as_tensor(d, dtype=torch.float32)
+    turned = ref.rope(x[:, None], torch.zeros(len(x)), torch.ones(8), kw.get("interleaved", False), 0, 1.0)[:, 0]
+    for got, y in zip(append(x, d, **kw), (turned, turned, x.double())):
+        y = y / d.double()
+        want = torch.where(y.isnan(), y, val(e4m3(y.nan_to_num(0.0, 1e9, -1e9))))
+        same = (got == want) | (got.isnan() & want.isnan())
+        assert same.all(), [(float(x[i]), float(got[i]), float(want[i])) for i in (~same).nonzero()[:4].unbind(1)]
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_quotients_halfway_between_two_values(dtype, inter):
+    """x / descale halfway between neighbours of E4M3 goes to the even one, whatever the descale's reciprocal
+    rounds to: x = (odd five-bit number) times a three-bit descale, exact in both types."""
+    odd = torch.arange(17, 32, 2, dtype=torch.float64)
+    t = torch.cat([odd * 2.0 ** e for e in range(-10, 5)] + [torch.arange(1, 16, 2) * 2.0 ** -10])
+    t = torch.cat([t, -t])
+    t = torch.nn.functional.pad(t, (0, -len(t) % 64)).reshape(-1, 64)
+    for d in (3.0, 5.0, 7.0, 3 / 64, 5 / 128, 7 / 32, 7 * 2.0 ** 10):
+        x = (t * d).to(dtype)
+        assert torch.equal(x.double(), t * d) or dtype is torch.float16  # fp16 has fewer exponents
+        check_append(x, d, interleaved=inter)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_quotients_are_those_of_fp32_division(dtype):
+    g = torch.Generator().manual_seed(53)
+    for k in range(20):
+        x = (torch.randn((40, 64), generator=g) * 2.0 ** (k - 10)).to(dtype)
+        d = torch.rand((), generator=g) * 2.0 ** (k - 10) + 2.0 ** (k - 11)
+        check_append(x, d)
+
+
+@pytest.mark.parametrize("d", [2.0 ** -126, 1.5 * 2.0 ** -126, 2.0 ** -64, 1.0, 1e30, 1.75 * 2.0 ** 126, 3e38])
+def test_quotients_at_the_ends_of_the_range(d):
+    """Zeros, infinities, NaN and the largest and smallest values by the smallest and largest normal descales."""
+    v = [0.0, -0.0, math.inf, -math.inf, math.nan, 3e38, -3e38, 2.0 ** -133, 2.0 ** -126, 1.0, 1e30, 1e10, d, -448.0 * d, 18.0 * d, 1e5 * d]
+    if d < 2.0 ** 100:  # halfway between two values
+        v += [2.0 ** -10 * d, 3 * 2.0 ** -10 * d, 17.0 * d, -464.0 * d]
+    x = torch.zeros((len(v), 64), dtype=torch.bfloat16)
+    x[:, 20] = torch.tensor(v, dtype=torch.float64).bfloat16()  # a dim that passes through, in a row of zeros
+    check_append(x, d)
