@@ -57,6 +57,12 @@ __device__ __forceinline__ void e4m3x4_to_h2(uint32_t w, uint32_t &lo, uint32_t 
     lo = ptx::e4m3x2_to_h2(w);
     hi = ptx::e4m3x2_to_h2(w >> 16);
 }
+// {hi, lo} -> f16x2 (lo in the low half), round to nearest even, saturating; NaN stays
+__device__ __forceinline__ uint32_t cvt_f16x2_sat(float hi, float lo) {
+    uint32_t d;
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
 // two 16 x 16 byte tiles transposed, rows at the addresses of lanes 0 .. 15 and 16 .. 31: lane (r, c) gets
 // column r of rows 4c .. 4c + 3 and column r + 8 of them, of either tile
 __device__ __forceinline__ void ld_trans_b8(uint32_t (&d)[4], uint32_t addr) {

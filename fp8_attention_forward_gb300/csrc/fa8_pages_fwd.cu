@@ -11,9 +11,9 @@
 // its own running maximum, sum and O^T in registers, and has one K and one V buffer that TMA fills
 // (boxes of one head's rows of a page, swizzled): the next K while this chunk goes through softmax and
 // PV, the next V during PV and the next S^T.  V's 16 x 16 byte tiles are transposed as they are loaded.  P is
-// rounded to f16 (2^-11 relative; p <= 2^8, as the maximum it is taken against trails by no more, so nothing
-// saturates), not to E4M3 as in fa8_fwd: V widens to f16 anyway.  The warps, then the CTAs of the
-// cluster through distributed shared memory, merge by their maxima: no workspace, no second kernel.
+// rounded to f16 (2^-11 relative down to 2^-21 of the row's maximum, and by 2^-32 of it below), not to E4M3 as in
+// fa8_fwd: V widens to f16 anyway.  The warps, then the CTAs of the cluster through distributed shared memory,
+// merge by their maxima: no workspace, no second kernel.
 //
 // Measured (d = dv = 128, 64 x 8 lists of 2048 keys, 267 MB): 48 us, 5.6 TB/s, 0.82 of the copy rate.
 // Many tokens of one request (512 x 8 lists of 2048 keys, 2.1 GB through L2): 157 us, 13.6 TB/s; in chunks
@@ -64,7 +64,10 @@ struct PagesParams {
 };
 
 constexpr int kPgMaxCluster = 8;
-constexpr float kPgSlack = 8.f;
+// P is taken against 2^kPgBias below a row's maximum, and that maximum moves only for scores 2^kPgSlack above it:
+// p <= 2^15 stays in f16's range, and p of 2^-31 of the maximum is still more than zero.  (Scores past 2^24, where
+// an fp32 step is a factor of two or more, saturate.)
+constexpr float kPgBias = 7.f, kPgSlack = 8.f;
 
 // MANY: many tokens per request, whose lists L2 serves: longer chunks, fewer CTAs.
 template <int D, int DV, int NT, int PW, bool MANY>
@@ -259,7 +262,8 @@ __global__ void __launch_bounds__(32 * PW, PgCfg<D, DV, NT, PW, MANY>::CTAS) fwd
         fetch_v();
     }
 
-    float m[NT][2], l[NT][2];  // running maximum (log2 units) and this lane's share of the sum, rows 2c, 2c + 1
+    // running maximum less kPgBias (log2 units) and this lane's share of the sum, rows 2c, 2c + 1
+    float m[NT][2], l[NT][2];
     float o[C::DT][NT][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -347,8 +351,8 @@ __global__ void __launch_bounds__(32 * PW, PgCfg<D, DV, NT, PW, MANY>::CTAS) fwd
             fetch_k();
         }
         uint32_t pb[C::MT][NT][2];
-        // The maximum that P is taken against moves only when some score is 2^kPgSlack above it (p stays below
-        // f16's range, sums are fp32 anyway): most chunks need no maximum over lanes and no rescaling.
+        // The maximum that P is taken against moves only when some score is 2^kPgSlack above it (sums are fp32
+        // anyway): most chunks need no maximum over lanes and no rescaling.
         float mx[NT][2];
         bool moved = false;
 #pragma unroll
@@ -359,7 +363,7 @@ __global__ void __launch_bounds__(32 * PW, PgCfg<D, DV, NT, PW, MANY>::CTAS) fwd
 #pragma unroll
                 for (int x = 0; x < C::MT; ++x) y = fmaxf(y, fmaxf(s[x][t][e], s[x][t][2 + e]));
                 mx[t][e] = y * cs;
-                moved |= mx[t][e] > m[t][e] + kPgSlack;
+                moved |= mx[t][e] > m[t][e] + (kPgBias + kPgSlack);
             }
         if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
@@ -369,7 +373,7 @@ __global__ void __launch_bounds__(32 * PW, PgCfg<D, DV, NT, PW, MANY>::CTAS) fwd
                     float mn = mx[t][e];
 #pragma unroll
                     for (int sh = 4; sh < 32; sh <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, sh));
-                    mn = fmaxf(m[t][e], mn);
+                    mn = fmaxf(m[t][e], mn - kPgBias);
                     const float alpha = mn == -INFINITY ? 1.f : ptx::ex2(m[t][e] - mn);  // 0 while nothing has been seen
                     m[t][e] = mn;
                     l[t][e] *= alpha;
@@ -390,7 +394,7 @@ __global__ void __launch_bounds__(32 * PW, PgCfg<D, DV, NT, PW, MANY>::CTAS) fwd
                     const float p0 = ptx::ex2(fmaf(s[x][t][2 * h], cs, r0)), p1 = ptx::ex2(fmaf(s[x][t][2 * h + 1], cs, r1));
                     l[t][0] += p0;
                     l[t][1] += p1;
-                    pb[x][t][h] = trans8x8(ptx::cvt_f16x2(p1, p0));
+                    pb[x][t][h] = trans8x8(cvt_f16x2_sat(p1, p0));
                 }
         }
         // ---- O^T

@@ -1,5 +1,5 @@
 """Corners of the paged-cache operators on the GPU: exact choices beside NaN pages and where an MMA's dropped
-bits add up, and quotients halfway between two E4M3 values."""
+bits add up, quotients halfway between two E4M3 values, small weights and the largest scores."""
 import math
 
 import pytest
@@ -138,3 +138,56 @@ def test_quotients_at_the_ends_of_the_range(d):
     x = torch.zeros((len(v), 64), dtype=torch.bfloat16)
     x[:, 20] = torch.tensor(v, dtype=torch.float64).bfloat16()  # a dim that passes through, in a row of zeros
     check_append(x, d)
+
+
+# ------------------------------------------------------------------ attention over listed pages
+@pytest.mark.parametrize("Hq,D", [(1, 64), (4, 128), (12, 128), (8, 256)])
+@pytest.mark.parametrize("tokens", [1, 600])
+def test_many_small_weights_add_up(tokens, Hq, D):
+    """Keys of weight 2^-x beside one of weight 1 and value 0 in every 32: all that O holds are the small ones.
+    P is taken in units of 2^-31 of the maximum or less, so each weight is off by at most 2^-32 (of a sum of
+    about n / 32, in n keys of value 448), or by 2^-11 of itself; then O's rounding, and 2^-15 for the fp32 steps
+    (an exponent of 30 in 2^-23, twice)."""
+    n, ps = 2048, 16
+    p = Problem([n + tokens], [tokens], Hq=Hq, Hkv=1, D=D, DV=D, ps=ps, seed=54)
+    phys = p.bt[0].long()
+    j = torch.arange(n)
+    small = j % 32 != 5
+    p.q = torch.zeros((1, tokens, Hq, D)).to(E4M3)
+    q = val(p.q)
+    q[..., 1] = 1.0
+    p.q = q.float().to(E4M3)
+    lists = torch.arange(n // ps, dtype=torch.int32).expand(1, tokens, 1, n // ps).contiguous().cuda()
+    for x in (20.0, 24.0, 28.0, 30.0):
+        k, v = torch.zeros(p.k.shape, dtype=torch.float64), torch.zeros(p.v.shape, dtype=torch.float64)
+        k[phys[j // ps], j % ps, 0, 1] = torch.where(small, -x, 0.0).double()
+        v[phys[j // ps], j % ps, 0] = torch.where(small, 448.0, 0.0).double()[:, None]
+        out, lse = fa8.fwd_pages(p.q.cuda(), k.float().to(E4M3).cuda(), v.float().to(E4M3).cuda(), lists,
+                                 softmax_scale=math.log(2), **p.index_args())
+        ok()
+        count = int(small.sum())
+        total = (n - count) + count * 2.0 ** -x
+        want = count * 2.0 ** -x * 448 / total
+        tol = want * (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -15) + count * 2.0 ** -32 * 448 / total
+        assert (out.double().cpu() - want).abs().max() <= tol, (x, out.flatten()[:4], want)
+        assert (lse.double().cpu() - math.log(total)).abs().max() <= 2.0 ** -18
+
+
+@pytest.mark.parametrize("scale", [1.0, 2.0])
+@pytest.mark.parametrize("climb", [0.0, 0.125, 1.0])
+def test_largest_scores_leave_no_nan(climb, scale):
+    """Scores of 448 x 448 over all channels, above 2^24 in log2 units, equal or climbing slowly over the list: V is
+    1 everywhere, so O is 1 but for the weights that saturate (by two at most) and bf16's rounding."""
+    n, ps = 1000, 16
+    p = Problem([n], [1], Hq=2, Hkv=1, D=64, DV=64, ps=ps, seed=55)
+    j = torch.arange(n)
+    q, k = torch.full((1, 1, 2, 64), 448.0), torch.full(p.k.shape, 448.0)
+    q[..., 1] = climb
+    k[p.bt[0].long()[j // ps], j % ps, 0, 1] = (j // 40).float().to(E4M3).float()
+    v = torch.ones(p.v.shape).to(E4M3)
+    lists = torch.arange(-(-n // ps), dtype=torch.int32).reshape(1, 1, 1, -1).cuda()
+    out, lse = fa8.fwd_pages(q.to(E4M3).cuda(), k.to(E4M3).cuda(), v.cuda(), lists, softmax_scale=scale, **p.index_args())
+    ok()
+    assert (out >= 0.5).all() and (out <= 1.0 + 2.0 ** -8).all(), out.flatten()[:4]
+    z = (q.to(E4M3).double()[0, 0, 0] * k.to(E4M3).double()[p.bt[0].long()[j // ps], j % ps, 0]).sum(-1) * scale
+    assert ((lse.double().cpu() - torch.logsumexp(z, 0)).abs() <= 2.0 ** -21 * z.max()).all()
