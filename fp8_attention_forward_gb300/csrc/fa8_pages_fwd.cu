@@ -207,7 +207,8 @@ __global__ void __launch_bounds__(32 * PW, PgCfg<D, DV, NT, PW, MANY>::CTAS) fwd
     __syncthreads();
     const int bpp = ps / p.box;            // boxes per page
     const int boxes = s_used * bpp;        // boxes of the list
-    const float cs = p.scale_log2 * dqv * dkv;
+    float cs = p.scale_log2 * dqv * dkv;
+    if (cs == 0.f) cs = 0x1p-126f;  // below fp32: a masked -inf must stay one
 
     // ---- the warp's chunk buffer, one of K and one of V: chunk it is boxes (first + it * stride) <<
     // box_shift ..; K is fetched while the chunk before goes through softmax and PV, V during PV and S^T

@@ -191,3 +191,22 @@ def test_largest_scores_leave_no_nan(climb, scale):
     assert (out >= 0.5).all() and (out <= 1.0 + 2.0 ** -8).all(), out.flatten()[:4]
     z = (q.to(E4M3).double()[0, 0, 0] * k.to(E4M3).double()[p.bt[0].long()[j // ps], j % ps, 0]).sum(-1) * scale
     assert ((lse.double().cpu() - torch.logsumexp(z, 0)).abs() <= 2.0 ** -21 * z.max()).all()
+
+
+@pytest.mark.parametrize("scale,descale", [(1e-30, 1e-10), (1e-38, 1e-30), (1e-20, 1.0)])
+def test_vanishing_scales_weigh_keys_alike(scale, descale):
+    """A scale whose product with the descales is below fp32: every visible key has one weight, and the keys behind
+    them have none.  O is V's mean to bf16's rounding, LSE the logarithm of the number of keys."""
+    n, ps = 77, 16
+    p = Problem([n], [1], Hq=4, Hkv=2, D=64, DV=64, ps=ps, seed=56)
+    p.poison()
+    lists = torch.arange(-(-n // ps), dtype=torch.int32).expand(1, 1, 2, -1).contiguous().cuda()
+    d = torch.tensor(descale).cuda()
+    out, lse = fa8.fwd_pages(p.q.cuda(), p.k.cuda(), p.v.cuda(), lists, softmax_scale=scale, descale_q=d, descale_k=d,
+                             **p.index_args())
+    ok()
+    j = torch.arange(n)
+    v = val(p.v)[p.bt[0].long()[j // ps], j % ps]
+    want, mass = v.mean(0).repeat_interleave(2, 0), v.abs().mean(0).repeat_interleave(2, 0)
+    assert ((out.double().cpu()[0, 0] - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -11 * mass).all(), out.flatten()[:4]
+    assert ((lse.double().cpu() - math.log(n)).abs() <= 2.0 ** -20).all(), lse
