@@ -236,7 +236,8 @@ __global__ void __launch_bounds__(kRopeThreads, 5) rope_append_kernel(const __gr
         Lk = p.cu_k[b + 1] - kstart;
     }
     const int j = Lk - Lq + i;  // key index of this token
-    bool ok = j >= 0;
+    const bool none = j < 0 && Lk >= 0;  // more new tokens than keys (a padded slot): nothing to append
+    bool ok = j >= 0 && Lk >= 0;
     long long outer = b, row = j;
     if (ok && p.kv_mode == 2) {
         const int pi = j / p.tab.page_size;
@@ -250,7 +251,7 @@ __global__ void __launch_bounds__(kRopeThreads, 5) rope_append_kernel(const __gr
         row = (long long)kstart + j;
         ok = ok && kstart >= 0 && row < p.total_k;
     }
-    if (!ok && x == 0 && y == 0) atomicOr(p.status, kStatusBounds);
+    if (!ok && !none && x == 0 && y == 0) atomicOr(p.status, kStatusBounds);
     // ---- cosines and sines of its 8 pairs, packed as rope_store takes them
     uint64_t cc[INTER ? 8 : 4] = {}, ss[INTER ? 8 : 4] = {}, ns[INTER ? 1 : 4] = {};
     if (rotated) {

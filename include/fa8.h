@@ -195,7 +195,8 @@ FA8_API fa8_status fa8_fwd_static_scratch(const fa8_tensor *q, const fa8_tensor 
  *
  * Shared conventions.  "New tokens" are the last Lq keys of each request: batched
  * (B, Sq, ...) or packed (total_q, ...) with cu_seqlens_q, as q in fa8_fwd; token i of a
- * request with Lk keys is its key Lk - Lq + i.  Output rows of a packed tensor behind the last
+ * request with Lk keys is its key Lk - Lq + i.  Where Lk < Lq (a padded slot may have no key)
+ * the first tokens have none: they see nothing, and nothing is appended for them.  Output rows of a packed tensor behind the last
  * sequence stay as they were.  A tensor that a call writes must not have expanded dims.
  * A cu_seqlens_k or block_table entry out of range
  * raises FA8_ERR_DEVICE_BOUNDS in fa8_check and is never followed.  Every call enqueues one

@@ -1,5 +1,6 @@
 """Corners of the paged-cache operators on the GPU: exact choices beside NaN pages and where an MMA's dropped
-bits add up, quotients halfway between two E4M3 values, small weights and the largest scores."""
+bits add up, quotients halfway between two E4M3 values, small weights, the largest scores and vanishing
+scales, and padded slots of a batch."""
 import math
 
 import pytest
@@ -210,3 +211,44 @@ def test_vanishing_scales_weigh_keys_alike(scale, descale):
     want, mass = v.mean(0).repeat_interleave(2, 0), v.abs().mean(0).repeat_interleave(2, 0)
     assert ((out.double().cpu()[0, 0] - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -11 * mass).all(), out.flatten()[:4]
     assert ((lse.double().cpu() - math.log(n)).abs() <= 2.0 ** -20).all(), lse
+
+
+@pytest.mark.parametrize("layout", ["paged", "varlen", "dense"])
+def test_padded_slots_append_nothing(layout):
+    """Requests without keys, or with fewer than new tokens, in a batch: the other requests' keys are appended, the
+    rest of the cache stays, Q is stored for all, and nothing is reported; keys that cu_seqlens_k takes back are."""
+    keys = [20, 20, 20] if layout == "dense" else [70, 0, 2]
+    Sq = 33 if layout == "dense" else 3
+    p = Problem(keys, [Sq] * 3, Hq=2, Hkv=1, D=64, DV=64, ps=16, seed=57)
+    x = torch.randn((3, Sq, 2, 64), generator=p.g).bfloat16().cuda()
+    w = torch.ones(16, dtype=torch.float64, device="cuda")
+    args = p.index_args()
+    kw = {"paged": args, "varlen": dict(args, block_table=None, page_size=0), "dense": {}}[layout]
+    if layout == "paged":
+        ko, vo = p.k.cuda(), p.v.cuda()
+    else:
+        shape = (3, 20, 1, 64) if layout == "dense" else (72, 1, 64)
+        ko, vo = (e4m3(torch.randn(shape, generator=p.g)).cuda() for _ in range(2))
+    before = [t.clone().view(torch.uint8) for t in (ko, vo)]
+
+    def run(**change):
+        q8 = fa8.rope_append(x, x[:, :, :1], x[:, :, :1], w, k_out=ko, v_out=vo, rotary_offset=16, **dict(kw, **change))
+        return q8, fa8.check()
+
+    q8, status = run()
+    assert status == fa8.FA8_SUCCESS
+    assert torch.equal(val(q8.cpu())[..., :16], val(e4m3(x.cpu()))[..., :16])  # dims that pass through
+    written = torch.zeros(before[0].shape[:-2], dtype=torch.bool)
+    for b, i, _ in p.tokens():
+        j = p.keys[b] - Sq + i
+        if j >= 0:
+            at = {"paged": lambda: (int(p.bt[b, j // 16]), j % 16), "varlen": lambda: (int(p.cu_k[b]) + j,),
+                  "dense": lambda: (b, j)}[layout]()
+            written[at] = True
+            for out in (ko, vo):
+                assert torch.equal(val(out[at].cpu())[0, :16], val(e4m3(x[b, i, 0].cpu()))[:16])
+    for out, b in zip((ko, vo), before):
+        assert torch.equal(out.view(torch.uint8)[~written.cuda()], b[~written.cuda()])
+    if layout != "dense":
+        cu = torch.tensor([0, 70, 65, 67], dtype=torch.int32, device="cuda")
+        assert run(cu_seqlens_k=cu)[1] == fa8.FA8_ERR_DEVICE_BOUNDS
