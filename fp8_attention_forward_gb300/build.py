@@ -12,6 +12,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -52,19 +53,19 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(f) <= t for f in _sources() + _headers() + [__file__])
 
 
-def args_path() -> str:
-    """Where the argument module for the running torch lies."""
-    import torch
-
-    return os.path.join(BUILD, f"fa8_args-{torch.__version__}.so")
+def args_path(torch_version: str) -> str:
+    """Where the argument module for this interpreter and that torch lies."""
+    return os.path.join(BUILD, f"fa8_args-{torch_version}{sysconfig.get_config_var('EXT_SUFFIX')}")
 
 
 def build_args():
-    """Compiles csrc/fa8_args.cpp, the Python module that packs tensor views (needs Python's and torch's
-    headers: without them the binding packs the views itself)."""
-    import torch
-
-    out, src = args_path(), os.path.join(CSRC, "fa8_args.cpp")
+    """Compiles csrc/fa8_args.cpp, the Python module that packs tensor views.  It needs torch, its and Python's
+    headers and g++; where one is missing or fails, the binding packs the views itself and this returns None."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    out, src = args_path(torch.__version__), os.path.join(CSRC, "fa8_args.cpp")
     py, pt = sysconfig.get_paths()["include"], os.path.dirname(torch.__file__)
     inc = os.path.join(pt, "include")
     if not os.path.exists(os.path.join(py, "Python.h")) or not os.path.exists(os.path.join(inc, "ATen", "ATen.h")):
@@ -79,9 +80,16 @@ def build_args():
     cmd += [x for d in (py, inc, os.path.join(inc, "torch", "csrc", "api", "include")) for x in ("-isystem", d)]
     cmd += ["-I", os.path.join(ROOT, "include"), src, "-o", tmp, "-L", os.path.join(pt, "lib"), "-ltorch_python",
             "-ltorch_cpu", "-lc10"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("g++ failed on fa8_args.cpp:\n" + r.stdout + r.stderr)
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        failed = r.returncode != 0 and r.stdout + r.stderr
+    except OSError as e:
+        failed = str(e)
+    if failed:
+        if os.path.exists(out):  # of an older source
+            os.remove(out)
+        warnings.warn("fa8_args.cpp was not compiled, the binding packs tensor views in Python:\n" + failed)
+        return None
     os.replace(tmp, out)
     return out
 
@@ -110,12 +118,13 @@ def build(force: bool = False, ptxas_verbose: bool = False, jobs: int | None = N
     jobs = jobs or min(len(srcs), os.cpu_count() or 4)
     logs = []
     with cf.ThreadPoolExecutor(jobs + 1) as ex:
-        args = ex.submit(build_args)
+        args = ex.submit(build_args) if build_dir == BUILD else None
         for src, rc, out in ex.map(one, zip(srcs, objs)):
             logs.append(f"== {os.path.basename(src)}\n{out}")
             if rc != 0:
                 raise RuntimeError(f"nvcc failed on {src}:\n{out}")
-        args.result()
+        if args:
+            args.result()
     with open(os.path.join(build_dir, "ptxas.log"), "w") as f:
         f.write("\n".join(logs))
     tmp = lib + f".tmp{os.getpid()}"

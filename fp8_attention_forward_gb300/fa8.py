@@ -15,6 +15,8 @@ from typing import Optional
 
 import torch
 
+from .build import args_path
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # FA8_LIBRARY may point at another build of the same library (e.g. one with FA8_TRACE)
 LIB_PATH = os.environ.get("FA8_LIBRARY") or os.path.join(_HERE, "_build", "libfa8.so")
@@ -280,11 +282,11 @@ def _packed(name):
 
 
 def _args_module():
-    """The module that packs the views in C++, or None where it was not built for this torch."""
+    """The module that packs the views in C++, or None where it was not built for this Python and torch."""
     from importlib.machinery import ExtensionFileLoader
     from importlib.util import module_from_spec, spec_from_file_location
 
-    path = os.path.join(_HERE, "_build", f"fa8_args-{torch.__version__}.so")
+    path = args_path(torch.__version__)
     if not os.path.exists(path):
         return None
     return module_from_spec(spec_from_file_location("fa8_args", path, loader=ExtensionFileLoader("fa8_args", path)))
