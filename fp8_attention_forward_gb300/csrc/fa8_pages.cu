@@ -45,10 +45,12 @@ __device__ __forceinline__ uint32_t hmax2_nan(uint32_t a, uint32_t b) {
 // A warp takes 128 bytes (eight 16-channel pieces, a whole line of every row) of one page: lane l holds
 // piece l mod 8 of rows l / 8, l / 8 + 4, ..; then the four row parts meet by shuffles.  E4M3 -> f16 is
 // exact, so the packed f16 minimum and maximum (NaN-propagating) are, and so is the way back.
-// Bound: HBM, one read of the pages' K.  Measured, 2048 pages of 64 keys x 8 heads of 128 (137 MB): 25 us,
-// 5.4 TB/s, 0.80 of the copy rate (a thread per 16 channels walking all rows: 32 us); as many keys in pages
-// of 16 and 8, where joining the row parts weighs more: 41 and 57 us (eight loads a lane whatever the page:
-// 45 and 80); the one new page of 64 requests: 2.9 us (4.6).
+// Bound: HBM, one read of the pages' K; short of it no unit alone (cold: DRAM 59 %, ALU pipe 64 %, 27 warps an SM
+// that wait for loads).  Measured from a graph's replays, 2048 pages of 64 keys x 8 heads of 128 (137 MB): 25 us,
+// 5.4 TB/s, 0.80 of the copy rate, as called 27 us (a thread per 16 channels walking all rows: 32 us); as many
+// keys in pages of 16 and 8, where joining the row parts weighs more: 40 and 57 us (eight loads a lane whatever
+// the page: 45 and 80); the one new page of 64 requests: 2.9 us (4.6).  With cu_seqlens_q a warp is launched for
+// every column of the table, with or without work.
 template <int U>
 __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const __grid_constant__ BoundsParams p) {
     const int b = blockIdx.x / p.blocks_per_req;
@@ -229,8 +231,8 @@ struct Team {
     }
     // The rank-th largest (rank >= 1) of scores [0, n), as ordered integers: bisection by counting, done
     // when exactly `rank` scores lie in the upper part (after about as many steps as n has bits).  A thread
-    // keeps HELD scores in registers; one warp takes twice as many of a longer list (1024 pages: 70 us
-    // for 512 tokens x 8 heads against 80; 2048: 175 against 183), four warps gain nothing by it.
+    // keeps HELD scores in registers; one warp takes twice as many of a longer list (1024 pages: 76 us
+    // for 512 tokens x 8 heads against 84; 2048: 173 against 185), four warps gain nothing by it.
     template <int HELD>
     __device__ __forceinline__ unsigned int kth_score(const float *scores, int n, unsigned int rank) const {
         unsigned int v[HELD], hi = 0, nlo = 0;
@@ -366,7 +368,7 @@ __device__ __forceinline__ unsigned long long exact_key(const uint8_t *src, cons
 // 51; per-lane bulk copies: 65; fragments straight to registers: 73); 512 tokens x 8 heads over 512 pages:
 // 43 us (a token at a time: 164), over 2048 pages 174 us (282 with 64-bit keys of every page in shared memory
 // and one load at a time behind the held scores); one pair of 2048 pages, d = 256, a cluster of 16 CTAs: 13 us
-// (one CTA: 22); 8 of 16384, d = 128: 76 us, most of it the choice.  With an eps that counts on fp32's 24 bits
+// (one CTA: 42); 8 of 16384, d = 128: 76 us, most of it the choice.  With an eps that counts on fp32's 24 bits
 // alone, (D + 2 * 2 D / 16) 2^-23 A: 52, 47, 183, 16 and 79 us, for the pages that are scored again; with |x| + |y| of
 // two pages as their maximum, an instruction less: 48, 45, 177, 13 and 76 us.
 template <int D, int NT, int TB>
@@ -971,9 +973,9 @@ fa8_status fa8_select_pages(const fa8_tensor *q, const fa8_tensor *bounds, fa8_t
     // Several tokens per request and enough of them to fill the GPU in blocks of four: one pass over
     // the bounds serves four tokens.  Else a token at a time, and where there are few (token, kv-head)
     // pairs a cluster of CTAs shares each pair's pages, 128 or more a CTA, up to the seven CTAs that fit an
-    // SM (512 ragged pairs of up to 2048 pages: 46 us in clusters of two, 55 without).  Clusters of 16 only
-    // while every CTA may have an SM (one pair of 2048 pages, d = 256: 12.1 us against 14.3; 64 pairs: 27.7
-    // against 24.2).
+    // SM (512 ragged pairs of up to 2048 pages: 48 us in clusters of two, 55 without).  Clusters of 16 only
+    // while every CTA may have an SM (one pair of 2048 pages, d = 256: 12.7 us against 14.8 in eight and 42 in one
+    // CTA; 64 pairs: 33 against 29 in eight).
     const long long blocks = p.cu_q ? (long long)qs.T / 4 + qs.B : (long long)qs.B * ((qs.Sq + 3) / 4);
     const bool four = p.G <= 8 && (long long)qs.T >= 4LL * qs.B && blocks * Hkv >= 2LL * ds->sm_count &&
                       p.tab.max_pages <= fa8::kSelMaxTable4;

@@ -15,10 +15,11 @@
 // fa8_fwd: V widens to f16 anyway.  The warps, then the CTAs of the cluster through distributed shared memory,
 // merge by their maxima: no workspace, no second kernel.
 //
-// Measured (d = dv = 128, 64 x 8 lists of 2048 keys, 267 MB): 48 us, 5.6 TB/s, 0.82 of the copy rate.
-// Many tokens of one request (512 x 8 lists of 2048 keys, 2.1 GB through L2): 157 us, 13.6 TB/s; in chunks
-// of 32 keys 168 us, with shared memory at 70 %, the ALU pipe, which widens E4M3 to f16, at 54 % and issue
-// slots at 56 %; the copies and the softmax without the products, 122 us.  Tried: V's fragments by 16-byte
+// Measured from a graph's replays (d = dv = 128, 64 x 8 lists of 2048 keys, 267 MB): 47 to 51 us by the box, 5.2 to
+// 5.7 TB/s, 0.77 to 0.84 of the copy rate; as called, inputs changing, 53 us.  Many tokens of one request (512 x 8
+// lists of 2048 keys, 2.1 GB through L2): 158 us, 13.6 TB/s, with shared memory at 65 %, L2 at 55 %, the ALU pipe,
+// which widens E4M3 to f16, at 52 % and issue slots at 51 %; in chunks of 32 keys 168 us, of which the copies and
+// the softmax without the products take 122.  Tried: V's fragments by 16-byte
 // loads whose bytes are paired by permutes, 52 and 210 us; both operands straight to registers, 63 and 303;
 // by 16-byte asynchronous copies, 61 and 258 (L2 is asked for every sector twice); QK by the E4M3 warp MMA,
 // 3 % slower (it widens too); a second K or V buffer, 3 to 5 % slower.
@@ -671,9 +672,9 @@ extern "C" fa8_status fa8_fwd_pages(const fa8_tensor *q, const fa8_tensor *k, co
     p.status = ds->status;
     p.timeout_ns = wait_timeout_ns();
     // Clusters split a list over CTAs while all of them run at once and every warp keeps at least two
-    // chunks (one of 64 keys); where clusters of eight still leave a quarter of the SMs empty, CTAs of eight warps, one per
-    // SM, split it once more (8 lists of 4096 keys, d = dv = 256: 12.0 us against 15.5 with four warps; 14
-    // lists 13.0 against 16.9; 16 lists, whose clusters no longer fit at once, 23.8 against 17.9).
+    // chunks (one of 64 keys); where clusters of eight still leave a quarter of the SMs empty, CTAs of eight
+    // warps, one per SM, split it once more (8 lists of 4096 keys, d = dv = 256: 12.0 us against 15.5 with four
+    // warps; 14 lists 13.0 against 16.9; 16 lists, whose clusters no longer fit at once, 23.8 against 17.9).
     const long long keys = (long long)p.K * page_size;
     const int kc = qs.D + DV <= 256 ? 32 : 16, per_sm = nt == 2 && qs.D + DV > 256 ? 2 : 4;
     p.cluster = 1;

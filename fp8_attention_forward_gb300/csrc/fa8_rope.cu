@@ -8,12 +8,13 @@
 // turn is the low 64 bits of an integer product: exact at every position (an fp32 angle is off
 // by 2^-24 of itself, 0.06 rad at position 2^20), and no range reduction follows.
 //
-// Bound: HBM, 2 bytes read and 1 written per element; next, the instructions per element.  A thread
+// Bound: HBM, 2 bytes read and 1 written per element; short of it, latency: 17 warps an SM wait for their loads
+// (issue slots 51 % used).  A thread
 // keeps the same 16 dims of a head over the heads of one token, so its 8 pairs of sines serve all of
 // them, arithmetic goes two values an instruction, and no barrier follows the loads.  Measured from a graph's
-// replays, 8192 tokens of 32 + 2 x 8 heads of 128 dims (151 MB): 29 us, 5.2 TB/s, 0.77 of the copy rate (28 with a
-// quotient by the rounded reciprocal alone, which moves values halfway between two); sines through
-// shared memory, four tokens a CTA: 57 us; sincospif per pair and heads by select: 46 us; one decode
+// replays, 8192 tokens of 32 + 2 x 8 heads of 128 dims (151 MB): 29 us, 5.2 TB/s, 0.77 of the copy rate (as
+// called, inputs changing: 33; with the rounded reciprocal alone, which moves values halfway between two: 28);
+// sines through shared memory, four tokens a CTA: 57 us; sincospif per pair and heads by select: 46 us; one decode
 // token: 3.1 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -175,8 +176,9 @@ __device__ __forceinline__ void rope_store(uint8_t *dst, int gap, const uint4 &r
 }
 
 // A thread: 16 dims (x) of every blockDim.y-th head of one token.  blockDim = (D / 16, head lanes,
-// tokens).  ALL: every dim is rotated.  The loads of its first K and V head and of a batch of NB q-heads go out first; the angles
-// of its 8 pairs, shared by all heads, and the cache slot are computed while they are in flight.
+// tokens).  ALL: every dim is rotated.  The loads of its first K and V head and of a batch of NB q-heads go
+// out first; the angles of its 8 pairs, shared by all heads, and the cache slot are computed while they are in
+// flight.
 template <typename T, bool INTER, int NB, bool ALL>
 __global__ void __launch_bounds__(kRopeThreads, 5) rope_append_kernel(const __grid_constant__ RopeParams p) {
     __shared__ __align__(16) unsigned long long turn[kRopeMaxPairs];
@@ -335,8 +337,8 @@ cudaError_t launch_rope_batch(const RopeParams &p, int lanes, int spread, cudaSt
 template <typename T, bool INTER>
 cudaError_t launch_rope(const RopeParams &p, int sm_count, cudaStream_t s) {
     // Enough tokens for two CTAs per SM: half as many head lanes as kv-heads, four at most, so that a
-    // thread's heads share its angles (8192 tokens of 32 + 2 x 8 heads, d = 128: 28 us with four lanes,
-    // 30 with eight, 31 with two).  Fewer: a lane per q-head, and the heads over several CTAs, to shorten
+    // thread's heads share its angles (8192 tokens of 32 + 2 x 8 heads, d = 128: 29 us with four lanes,
+    // 31 with eight, 32 with two).  Fewer: a lane per q-head, and the heads over several CTAs, to shorten
     // the chain.
     const int lanes = std::max(1, std::min(p.Hkv / 2, 4));
     if ((long long)p.T * lanes * (p.D / 16) >= 2LL * sm_count * kRopeThreads) return launch_rope_batch<T, INTER, 2>(p, lanes, 1, s);
