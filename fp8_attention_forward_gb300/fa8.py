@@ -327,15 +327,21 @@ def _beside(stream, make, *args):
 def _empty(q, dtype, drop, *dims):
     """A new tensor beside q, of its shape with the last ``drop`` dims replaced."""
     module = _module()
-    if module is None or dtype not in _DTYPES:
-        return torch.empty((*q.shape[:-drop], *dims), dtype=dtype, device=q.device)
-    return module.empty(q, _DTYPES[dtype], drop, *dims)
+    if module is not None and dtype in _DTYPES:
+        try:
+            return module.empty(q, _DTYPES[dtype], drop, *dims)
+        except RuntimeError:
+            pass  # torch raises its own error, e.g. OutOfMemoryError
+    return torch.empty((*q.shape[:-drop], *dims), dtype=dtype, device=q.device)
 
 
 def _empty_lse(q):
     module = _module()
     if module is not None:
-        return module.empty_lse(q)
+        try:
+            return module.empty_lse(q)
+        except RuntimeError:
+            pass
     shape = (q.shape[0], q.shape[2], q.shape[1]) if q.dim() == 4 else (q.shape[1], q.shape[0])
     return torch.empty(shape, dtype=torch.float32, device=q.device)
 

@@ -252,3 +252,22 @@ def test_padded_slots_append_nothing(layout):
     if layout != "dense":
         cu = torch.tensor([0, 70, 65, 67], dtype=torch.int32, device="cuda")
         assert run(cu_seqlens_k=cu)[1] == fa8.FA8_ERR_DEVICE_BOUNDS
+
+
+# ------------------------------------------------------------------ the binding
+@pytest.mark.parametrize("python", [False, True])
+def test_outputs_that_do_not_fit_raise_as_torch_does(python, monkeypatch):
+    """Outputs of petabytes (of an expanded q): torch's OutOfMemoryError, which callers catch to free memory."""
+    monkeypatch.setattr(fa8, "_entries", {})
+    if python:
+        monkeypatch.setattr(fa8, "_args_module", lambda: None)
+    q = torch.zeros((1, 1, 8, 128), dtype=torch.uint8, device="cuda").view(E4M3).expand(1 << 20, 1 << 20, 8, 128)
+    p = Problem([16], [1], Hq=8, Hkv=8, seed=58)
+    k, v = p.k.cuda(), p.v.cuda()
+    bnd = torch.zeros((p.k.shape[0], 8, 2, 128), dtype=torch.uint8, device="cuda").view(E4M3)
+    pages = torch.zeros((1, 1, 1, 1), dtype=torch.int32, device="cuda")
+    for call in (lambda: fa8.select_pages(q, bnd, 64, **p.index_args()), lambda: fa8.fwd_pages(q, k, v, pages, **p.index_args()),
+                 lambda: fa8.fwd_pages(q, k, v, pages, out=k, **p.index_args())):
+        with pytest.raises(torch.OutOfMemoryError):
+            call()
+    ok()
