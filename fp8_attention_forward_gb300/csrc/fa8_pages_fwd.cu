@@ -15,7 +15,7 @@
 // fa8_fwd: V widens to f16 anyway.  The warps, then the CTAs of the cluster through distributed shared memory,
 // merge by their maxima: no workspace, no second kernel.
 //
-// Measured from a graph's replays (d = dv = 128, 64 x 8 lists of 2048 keys, 267 MB): 47 to 51 us by the box, 5.2 to
+// Measured from a graph's replays (d = dv = 128, 64 x 8 lists of 2048 keys, 267 MB): 47 to 51 us by the GPU, 5.2 to
 // 5.7 TB/s, 0.77 to 0.84 of the copy rate; as called, inputs changing, 53 us.  Many tokens of one request (512 x 8
 // lists of 2048 keys, 2.1 GB through L2): 158 us, 13.6 TB/s, with shared memory at 65 %, L2 at 55 %, the ALU pipe,
 // which widens E4M3 to f16, at 52 % and issue slots at 51 %; in chunks of 32 keys 168 us, of which the copies and

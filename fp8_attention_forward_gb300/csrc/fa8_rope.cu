@@ -126,7 +126,7 @@ __device__ __forceinline__ uint64_t widen2(uint32_t x, __half) {
 struct Divisor {
     uint64_t hi, lo;
     __device__ __forceinline__ explicit Divisor(float d) {
-        const float h = 0.25f * __fdividef(1.f - 0x1p-21f, 0.25f * d);  // defined up to 2^126
+        const float h = 0.25f * __fdividef(1.f - 0x1p-21f, 0.25f * d);  // defined from 2^-126 to 2^126
         const float l = fmaxf(h * fmaf(-h, d, 1.f), 0x1p-149f);
         hi = ptx::f2pack(h, h);
         lo = ptx::f2pack(l, l);

@@ -196,13 +196,13 @@ FA8_API fa8_status fa8_fwd_static_scratch(const fa8_tensor *q, const fa8_tensor 
  * Shared conventions.  "New tokens" are the last Lq keys of each request: batched
  * (B, Sq, ...) or packed (total_q, ...) with cu_seqlens_q, as q in fa8_fwd; token i of a
  * request with Lk keys is its key Lk - Lq + i.  Where Lk < Lq (a padded slot may have no key)
- * the first tokens have none: they see nothing, and nothing is appended for them.  Output rows of a packed tensor behind the last
- * sequence stay as they were.  A tensor that a call writes must not have expanded dims.
- * A cu_seqlens_k or block_table entry out of range
- * raises FA8_ERR_DEVICE_BOUNDS in fa8_check and is never followed.  Every call enqueues one
- * kernel on `stream`, needs no workspace, allocates nothing, and its launch depends on
- * shapes and the SM count only, so it can be graph-captured.  Results do not depend on
- * timing: equal inputs give equal bits.
+ * the first tokens have no key: nothing is appended for them, and they see nothing when
+ * causal = 1.  Output rows of a packed tensor behind the last sequence stay as they were.  A
+ * tensor that a call writes must not have expanded dims.  A cu_seqlens_k or block_table entry
+ * out of range raises FA8_ERR_DEVICE_BOUNDS in fa8_check and is never followed.  Every call
+ * enqueues one kernel on `stream`, needs no workspace, allocates nothing, and its launch
+ * depends on shapes and the SM count only, so it can be graph-captured.  Results do not depend
+ * on timing: equal inputs give equal bits.
  * ------------------------------------------------------------------------------------ */
 
 /* How fa8_rope_inv_freq stretches the frequencies w_i = base^(-2 i / rotary_dim). */
@@ -242,7 +242,7 @@ FA8_API fa8_status fa8_rope_inv_freq(int rotary_dim, double base, int scaling, d
  *   positions: int32, one per token, any strides; NULL = the token's key index.  The angle
  *     of pair i is position * inv_freq[i], reduced exactly at every position.
  *   rot_scale multiplies the rotated dims (YaRN's attention factor; 1 otherwise).
- *   descale_q/k/v: as in fa8_fwd, 2^-126 or more; out = e4m3(x / descale), round to nearest
+ *   descale_q/k/v: as in fa8_fwd, 2^-124 or more; out = e4m3(x / descale), round to nearest
  *     even (of the fp32 quotient, which keeps what is halfway between two values while the
  *     descale is below 2^100), saturating at +-448 (infinities too); NaN stays NaN.
  * The outputs must not overlap the inputs, and no two tokens may share a cache slot.
