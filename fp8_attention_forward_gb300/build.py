@@ -82,7 +82,7 @@ def build_args():
             "-ltorch_cpu", "-lc10"]
     try:
         r = subprocess.run(cmd, capture_output=True, text=True)
-        failed = r.returncode != 0 and r.stdout + r.stderr
+        failed = (r.stdout + r.stderr or f"g++ returned {r.returncode}") if r.returncode else ""
     except OSError as e:
         failed = str(e)
     if failed:

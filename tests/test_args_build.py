@@ -26,7 +26,7 @@ def test_no_torch_no_module(monkeypatch):
     assert build.build_args() is None
 
 
-@pytest.mark.parametrize("how", ["fails", "is missing"])
+@pytest.mark.parametrize("how", ["fails", "fails silently", "is missing"])
 def test_a_compiler_that_does_not_work_leaves_the_library(how, monkeypatch, tmp_path):
     """build() goes on to link the library; an older module does not stay."""
     pytest.importorskip("torch")
@@ -40,7 +40,7 @@ def test_a_compiler_that_does_not_work_leaves_the_library(how, monkeypatch, tmp_
         if cmd[0] == "g++":
             if how == "is missing":
                 raise FileNotFoundError("g++")
-            return subprocess.CompletedProcess(cmd, 1, "", "no such header")
+            return subprocess.CompletedProcess(cmd, 1, "", "no such header" if how == "fails" else "")
         built.append(cmd)
         return run(["touch", cmd[cmd.index("-o") + 1]], **kw)
 
