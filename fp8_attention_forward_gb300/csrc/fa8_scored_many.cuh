@@ -1085,6 +1085,9 @@ __global__ void __launch_bounds__(kScThreads, 1)
                 bool prep = partial || k0 + kScTile > left;  // scores are changed in place first
                 if (!wait(BAR(C::B_SF + bar / 2), (uint32_t)(i / C::NSB) & 1u)) { ok = false; break; }
                 ptx::tc_fence_after();
+                // Rows that do not exist (heads that do not divide 128, positions past the request's) have scores of whatever
+                // lies in their place of Q: their maximum is -inf, so that the votes below, and with them the other rows'
+                // weights, do not depend on it.
                 float mx = -INFINITY;
                 if (!prep) {  // (the bias counts as the largest of the tile's)
 #pragma unroll 1
@@ -1095,7 +1098,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
                         ptx::reg_fence16(v);
                         mx = sc_max16(mx, v);
                     }
-                    prep = CAP && !__all_sync(0xffffffffu, mx * k2 <= 30.f);
+                    prep = CAP && !__all_sync(0xffffffffu, mx * k2 <= 30.f || !row_ok);
                     mx = CAP ? sc_cap(mx, k2, cap) : mx * c;
                     if (BIAS) mx += slope * (float)(k0 + (slope > 0.f ? kScTile - 1 : 0) - pc);
                 }
@@ -1146,6 +1149,8 @@ __global__ void __launch_bounds__(kScThreads, 1)
                     ptx::tmem_wait_st();
                 }
 
+                if (!row_ok) mx = -INFINITY;
+
                 // the maximum moves only when some row's score is 2^kScSlack above it; then O is scaled in TMEM
                 float now;
                 if (!take_m(i, &now)) { ok = false; break; }
@@ -1169,6 +1174,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
                             mx = fmaxf(mx, fmaf(slope, (float)(k0 + 16 * h + e - pc), z));
                         }
                     }
+                    if (!row_ok) mx = -INFINITY;
                     moved = __any_sync(0xffffffffu, mx > m + (kScBias + kScSlack));
                 }
                 float alpha = 1.f;
@@ -1195,7 +1201,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
                 }
                 // ---- P = 2^(z - m), over the scores
                 const float ref = m == -INFINITY ? 0.f : -m;
-                if (BIAS && __all_sync(0xffffffffu, mx < m - 40.f)) {  // all too small for f16, and 2^-47 of the largest in the sum
+                if (BIAS && __all_sync(0xffffffffu, mx < m - 40.f || !row_ok)) {  // all too small for f16, and 2^-47 of the largest in the sum
                     const uint32_t w[16] = {};
                     ptx::tmem_st16(scol, w);
                     ptx::tmem_st16(scol + 16, w);

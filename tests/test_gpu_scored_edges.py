@@ -1,0 +1,71 @@
+"""Attention with changed scores and of drafted trees where it can go wrong quietly: rows of a unit that do not exist, windows
+at the end of 32 bits, caps far above the scores, NaN values that cost time, slots and tokens past the drafted ones."""
+import math
+
+import pytest
+import torch
+
+from fp8_attention_forward_gb300 import fa8
+
+import scored_ref as R
+
+pytestmark = pytest.mark.gpu
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
+B16 = HALF[torch.bfloat16]
+
+
+@pytest.fixture(autouse=True)
+def no_errors():
+    fa8.check()
+    yield
+    assert fa8.check() == fa8.FA8_SUCCESS
+
+
+def slopes_of(n):
+    return (2.0 ** (-8.0 * torch.arange(1, n + 1) / n)).float()
+
+
+def call(p, **kw):
+    kw = {n: x.cuda() if isinstance(x, torch.Tensor) else x for n, x in kw.items()}
+    return fa8.fwd_scored(p.q.cuda(), p.k.cuda(), p.v.cuda(), **p.kw(), **kw)
+
+
+def same_bits(a, b):
+    return all(torch.equal(x.contiguous().view(torch.uint8), y.contiguous().view(torch.uint8)) for x, y in zip(a, b))
+
+
+# ------------------------------------------------------------------ rows that do not exist
+def leave_in_shared_memory(byte, D, DV):
+    """A call whose queries, all of this byte, fill every unit's 128 rows on every SM."""
+    blocks = 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    q = torch.full((1, 32 * blocks, 4, D), byte, dtype=torch.uint8, device="cuda").view(R.E4M3)
+    k = torch.zeros((1, 64, 1, D), dtype=torch.uint8, device="cuda").view(R.E4M3)
+    v = torch.zeros((1, 64, 1, DV), dtype=torch.uint8, device="cuda").view(R.E4M3)
+    fa8.fwd_scored(q, k, v)
+
+
+@pytest.mark.parametrize("G", [3, 5, 12])
+@pytest.mark.parametrize("D,DV", [(128, 128), (64, 64), (256, 256)])
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (20.0, False), (0.0, True), (20.0, True)])
+def test_equal_bits_whatever_shared_memory_held(G, D, DV, cap, bias):
+    """Heads that do not divide a unit's 128 rows leave some without a query: what is made of them changes nothing."""
+    for keys, m in (([900, 333], 200), ([5000], 60)):
+        p = R.Problem(keys, [m] * len(keys), Hq=2 * G, Hkv=2, D=D, DV=DV, seed=G)
+        got = []
+        for byte in (0x00, 0x7E, 0xFE, 0x7F):  # zeros, the largest, the smallest, NaN
+            leave_in_shared_memory(byte, D, DV)
+            got.append(call(p, softcap=cap, slopes=slopes_of(2 * G) if bias else None, causal=True))
+        assert all(same_bits(got[0], x) for x in got[1:])
+
+
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (20.0, False), (0.0, True), (20.0, True)])
+def test_a_packed_request_does_not_depend_on_the_next(cap, bias):
+    """The last rows of a packed request share a unit with queries of the next one, and those are not its own."""
+    p = R.Problem([700, 900], [37, 70], Hq=8, Hkv=2, packed=True, seed=1)
+    kw = dict(softcap=cap, slopes=slopes_of(8) if bias else None, causal=True)
+    got = []
+    for byte in (0x00, 0x7E, 0xFE, 0x7F):
+        p.q.view(torch.uint8)[37:] = byte
+        out, lse = call(p, **kw)
+        got.append((out[:37], lse[:, :37]))
+    assert all(same_bits(got[0], x) for x in got[1:])
