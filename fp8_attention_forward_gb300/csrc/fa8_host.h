@@ -64,6 +64,11 @@ struct Cluster16 {
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool supported_dims(int d, int dv);
+// The window that kernels get: one that no token's first key is behind is none (-1), since a position below zero less it
+// could pass 32 bits.  max_keys, tokens: the most of a request.
+inline int window_of(int window, long long max_keys, long long tokens) {
+    return window >= max_keys || window + tokens > 0x7fffffffLL ? -1 : window;
+}
 // A contiguous 1-D int32 tensor of n entries.
 fa8_status check_int_vec(const fa8_tensor *t, const char *name, long long n);
 // E4M3 payload: last dim contiguous, other strides positive multiples of 16 bytes, 16-byte base.

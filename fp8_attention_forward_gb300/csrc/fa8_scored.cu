@@ -318,7 +318,7 @@ extern "C" fa8_status fa8_fwd_scored(const fa8_tensor *q, const fa8_tensor *k, c
     if (causal != 0 && causal != 1) return fail(FA8_ERR_INVALID_ARG, "causal must be 0 or 1");
     if (window_left < -1) return fail(FA8_ERR_INVALID_ARG, "window_left must be -1 or >= 0");
     L.p.causal = causal;
-    L.p.window_left = window_left;
+    L.p.window_left = window_of(window_left, L.max_keys, L.qs.cu_q ? L.qs.T : L.qs.Sq);
     if (ranges) {
         if ((st = check_per_token(ranges, "ranges", L.qs, 2, L.p.r_s))) return st;
         if (!ranges->data && L.qs.T > 0) return fail(FA8_ERR_INVALID_ARG, "ranges needs data");

@@ -69,3 +69,15 @@ def test_a_packed_request_does_not_depend_on_the_next(cap, bias):
         out, lse = call(p, **kw)
         got.append((out[:37], lse[:, :37]))
     assert all(same_bits(got[0], x) for x in got[1:])
+
+
+# ------------------------------------------------------------------ windows at the end of 32 bits
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 3, 2 ** 31 - 100, 2 ** 30])
+@pytest.mark.parametrize("m,packed", [(4, False), (150, False), (150, True)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_a_window_without_end_and_more_tokens_than_keys(window, m, packed, causal):
+    """Positions below zero less such a window pass 32 bits; the tokens see what they see without a window."""
+    p = R.Problem([m - 2, 1, 40, 0], [m] * 4, Hq=4, Hkv=1, seed=m, packed=packed)
+    for cap, slopes in ((3.0, None), (0.0, slopes_of(4))):
+        want = R.attend(p, cap=cap, slopes=slopes, causal=causal, window=window)
+        R.check(p, call(p, softcap=cap, slopes=slopes, causal=causal, window_left=window), want, B16)
