@@ -872,7 +872,7 @@ fa8_status fa8_fwd(const fa8_tensor *q, const fa8_tensor *k, const fa8_tensor *v
     }
     p.scale_log2 = softmax_scale * 1.4426950408889634f;
     p.causal = causal;
-    p.window_left = window_left;
+    p.window_left = window_of(window_left, pl.max_lk, pl.q_varlen ? pl.total_q : pl.Sq);
     p.num_splits = pl.splits;
     p.split_mode = pl.splits > 1;
     p.units = (int)std::min<long long>(pl.units, 0x7fffffffLL);

@@ -81,3 +81,17 @@ def test_a_window_without_end_and_more_tokens_than_keys(window, m, packed, causa
     for cap, slopes in ((3.0, None), (0.0, slopes_of(4))):
         want = R.attend(p, cap=cap, slopes=slopes, causal=causal, window=window)
         R.check(p, call(p, softcap=cap, slopes=slopes, causal=causal, window_left=window), want, B16)
+
+
+# ------------------------------------------------------------------ the forward's window
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 3, 2 ** 30])
+@pytest.mark.parametrize("D,m", [(128, 2), (128, 150), (192, 150)])
+@pytest.mark.parametrize("layout,packed", [("dense", False), ("paged", False), ("varlen", True)])
+def test_the_forward_under_a_window_without_end(window, D, m, layout, packed):
+    """fa8_fwd likewise: the same bits as without a window."""
+    keys = [max(1, m - 60)] * 3 if layout == "dense" else [max(0, m - 60), 1, 40]
+    p = R.Problem(keys, [m] * 3, Hq=4, Hkv=1, D=D, DV=D, layout=layout, packed=packed, seed=m)
+    q, k, v, kw = p.q.cuda(), p.k.cuda(), p.v.cuda(), p.kw()
+    for causal in (True, False):
+        a, b = (fa8.fwd(q, k, v, causal=causal, window_left=w, **kw) for w in (window, -1))
+        assert same_bits(a, b)
