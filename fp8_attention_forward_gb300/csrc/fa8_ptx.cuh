@@ -220,6 +220,10 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         : FA8_R8(r, 0), FA8_R8(r, 8)
         : "r"(taddr));
 }
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];" : FA8_R8(r, 0) : "r"(taddr));
+}
+__device__ __forceinline__ void reg_fence8(uint32_t (&r)[8]) { asm volatile("" : FA8_P8(r, 0)); }
 __device__ __forceinline__ void reg_fence16(uint32_t (&r)[16]) {
     asm volatile("" : FA8_P8(r, 0), FA8_P8(r, 8));
 }

@@ -228,7 +228,7 @@ fa8_status forward(Launch *L, const fa8_tensor *q, const fa8_tensor *k, const fa
     if (softmax_scale <= 0.f) softmax_scale = 1.0f / std::sqrt((float)qs.D);
     p.scale_log2 = softmax_scale * 1.4426950408889634f;
     p.cap_log2 = softcap * 1.4426950408889634f;
-    if (softcap > 0.f && !(p.cap_log2 >= 0x1p-100f && p.cap_log2 <= 0x1p100f)) return fail(FA8_ERR_UNSUPPORTED, "softcap is out of range");
+    if (softcap > 0.f && p.cap_log2 < 0x1p-100f) return fail(FA8_ERR_UNSUPPORTED, "softcap is out of range");
     if ((st = plan(L, p.ranges != nullptr, 1))) return st;  // refuses what no device takes
     if (qs.T == 0) return FA8_SUCCESS;
     if (!q->data || !out->data || (lse && !lse->data) || (p.has_kv && (!k->data || !v->data)))

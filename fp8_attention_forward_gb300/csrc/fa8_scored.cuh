@@ -136,16 +136,28 @@ __device__ __forceinline__ uint32_t sc_see32(const ScRow &r, int words, int k) {
     return m;
 }
 
-// cap tanh(s k): with t = 2^(-2 |x| log2 e), tanh |x| = (1 - t) / (1 + t), to 2^-22 absolutely.
-// k2 = 2 log2(e) scale / cap.
 __device__ __forceinline__ float rcp(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ float sc_cap(float s, float k2, float cap) {
+// cap tanh(z / cap) of z = s c, with k2 = 2 log2(e) c / cap.  With t = 2^(-|s k2|), tanh |x| = (1 - t) / (1 + t), to 2^-22
+// absolutely: of a cap far above the scores that is more than the scores' own rounding.
+__device__ __forceinline__ float sc_cap_near(float s, float k2, float cap) {
     const float x = s * k2, t = ptx::ex2(-fabsf(x));
     return copysignf(cap, x) * ((1.f - t) * rcp(1.f + t));
+}
+// Caps above 128, in log2 units, need more than that (sc_cap).
+constexpr float kFarCap = 128.01f * kLog2e;
+// To 2^-20 of itself: below a quarter of the cap 1 - t would cancel, and z is multiplied by the series of tanh(x) / x,
+// 1 - x^2 / 3 + 2 x^4 / 15 - 17 x^6 / 315 + 62 x^8 / 2835, whose next term is under 2^-26 there.
+constexpr float kCapSeries = 0.25f * 2.f * kLog2e;  // |s k2| up to which
+__device__ __forceinline__ float sc_cap_series(float s, float c, float k2) {
+    const float x = s * k2, w = x * x * (0.25f * kLn2 * kLn2);
+    return s * c * fmaf(w, fmaf(w, fmaf(w, fmaf(w, 62.f / 2835.f, -17.f / 315.f), 2.f / 15.f), -1.f / 3.f), 1.f);
+}
+__device__ __forceinline__ float sc_cap(float s, float c, float k2, float cap) {
+    return fabsf(s * k2) < kCapSeries ? sc_cap_series(s, c, k2) : sc_cap_near(s, k2, cap);
 }
 
 // The row's bias is -slope |pos - j|.  Seen from pc = pos moved into [lo, hi), which keeps its products

@@ -273,13 +273,20 @@ __global__ void __launch_bounds__(32 * PW, FewCfg<D, DV, NT, PW>::CTAS)
             fetch_k();
         }
         // ---- scores in log2 units: element [x][t][2 h + e] is key 16 x + 8 h + r, row 8 t + 2 c + e
-        if (cap > 0.f) {
+        if (cap > kFarCap) {
 #pragma unroll
             for (int x = 0; x < C::MT; ++x)
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[x][t][e] = sc_cap(s[x][t][e], k2, cap);
+                    for (int e = 0; e < 4; ++e) s[x][t][e] = sc_cap(s[x][t][e], cs, k2, cap);
+        } else if (cap > 0.f) {
+#pragma unroll
+            for (int x = 0; x < C::MT; ++x)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[x][t][e] = sc_cap_near(s[x][t][e], k2, cap);
         } else {
 #pragma unroll
             for (int x = 0; x < C::MT; ++x)

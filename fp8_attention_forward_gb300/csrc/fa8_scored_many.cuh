@@ -334,7 +334,7 @@ __device__ __forceinline__ void sc_split(uint64_t y, uint32_t *u) {
     u[0] = __float_as_uint(a);
     u[1] = __float_as_uint(b);
 }
-// 1 / (1 + e^(2 x)) of four scores, x = s k / cap as in sc_cap: tanh x = 1 - 2 / (1 + e^(2 x)) to 2^-22 absolutely.  They
+// 1 / (1 + e^(2 x)) of four scores, x = s k / cap as in sc_cap_near: tanh x = 1 - 2 / (1 + e^(2 x)) to 2^-22 absolutely.  They
 // share one reciprocal, which e^(2 x) of at most 2^30 keeps in range (CUT: larger ones are cut there); a NaN
 // reaches all four.
 template <bool CUT>
@@ -373,6 +373,7 @@ __device__ __forceinline__ float sc_max16(float m, const uint32_t (&u)[16]) {
 }
 // How a tile's scores become weights 2^z: z = u c + ref; with the cap; u + ref of scores changed in place; and
 // the first two with a bias that grows by `slope` per key.
+enum { kScNoCap, kScNearCap, kScFarCap };  // of the kernels: up to kFarCap, above
 enum { kScPlain, kScCap, kScDone, kScBiased, kScCapBiased };
 // P of 16 keys: 8 columns of f16 pairs, the unrounded weights into two sums.  r: what every two keys add; bias2:
 // its growth over four.
@@ -436,6 +437,33 @@ __device__ __forceinline__ void sc_p64(uint32_t scol, float c, float ref, float 
     l2 = ptx::fadd2(acc0, acc1);
 }
 
+// The tile's scores, in log2 units and capped in place, to 2^-20 of themselves.  Two exponentials and a shared reciprocal are
+// good to 2^-20 of the cap, at 128 half of the weights' rounding; caps above that (kFarCap) take this pass of their own and go
+// on as scores without one (two causal prompts of 4096, a cap of 1000: 412 us, of 50 338).
+__device__ __forceinline__ void sc_cap64(uint32_t scol, float c, float k2, float cap) {
+#pragma unroll 1
+    for (int h = 0; h < kScTile; h += 8) {
+        uint32_t v[8];
+        ptx::tmem_ld8(scol + h, v);
+        ptx::tmem_wait_ld();
+        ptx::reg_fence8(v);
+        float s[8], x = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            s[e] = u2f(v[e]);
+            x = sc_max3(x, fabsf(s[e] * k2), x);
+            v[e] = __float_as_uint(sc_cap_series(s[e], c, k2));
+        }
+        if (!__all_sync(0xffffffffu, x < kCapSeries)) {  // (rare under a cap of this size)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (!(fabsf(s[e] * k2) < kCapSeries)) v[e] = __float_as_uint(sc_cap_near(s[e], k2, cap));
+        }
+        ptx::tmem_st8(scol + h, v);
+    }
+    ptx::tmem_wait_st();
+}
+
 // A bounded wait.  The timer is asked once in 256 tries: reading it takes longer than most waits.
 __device__ __forceinline__ bool sc_wait_lane(uint32_t bar, uint32_t parity, uint32_t abort_saddr, unsigned long long timeout,
                                              unsigned int *status) {
@@ -487,12 +515,14 @@ __device__ __forceinline__ bool sc_take(uint32_t saddr, uint32_t n, float *m, ui
     return __all_sync(0xffffffffu, ok);
 }
 
-// CAP, BIAS: kernels of their own (either in the other's code: d = 64 with slopes 239 us)
-template <int D, int DV, bool CAP, bool BIAS>
+// CAPS, BIAS: kernels of their own (slopes in the other kernels' code: d = 64 with slopes 239 us; far caps in the near ones':
+// capped prompt 350 beside 337)
+template <int D, int DV, int CAPS, bool BIAS>
 __global__ void __launch_bounds__(kScThreads, 1)
     scored_kernel(const __grid_constant__ ScoredParams p, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v) {
     using C = ScCfg<D, DV>;
+    constexpr bool CAP = CAPS == kScNearCap, FAR = CAPS == kScFarCap;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -1063,7 +1093,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
                 slope = x.slope;
                 pc = x.pc;
             }
-            const float c = u.scale, cap = p.cap_log2, k2 = CAP ? 2.f * kLog2e * c / cap : 0.f;
+            const float c = FAR ? 1.f : u.scale, cap = p.cap_log2, k2 = CAPS != kScNoCap ? 2.f * kLog2e * u.scale / cap : 0.f;
             // tiles in [flo, fhi) need no mask in this warp; those that end before `left` lie left of all its positions
             const int flo = __reduce_max_sync(0xffffffffu, row.lo), fhi = __reduce_min_sync(0xffffffffu, min(row.hi, max(0, row.lp)));
             // (a negative scale, whose largest score is not the largest product's, has every tile's changed first)
@@ -1085,6 +1115,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
                 bool prep = partial || k0 + kScTile > left;  // scores are changed in place first
                 if (!wait(BAR(C::B_SF + bar / 2), (uint32_t)(i / C::NSB) & 1u)) { ok = false; break; }
                 ptx::tc_fence_after();
+                if (FAR) sc_cap64(scol, u.scale, k2, cap);
                 // Rows that do not exist (heads that do not divide 128, positions past the request's) have scores of whatever
                 // lies in their place of Q: their maximum is -inf, so that the votes below, and with them the other rows'
                 // weights, do not depend on it.
@@ -1099,7 +1130,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
                         mx = sc_max16(mx, v);
                     }
                     prep = CAP && !__all_sync(0xffffffffu, mx * k2 <= 30.f || !row_ok);
-                    mx = CAP ? sc_cap(mx, k2, cap) : mx * c;
+                    mx = CAP ? sc_cap_near(mx, k2, cap) : mx * c;
                     if (BIAS) mx += slope * (float)(k0 + (slope > 0.f ? kScTile - 1 : 0) - pc);
                 }
                 if (prep) {
@@ -1170,7 +1201,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
                         ptx::reg_fence16(v);
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            const float z = CAP ? sc_cap(u2f(v[e]), k2, cap) : u2f(v[e]) * c;
+                            const float z = CAP ? sc_cap_near(u2f(v[e]), k2, cap) : u2f(v[e]) * c;
                             mx = fmaxf(mx, fmaf(slope, (float)(k0 + 16 * h + e - pc), z));
                         }
                     }
@@ -1314,7 +1345,7 @@ __global__ void __launch_bounds__(128) scored_merge_kernel(const __grid_constant
     store8(dst, o, p.out_fp16);
 }
 
-template <int D, int DV, bool CAP, bool BIAS>
+template <int D, int DV, int CAPS, bool BIAS>
 fa8_status launch_scored_mode(const ScoredParams &p, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, int grid, int dev,
                               cudaStream_t s) {
     using C = ScCfg<D, DV>;
@@ -1323,14 +1354,14 @@ fa8_status launch_scored_mode(const ScoredParams &p, const CUtensorMap &tq, cons
     // setmaxnreg draws on the registers of the launch: a count that the split was not planned for would wait forever
     if (regs < 0) {
         cudaFuncAttributes a;
-        const cudaError_t e = cudaFuncGetAttributes(&a, scored_kernel<D, DV, CAP, BIAS>);
+        const cudaError_t e = cudaFuncGetAttributes(&a, scored_kernel<D, DV, CAPS, BIAS>);
         if (e != cudaSuccess) return host::cuda_fail(e, "scored attention kernel");
         regs = a.numRegs;
     }
     if (regs != kScRegs) return host::fail(FA8_ERR_CUDA, "scored attention kernel compiled to %d registers, %d planned", regs.load(), kScRegs);
-    cudaError_t e = opt_in(scored_kernel<D, DV, CAP, BIAS>, C::SMEM_BYTES, dev);
+    cudaError_t e = opt_in(scored_kernel<D, DV, CAPS, BIAS>, C::SMEM_BYTES, dev);
     if (e != cudaSuccess) return host::cuda_fail(e, "scored attention shared memory");
-    scored_kernel<D, DV, CAP, BIAS><<<grid, kScThreads, C::SMEM_BYTES, s>>>(p, tq, tk, tv);
+    scored_kernel<D, DV, CAPS, BIAS><<<grid, kScThreads, C::SMEM_BYTES, s>>>(p, tq, tk, tv);
     e = cudaGetLastError();
     if (e == cudaSuccess && p.split && grid > 1) {
         cudaLaunchConfig_t cfg = {};
@@ -1351,10 +1382,13 @@ fa8_status launch_scored_mode(const ScoredParams &p, const CUtensorMap &tq, cons
     template <>                                                                                                                    \
     fa8_status launch_scored_many<D_, DV_>(ScoredParams & p, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,  \
                                            int grid, int dev, cudaStream_t s) {                                                    \
-        if (p.slopes && p.cap_log2 > 0) return launch_scored_mode<D_, DV_, true, true>(p, tq, tk, tv, grid, dev, s);               \
-        if (p.slopes) return launch_scored_mode<D_, DV_, false, true>(p, tq, tk, tv, grid, dev, s);                                \
-        if (p.cap_log2 > 0) return launch_scored_mode<D_, DV_, true, false>(p, tq, tk, tv, grid, dev, s);                          \
-        return launch_scored_mode<D_, DV_, false, false>(p, tq, tk, tv, grid, dev, s);                                             \
+        const int caps = p.cap_log2 > kFarCap ? kScFarCap : (p.cap_log2 > 0.f ? kScNearCap : kScNoCap);                            \
+        if (p.slopes && caps == kScFarCap) return launch_scored_mode<D_, DV_, kScFarCap, true>(p, tq, tk, tv, grid, dev, s);       \
+        if (p.slopes && caps == kScNearCap) return launch_scored_mode<D_, DV_, kScNearCap, true>(p, tq, tk, tv, grid, dev, s);     \
+        if (p.slopes) return launch_scored_mode<D_, DV_, kScNoCap, true>(p, tq, tk, tv, grid, dev, s);                             \
+        if (caps == kScFarCap) return launch_scored_mode<D_, DV_, kScFarCap, false>(p, tq, tk, tv, grid, dev, s);                  \
+        if (caps == kScNearCap) return launch_scored_mode<D_, DV_, kScNearCap, false>(p, tq, tk, tv, grid, dev, s);                \
+        return launch_scored_mode<D_, DV_, kScNoCap, false>(p, tq, tk, tv, grid, dev, s);                                          \
     }
 
 }  // namespace fa8

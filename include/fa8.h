@@ -327,7 +327,7 @@ FA8_API fa8_status fa8_fwd_pages(const fa8_tensor *q, const fa8_tensor *k, const
  * fa8_fwd_scored -- the attention of fa8_fwd with
  *   z = softmax_scale dq dk q.k,  z = softcap tanh(z / softcap),  z = z - slopes[h] |pos - j|
  * in place of the scaled score, j the key's index in its request and pos = i + Lk - Lq the token's (either change
- * only where it is asked for; tanh is within 2^-22 absolutely).
+ * only where it is asked for; a capped score is within 2^-20 of itself, or of the cap where that is up to 128).
  *   softcap: 0 = none, else positive.
  *   slopes: fp32 (Hq,), contiguous; NULL = none.
  *   causal, window_left: as in fa8_fwd.

@@ -95,3 +95,23 @@ def test_the_forward_under_a_window_without_end(window, D, m, layout, packed):
     for causal in (True, False):
         a, b = (fa8.fwd(q, k, v, causal=causal, window_left=w, **kw) for w in (window, -1))
         assert same_bits(a, b)
+
+
+# ------------------------------------------------------------------ large caps
+@pytest.mark.parametrize("cap", [30.0, 128.0, 129.0, 1e3, 1e4, 1e6, 1e8, 1e12, 1e30])
+@pytest.mark.parametrize("m", [1, 3, 40, 150])
+@pytest.mark.parametrize("scale", [0.0, 1.0, 8.0])
+@pytest.mark.parametrize("bias", [False, True])
+def test_caps_far_above_the_scores(cap, m, scale, bias):
+    """A cap of more than 128 costs a score 2^-20 of itself at the most, whatever the cap is; smaller ones 2^-20 of the cap:
+    a reciprocal and an exponential of 2^-22 each, the second weighed by at most a quarter, and six products and sums of
+    2^-24 of at most twice the value."""
+    p = R.Problem([300, 40], [m] * 2, Hq=4, Hkv=1, D=128, DV=128, seed=3)
+    slopes = slopes_of(4) if bias else None
+    o, lse, mag, _ = R.attend(p, cap=cap, slopes=slopes, scale=scale, causal=True)
+    err = R.attend(p, slopes=slopes, scale=scale, causal=True)[3]
+    for b in range(2):
+        f = (p.dq[b, 0] * p.dk[b, 0]).double() * (scale or 1.0 / math.sqrt(p.D))
+        z = (torch.einsum("ihd,jd->hij", p.q[b].double(), p.kl[b][:, 0].double()) * f).abs().amax(-1)
+        err[b] += 2.0 ** -20 * (z.clamp(max=cap) if cap > 128 else cap)
+    R.check(p, call(p, softcap=cap, slopes=slopes, softmax_scale=scale, causal=True), (o, lse, mag, err), B16)
