@@ -141,6 +141,8 @@ __device__ __forceinline__ float rcp(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// 2 log2(e) c / cap, finite for the least caps too: a score of zero stays zero.
+__device__ __forceinline__ float sc_k2(float c, float cap) { return fminf(fmaxf(2.f * kLog2e * c / cap, -0x1p100f), 0x1p100f); }
 // cap tanh(z / cap) of z = s c, with k2 = 2 log2(e) c / cap.  With t = 2^(-|s k2|), tanh |x| = (1 - t) / (1 + t), to 2^-22
 // absolutely: of a cap far above the scores that is more than the scores' own rounding.
 __device__ __forceinline__ float sc_cap_near(float s, float k2, float cap) {

@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(32 * PW, FewCfg<D, DV, NT, PW>::CTAS)
     __syncthreads();
     float cs = p.scale_log2 * dqv * dkv;
     if (cs == 0.f) cs = 0x1p-126f;  // below fp32: a masked -inf must stay one
-    const float cap = p.cap_log2, k2 = cap > 0.f ? 2.f * kLog2e * cs / cap : 0.f;
+    const float cap = p.cap_log2, k2 = cap > 0.f ? sc_k2(cs, cap) : 0.f;
     float slope[NT][2];
     int pc[NT][2];
 #pragma unroll

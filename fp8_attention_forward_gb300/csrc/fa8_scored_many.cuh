@@ -1093,7 +1093,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
                 slope = x.slope;
                 pc = x.pc;
             }
-            const float c = FAR ? 1.f : u.scale, cap = p.cap_log2, k2 = CAPS != kScNoCap ? 2.f * kLog2e * u.scale / cap : 0.f;
+            const float c = FAR ? 1.f : u.scale, cap = p.cap_log2, k2 = CAPS != kScNoCap ? sc_k2(u.scale, cap) : 0.f;
             // tiles in [flo, fhi) need no mask in this warp; those that end before `left` lie left of all its positions
             const int flo = __reduce_max_sync(0xffffffffu, row.lo), fhi = __reduce_min_sync(0xffffffffu, min(row.hi, max(0, row.lp)));
             // (a negative scale, whose largest score is not the largest product's, has every tile's changed first)

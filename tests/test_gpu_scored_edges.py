@@ -115,3 +115,12 @@ def test_caps_far_above_the_scores(cap, m, scale, bias):
         z = (torch.einsum("ihd,jd->hij", p.q[b].double(), p.kl[b][:, 0].double()) * f).abs().amax(-1)
         err[b] += 2.0 ** -20 * (z.clamp(max=cap) if cap > 128 else cap)
     R.check(p, call(p, softcap=cap, slopes=slopes, softmax_scale=scale, causal=True), (o, lse, mag, err), B16)
+
+
+# ------------------------------------------------------------------ tiny caps
+@pytest.mark.parametrize("m", [1, 40])
+def test_a_tiny_cap_under_a_huge_scale(m):
+    """scale / cap past fp32: scores of zero stay zero, the others are the cap."""
+    p = R.Problem([300, 40], [m] * 2, Hq=4, Hkv=1, D=64, DV=64, seed=3)
+    p.q.view(torch.uint8)[:, :, 1] = 0
+    R.check(p, call(p, softcap=1e-30, softmax_scale=1e12, causal=True), R.attend(p, cap=1e-30, scale=1e12, causal=True), B16)
