@@ -220,22 +220,17 @@ __device__ __forceinline__ const uint8_t *sc_v_row(const ScoredParams &p, int b,
     }
     return p.v + page * p.v_s[0] + row * p.v_s[1] + kvh * p.v_s[2];
 }
-// Bit c: whether any of the keys in [j0, j1) that the row sees has a NaN in channel d0 + c (32 of them).
-// Only where a NaN has been met among keys that some rows of a tile see and others do not: it went into
-// the products as zero there.
-static __device__ __noinline__ uint32_t sc_nan32(const ScoredParams &p, int b, const ScReq &rq, const ScRow &row, int kvh, int j0, int j1, int d0) {
-    uint32_t found = 0;
-    for (int j = max(j0, row.lo); j < min(j1, row.hi); ++j) {
-        if (!sc_sees(row, p.words, j)) continue;
-        const uint8_t *v = sc_v_row(p, b, rq, kvh, j);
-        if (!v) continue;
-        for (int c = 0; c < 32; c += 4) {
-            const uint32_t w = *reinterpret_cast<const uint32_t *>(v + d0 + c);
-            const uint32_t n = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-            found |= ((n >> 7 & 1u) | (n >> 14 & 2u) | (n >> 21 & 4u) | (n >> 28 & 8u)) << c;
-        }
+// NaNs of V in tiles that some rows see and others do not go into the products as zeros there: a masked weight of zero would not
+// silence them.  The rows that see them get them at the end.
+// 16 bytes of V: bit c, whether channel c holds a NaN.
+__device__ __forceinline__ uint32_t sc_nans(const uint32_t (&w)[4]) {
+    uint32_t bits = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const uint32_t n = ((w[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+        bits |= ((n >> 7 & 1u) | (n >> 14 & 2u) | (n >> 21 & 4u) | (n >> 28 & 8u)) << (4 * e);
     }
-    return found;
+    return bits;
 }
 
 template <int D, int DV>

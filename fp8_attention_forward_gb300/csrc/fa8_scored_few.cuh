@@ -61,6 +61,37 @@ struct FewCfg {
     }
 };
 
+// Notes, for each row that sees one, the channels of the NaNs in V's chunks of kc keys that are marked (modulo 32): chunk it
+// begins at key k0 + it * step.  A lane looks through a key.  Whole warp.
+template <int DV>
+static __device__ __noinline__ void few_nans(const ScoredParams &p, int b, int kvh, int k0, int step, int kc, int chunks, const uint8_t *marked,
+                                             uint32_t *s_bad) {
+    const int lane = threadIdx.x & 31;
+    ScReq rq;
+    sc_lengths(p, b, &rq);
+    for (int it = 0; it < chunks; ++it) {
+        if (!marked[it & 31]) continue;
+        for (int h = lane; h < kc; h += 32) {
+            const int j = k0 + it * step + h;
+            const uint8_t *v = j < rq.Lk ? sc_v_row(p, b, rq, kvh, j) : nullptr;
+            if (!v) continue;
+            uint32_t bits[DV / 32], any = 0;
+#pragma unroll
+            for (int w = 0; w < DV / 32; ++w) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(v + 32 * w), y = *reinterpret_cast<const uint4 *>(v + 32 * w + 16);
+                any |= bits[w] = sc_nans({x.x, x.y, x.z, x.w}) | sc_nans({y.x, y.y, y.z, y.w}) << 16;
+            }
+            for (int i = 0; any && i < p.Sq; ++i) {
+                if (!sc_sees(sc_row(p, b, rq, i), p.words, j)) continue;
+                for (int rw = i * p.G; rw < (i + 1) * p.G; ++rw)
+#pragma unroll
+                    for (int w = 0; w < DV / 32; ++w)
+                        if (bits[w] & ~*reinterpret_cast<volatile uint32_t *>(s_bad + rw * (DV / 32) + w)) atomicOr(s_bad + rw * (DV / 32) + w, bits[w]);
+            }
+        }
+    }
+}
+
 template <int D, int DV, int NT, int PW>
 __global__ void __launch_bounds__(32 * PW, FewCfg<D, DV, NT, PW>::CTAS)
     scored_few_kernel(const __grid_constant__ ScoredParams p, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
@@ -70,7 +101,9 @@ __global__ void __launch_bounds__(32 * PW, FewCfg<D, DV, NT, PW>::CTAS)
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     __shared__ __align__(8) uint64_t s_bar[PW][2];
     __shared__ int s_abort, s_nan;
+    __shared__ __align__(4) uint8_t s_noted[32 * PW];  // each warp's chunks with NaNs, modulo 32
     __shared__ float s_m[C::ROWS], s_l[C::ROWS];
+    __shared__ uint32_t s_bad[C::ROWS * (DV / 32)];  // channels of the rows' outputs that are NaN
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int r = lane >> 2, c = lane & 3;
     const int CS = p.cluster;
@@ -90,6 +123,9 @@ __global__ void __launch_bounds__(32 * PW, FewCfg<D, DV, NT, PW>::CTAS)
             ptx::prefetch_tmap(&tm_v);
         }
     }
+    if (tid < C::ROWS * (DV / 32)) s_bad[tid] = 0;
+    static_assert(C::ROWS * (DV / 32) <= kThreads, "one each");
+    s_noted[tid] = 0;
     const uint32_t bar_k = ptx::smem_u32(s_bar[warp]), bar_v = bar_k + 8;
     if (lane == 0) {
         ptx::mbar_init(bar_k, 1);
@@ -408,7 +444,7 @@ __global__ void __launch_bounds__(32 * PW, FewCfg<D, DV, NT, PW>::CTAS)
                             w.w[e] &= ~((n >> 7) * 0xffu);
                         }
                         if (bad) {
-                            s_nan = 1;
+                            s_noted[32 * warp + (it & 31)] = 1;
                             ptx::st_shared_v4(a, w.w[0], w.w[1], w.w[2], w.w[3]);
                         }
                     }
@@ -457,6 +493,10 @@ __global__ void __launch_bounds__(32 * PW, FewCfg<D, DV, NT, PW>::CTAS)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) wo[(warp * C::ROWS + rw) * C::OPITCH + 16 * d + 8 * h + r] = o[d][t][2 * h + e];
         }
+    if (__any_sync(0xffffffffu, s_noted[32 * warp + lane])) {
+        s_nan = 1;
+        few_nans<DV>(p, b, kvh, (c0 + first) * C::KC, stride * C::KC, C::KC, chunks, s_noted + 32 * warp, s_bad);
+    }
     __syncthreads();
     for (int x = tid; x < rows * (DV / 2); x += kThreads) {
         const int rw = x / (DV / 2), d = 2 * (x - rw * (DV / 2));
@@ -513,14 +553,13 @@ __global__ void __launch_bounds__(32 * PW, FewCfg<D, DV, NT, PW>::CTAS)
             a1 = wo[rw * C::OPITCH + d + 1];
         }
         const int i = rw / p.G, hq = h0 + rw % p.G;
-        if (p.slopes || nan) {
-            const ScRow y = sc_row(p, b, rq, i);
-            if (p.slopes) M += sc_bias(p, y, i + rq.Lk - rq.Lq, hq).off;
-            if (nan) {
-                const uint32_t bad = sc_nan32(p, b, rq, y, kvh, slo, shi, d & ~31) >> (d & 31);
-                if (bad & 1u) a0 = NAN;
-                if (bad & 2u) a1 = NAN;
-            }
+        if (p.slopes) M += sc_bias(p, sc_row(p, b, rq, i), i + rq.Lk - rq.Lq, hq).off;
+        if (nan) {
+            const int word = rw * (DV / 32) + d / 32;
+            uint32_t bad = s_bad[word];
+            for (int k = 0; CS > 1 && k < CS; ++k) bad |= __float_as_uint(ld_cluster_f32(map_rank(ptx::smem_u32(s_bad + word), k)));
+            if (bad >> (d & 31) & 1u) a0 = NAN;
+            if (bad >> (d & 31) & 2u) a1 = NAN;
         }
         if (p.parts > 1) {
             const long long at = (long long)(blockIdx.x / CS) * rows + rw;

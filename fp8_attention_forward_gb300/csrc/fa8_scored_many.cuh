@@ -90,9 +90,9 @@ struct ScCfg {
     static constexpr int OFF_L = OFF_M + 1024;        // (maximum, sum) [unit parity][group][128]
     static constexpr int OFF_UNIT = OFF_L + 2048 * kScGroups;  // [kScUnits]: the unit, what its positions see [128] (lo, hi)
     static constexpr int OFF_ROWS = OFF_UNIT + 64 * kScUnits;
-    static constexpr int OFF_NAN = OFF_ROWS + 1024 * kScUnits;  // [kScUnits][widening warp] bytes
-    static constexpr int OFF_CL = (OFF_NAN + 4 * kScUnits + 15) / 16 * 16, OFF_SLOT = OFF_CL + 16, OFF_ABORT = OFF_SLOT + 4;
-    static_assert(OFF_UNIT % 16 == 0 && NUM_BARS * 8 <= OFF_M && OFF_ABORT + 4 <= MISC_BYTES, "misc area");
+    static constexpr int OFF_NAN = OFF_ROWS + 1024 * kScUnits;  // [kScUnits][widening warp]: tiles with NaNs, modulo 64
+    static constexpr int OFF_CL = OFF_NAN + 32 * kScUnits, OFF_SLOT = OFF_CL + 16, OFF_ABORT = OFF_SLOT + 4;
+    static_assert(OFF_UNIT % 16 == 0 && OFF_CL % 16 == 0 && NUM_BARS * 8 <= OFF_M && OFF_ABORT + 4 <= MISC_BYTES, "misc area");
 };
 
 // ---------------------------------------------------------------- units
@@ -464,6 +464,59 @@ __device__ __forceinline__ void sc_cap64(uint32_t scol, float c, float k2, float
     ptx::tmem_wait_st();
 }
 
+// NaNs of V in the noted tiles of unit un, into the outputs of those of the warp's rows (r) that see them, or into their parts, after
+// these have been written: the next unit's products do not wait for it.  A lane looks through a key.  Whole warp.
+template <typename C, int DV>
+static __device__ __noinline__ void sc_put_nans(const ScoredParams &p, const uint8_t *misc, uint32_t un, int r) {
+    constexpr int W = DV / 32;
+    const ScUnit &u = *reinterpret_cast<const ScUnit *>(misc + C::OFF_UNIT + 64 * (un % kScUnits));
+    const unsigned long long *noted = reinterpret_cast<const unsigned long long *>(misc + C::OFF_NAN) + 4 * (un % kScUnits);
+    const int lane = threadIdx.x & 31, nt = u.t1 - u.t0, i = u.pos0 + r / p.G;
+    const bool row_ok = r < p.P * p.G && i < u.rq.Lq;
+    ScRow row = {0, 0, 0, nullptr};
+    if (row_ok) row = sc_row(p, u.b, u.rq, i);
+    uint32_t bad[W] = {};
+    if (!__any_sync(0xffffffffu, row_ok)) return;
+    for (unsigned long long tiles = noted[0] | noted[1] | noted[2] | noted[3]; tiles; tiles &= tiles - 1) {
+        for (int t = __ffsll((long long)tiles) - 1; t < nt; t += 64) {
+            for (int h = 0; h < kScTile; h += 32) {
+                const int k = (u.t1 - 1 - t) * kScTile + h;
+                const uint8_t *v = k + lane < u.rq.Lk ? sc_v_row(p, u.b, u.rq, u.kvh, k + lane) : nullptr;
+                uint32_t bits[W], any = 0;
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    bits[w] = 0;
+                    if (v) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(v + 32 * w), y = *reinterpret_cast<const uint4 *>(v + 32 * w + 16);
+                        bits[w] = sc_nans({x.x, x.y, x.z, x.w}) | sc_nans({y.x, y.y, y.z, y.w}) << 16;
+                    }
+                    any |= bits[w];
+                }
+                for (uint32_t m = __ballot_sync(0xffffffffu, any != 0); m; m &= m - 1) {
+                    const int l = __ffs(m) - 1;
+                    const bool sees = sc_sees(row, p.words, k + l);
+#pragma unroll
+                    for (int w = 0; w < W; ++w) {
+                        const uint32_t x = __shfl_sync(0xffffffffu, bits[w], l);
+                        if (sees) bad[w] |= x;
+                    }
+                }
+            }
+        }
+    }
+    if (!row_ok) return;
+    const int hq = u.kvh * p.G + r % p.G;
+    uint16_t *out = static_cast<uint16_t *>(p.o) + (p.cu_q ? 0 : u.b) * p.o_s[0] + ((long long)u.rq.q0 + i) * p.o_s[1] + (long long)hq * p.o_s[2];
+    float *part = u.slot >= 0 ? p.part + ((long long)u.slot * 128 * (DV / 4) + r) * 4 : nullptr;
+#pragma unroll
+    for (int w = 0; w < W; ++w)
+        for (uint32_t m = bad[w]; m; m &= m - 1) {
+            const int c = 32 * w + __ffs(m) - 1;
+            if (part) part[(c / 4) * 128 * 4 + c % 4] = NAN;
+            else out[c] = 0x7fff;  // of bf16 and of fp16
+        }
+}
+
 // A bounded wait.  The timer is asked once in 256 tries: reading it takes longer than most waits.
 __device__ __forceinline__ bool sc_wait_lane(uint32_t bar, uint32_t parity, uint32_t abort_saddr, unsigned long long timeout,
                                              unsigned int *status) {
@@ -531,7 +584,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
     auto BAR = [&](int i) -> uint32_t { return bar0 + 8u * (uint32_t)i; };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc + C::OFF_SLOT);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + C::OFF_ABORT);
-    volatile uint8_t *nan_flag = misc + C::OFF_NAN;
+    volatile unsigned long long *nan_tiles = reinterpret_cast<volatile unsigned long long *>(misc + C::OFF_NAN);
     const uint32_t sQ = ptx::smem_u32(smem + C::OFF_Q), sK = ptx::smem_u32(smem + C::OFF_K), sV = ptx::smem_u32(smem + C::OFF_V),
                    sF = ptx::smem_u32(smem + C::OFF_F);
     if (tid < 128) reinterpret_cast<unsigned long long *>(misc + C::OFF_M)[tid] = 0;
@@ -878,8 +931,8 @@ __global__ void __launch_bounds__(kScThreads, 1)
         bool ok = true;
         while (ok && next_unit()) {
             const int nt = max(0, u.t1 - u.t0), even = nt + 1 & ~1;
-            const uint32_t nx = un - 1;  // (the unit that had this flag has written its output: its place is free)
-            if (lane == 0) nan_flag[(nx % kScUnits) * 4 + wid] = 0;
+            const uint32_t nx = un - 1;  // (the unit that had this word has written its output: its place is free)
+            if (lane == 0) nan_tiles[(nx % kScUnits) * 4 + wid] = 0;
             __syncwarp();
             for (int t = (wid - g) & (C::WIDE - 1); t < even; t += C::WIDE) {
                 const int at = g + t, fs = at % C::STF, k = (u.t1 - 1 - t) * kScTile;
@@ -895,6 +948,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
                 const int piece = lane % NP, key0 = lane / NP;
                 const int sw = C::CF == 128 ? key0 & 7 : (key0 >> 1) & 3;  // KP is a multiple of 8
                 static_assert(KP % 8 == 0 && kScTile % KP == 0, "passes");
+                bool found = false;
 #pragma unroll 1
                 for (int key = t < nt ? key0 + part * KP : kScTile; key < kScTile; key += KP * (4 / C::WIDE)) {
                     // lanes of odd keys take the chunks in another order where that spreads the banks
@@ -914,7 +968,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
                                 any |= bad;
                                 w[x].w[e] &= ~((bad >> 7) * 0xffu);
                             }
-                        if (any && k + key >= u.slo && k + key < u.shi) nan_flag[(nx % kScUnits) * 4 + wid] = 1;
+                        found |= any && k + key >= u.slo && k + key < u.shi;
                     }
 #pragma unroll
                     for (int x = 0; x < C::NCF; ++x) {
@@ -927,6 +981,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
                         ptx::st_shared_v4(row + (((2 * piece + 1) ^ sw) << 4), h[4], h[5], h[6], h[7]);
                     }
                 }
+                if (partial && __any_sync(0xffffffffu, found) && lane == 0) nan_tiles[(nx % kScUnits) * 4 + wid] |= 1ull << (t & 63);
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
@@ -984,7 +1039,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
             }
             bool nan = false;
 #pragma unroll
-            for (int w = 0; w < 4; ++w) nan |= nan_flag[(un % kScUnits) * 4 + w] != 0;
+            for (int w = 0; w < 4; ++w) nan |= nan_tiles[(un % kScUnits) * 4 + w] != 0;
             auto read = [&]() {  // O has been read: the next unit's products may go on
                 ptx::tc_fence_before();
                 __syncwarp();
@@ -994,7 +1049,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
             if (u.slot >= 0) part = reinterpret_cast<float4 *>(p.part) + (long long)u.slot * 128 * (DV / 4) + r;
             // small loops: code that runs once a unit is fetched anew each time (64 columns unrolled, a division and log2f before:
             // 7200 cycles from the last product to the end of O's read, for which the next unit's products wait)
-            const bool plain = any && !part && !nan;
+            const bool plain = any && !part;
             if (plain) {
 #pragma unroll 1
                 for (int x = 0; x < DV; x += 32) {
@@ -1040,12 +1095,6 @@ __global__ void __launch_bounds__(kScThreads, 1)
                     ptx::reg_fence16(v);
                     if (x + 16 == DV) read();
                 }
-                if (nan && row_ok) {
-                    const uint32_t bad = sc_nan32(p, u.b, u.rq, row, u.kvh, u.t0 * kScTile, u.t1 * kScTile, x & ~31) >> (x & 16);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        if (bad >> e & 1u) v[e] = 0x7fffffffu;
-                }
                 if (part && row_ok) {
 #pragma unroll
                     for (int e = 0; e < 16; e += 4)
@@ -1059,6 +1108,7 @@ __global__ void __launch_bounds__(kScThreads, 1)
                 }
                 __syncwarp();
             }
+            if (any && nan) sc_put_nans<C, DV>(p, misc, un, r);
             release_unit(un);
             ++un;
         }
@@ -1193,16 +1243,19 @@ __global__ void __launch_bounds__(kScThreads, 1)
                 bool moved = __any_sync(0xffffffffu, mx > m + (kScBias + kScSlack));
                 if (BIAS && !prep && (moved || k == 0)) {  // the bound is not enough: the largest with each key's bias
                     mx = -INFINITY;
+                    constexpr int N = CAP ? 8 : 16;  // columns a time (the prompts, 16 with a cap: 332 us beside 308; 8 without: 231 beside 224)
 #pragma unroll 1
-                    for (int h = 0; h < 4; ++h) {
-                        uint32_t v[16];
-                        ptx::tmem_ld16(scol + 16 * h, v);
+                    for (int h = 0; h < kScTile; h += N) {
+                        uint32_t v[N];
+                        if constexpr (CAP) ptx::tmem_ld8(scol + h, v);
+                        else ptx::tmem_ld16(scol + h, v);
                         ptx::tmem_wait_ld();
-                        ptx::reg_fence16(v);
+                        if constexpr (CAP) ptx::reg_fence8(v);
+                        else ptx::reg_fence16(v);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
+                        for (int e = 0; e < N; ++e) {
                             const float z = CAP ? sc_cap_near(u2f(v[e]), k2, cap) : u2f(v[e]) * c;
-                            mx = fmaxf(mx, fmaf(slope, (float)(k0 + 16 * h + e - pc), z));
+                            mx = fmaxf(mx, fmaf(slope, (float)(k0 + h + e - pc), z));
                         }
                     }
                     if (!row_ok) mx = -INFINITY;

@@ -124,3 +124,66 @@ def test_a_tiny_cap_under_a_huge_scale(m):
     p = R.Problem([300, 40], [m] * 2, Hq=4, Hkv=1, D=64, DV=64, seed=3)
     p.q.view(torch.uint8)[:, :, 1] = 0
     R.check(p, call(p, softcap=1e-30, softmax_scale=1e12, causal=True), R.attend(p, cap=1e-30, scale=1e12, causal=True), B16)
+
+
+# ------------------------------------------------------------------ NaN values that some tokens see
+def nan_problem(keys, m, D, DV, seed, at, **kw):
+    p = R.Problem([keys], [m], Hq=4, Hkv=1, D=D, DV=DV, seed=seed, **kw)
+    for j, c in at:
+        p.vl[0].view(torch.uint8)[j, 0, c] = 0x7F if c % 2 else 0xFF
+    p.lay_out()
+    return p
+
+
+@pytest.mark.parametrize("D,DV", [(64, 64), (96, 96), (128, 128), (192, 128), (192, 192), (256, 256)])
+@pytest.mark.parametrize("m,packed", [(1, False), (4, False), (60, False), (60, True), (300, False)])
+def test_nan_values_reach_those_that_see_them(D, DV, m, packed):
+    """In one tile and in several, alone and many, in gaps that no token sees, in every 16 channels."""
+    n = 2600
+    at = [(2, 0), (70, 1), (71, DV - 1), (700, 17), (1300, 33), (2590, 5)] + [(1400 + j, j % DV) for j in range(90)] + [(1900, c) for c in range(DV)]
+    p = nan_problem(n, m, D, DV, m, at, packed=packed)
+    r = torch.tensor([[(37 * i) % 1500, n - (53 * i) % 1500] if i % 5 else [0, 72 * (i % 2)] for i in range(m)], dtype=torch.int32)
+    for kw in (dict(ranges=r if packed else r[None]), dict(ranges=(r + 60) if packed else (r + 60)[None], causal=True), dict(causal=True, window=800)):
+        want = R.attend(p, cap=4.0, **kw)
+        kw["window_left"] = kw.pop("window", -1)
+        R.check(p, call(p, softcap=4.0, **kw), want, B16)
+    rows = torch.rand((m, m), generator=p.g) < 0.3
+    p.vl[0].view(torch.uint8)[n - m + m // 2, 0, 9] = 0x7F
+    p.lay_out()
+    words = -(-m // 32)
+    masks = R.pack(rows, words) if packed else R.pack(rows, words)[None]
+    R.check(p, fa8.fwd_tree(p.q.cuda(), p.k.cuda(), p.v.cuda(), masks.cuda(), **p.kw()), R.attend(p, rows=[rows]), B16)
+
+
+def time_of(f):
+    f()
+    times = []
+    for _ in range(5):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        f()
+        b.record()
+        b.synchronize()
+        times.append(a.elapsed_time(b))
+    return sorted(times)[2]
+
+
+@pytest.mark.parametrize("m,packed", [(1, False), (4, False), (60, False), (60, True)])
+def test_a_nan_value_in_a_long_request_costs_little(m, packed):
+    """One NaN among the values of a request whose keys some tokens see and others do not."""
+    n, D = 60000, 256
+    g = torch.Generator(device="cuda").manual_seed(0)
+    q = torch.randn((m, 4, D) if packed else (1, m, 4, D), generator=g, device="cuda").to(R.E4M3)
+    k, v = (torch.randn((n, 1, D), generator=g, device="cuda").to(R.E4M3) for _ in range(2))
+    ranges = torch.tensor([[0, n] if i % 2 else [n // 3, n // 3 + 7] for i in range(m)], dtype=torch.int32, device="cuda")
+    cu_k = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    kw = dict(ranges=ranges if packed else ranges[None], cu_seqlens_k=cu_k)
+    if packed:
+        kw["cu_seqlens_q"] = torch.tensor([0, m], dtype=torch.int32, device="cuda")
+    clean = time_of(lambda: fa8.fwd_scored(q, k, v, **kw))
+    for j in (n // 3 + 3, n // 2):
+        v.view(torch.uint8)[j, 0, 100] = 0x7F
+    with_nan = time_of(lambda: fa8.fwd_scored(q, k, v, **kw))
+    out = fa8.fwd_scored(q, k, v, **kw)[0].view(m, 4, D)
+    assert bool(out[..., 100].isnan().all()) and not bool(out[..., :100].isnan().any()) and not bool(out[..., 101:].isnan().any())
+    assert with_nan < 3 * clean + 0.1, f"{clean:.3f} ms, with a NaN {with_nan:.3f} ms"
