@@ -136,12 +136,12 @@ __global__ void __launch_bounds__(kKeepThreads) keep_tokens_kernel(const __grid_
     constexpr int ROWS = kKeepThreads / CB;
     auto taken = [&](int s) -> int {  // the token for slot s, or -1
         const int i = kept[s];
-        if (i < 0 || i == s) return -1;
+        if (i < 0) return -1;
         if (i >= Lq || s >= Lq) {
             if (tid % CB == 0) atomicOr(p.status, kStatusBounds);
             return -1;
         }
-        return i;
+        return i == s ? -1 : i;
     };
     for (int s = tid / CB; s < p.N; s += ROWS) {
         const int i = taken(s);

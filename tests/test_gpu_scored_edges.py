@@ -187,3 +187,19 @@ def test_a_nan_value_in_a_long_request_costs_little(m, packed):
     out = fa8.fwd_scored(q, k, v, **kw)[0].view(m, 4, D)
     assert bool(out[..., 100].isnan().all()) and not bool(out[..., :100].isnan().any()) and not bool(out[..., 101:].isnan().any())
     assert with_nan < 3 * clean + 0.1, f"{clean:.3f} ms, with a NaN {with_nan:.3f} ms"
+
+
+# ------------------------------------------------------------------ slots past the drafted tokens
+@pytest.mark.parametrize("layout", ["paged", "varlen", "dense"])
+def test_a_kept_slot_past_the_drafted_tokens_is_reported(layout):
+    """Even one that would keep its own."""
+    p = R.Problem([40, 40], [4, 4], Hq=2, Hkv=2, D=64, DV=64, layout=layout, seed=3)
+    k, v = p.k.cuda(), p.v.cuda()
+    kw = {n: x for n, x in p.kw().items() if not n.startswith("descale")}
+    kept = torch.tensor([[0, 1, 2, 3], [0, 1, -1, 3]], dtype=torch.int32, device="cuda")
+    fa8.keep_tokens(k, v, kept, new_tokens=4, **kw)
+    assert fa8.check() == fa8.FA8_SUCCESS
+    kept = torch.tensor([[0, 1, 2, 3, -1], [0, 1, -1, 3, 4]], dtype=torch.int32, device="cuda")
+    fa8.keep_tokens(k, v, kept, new_tokens=4, **kw)
+    assert fa8.check() == fa8.FA8_ERR_DEVICE_BOUNDS
+    assert torch.equal(k.view(torch.uint8).cpu(), p.k.view(torch.uint8)) and torch.equal(v.view(torch.uint8).cpu(), p.v.view(torch.uint8))
