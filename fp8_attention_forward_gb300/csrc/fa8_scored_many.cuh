@@ -115,7 +115,7 @@ __device__ __forceinline__ bool sc_slot(const int *cu_q, int B, int P, int x, in
         int cnt = 0;
         if (s < B) {
             const int len = cu_q[s + 1] - cu_q[s];
-            cnt = len > 0 ? (len + P - 1) / P : 0;
+            cnt = len > 0 ? (len - 1) / P + 1 : 0;
         }
         int inc = cnt;
 #pragma unroll

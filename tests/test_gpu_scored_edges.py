@@ -203,3 +203,14 @@ def test_a_kept_slot_past_the_drafted_tokens_is_reported(layout):
     fa8.keep_tokens(k, v, kept, new_tokens=4, **kw)
     assert fa8.check() == fa8.FA8_ERR_DEVICE_BOUNDS
     assert torch.equal(k.view(torch.uint8).cpu(), p.k.view(torch.uint8)) and torch.equal(v.view(torch.uint8).cpu(), p.v.view(torch.uint8))
+
+
+# ------------------------------------------------------------------ lengths near 2^31
+def test_a_length_near_2_31_is_reported():
+    """A packed request that claims more tokens than there are, by so much that its blocks of rows pass 32 bits."""
+    p = R.Problem([300], [20], Hq=4, Hkv=1, packed=True, seed=2)
+    kw = dict(p.kw(), cu_seqlens_q=torch.tensor([0, 2 ** 31 - 1], dtype=torch.int32, device="cuda"))
+    out = torch.full((20, 4, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    fa8.fwd_scored(p.q.cuda(), p.k.cuda(), p.v.cuda(), out=out, **kw)
+    assert fa8.check() == fa8.FA8_ERR_DEVICE_BOUNDS
+    assert bool((out == 7.0).all())
