@@ -207,7 +207,8 @@ extern "C" fa8_status fa8_tree_masks(const fa8_tensor *parents, fa8_tensor *mask
         return st;
     const long long words = masks->shape[masks->ndim - 1];
     if (words > fa8::kMaxTreeWords) return fail(FA8_ERR_UNSUPPORTED, "%lld words per mask, at most %d are supported", words, fa8::kMaxTreeWords);
-    if (!cu_seqlens_q && words * 32 < p.Sq) return fail(FA8_ERR_INVALID_ARG, "masks of %lld words do not hold %d tokens", words, p.Sq);
+    if ((!cu_seqlens_q && words * 32 < p.Sq) || (words == 0 && T > 0))
+        return fail(FA8_ERR_INVALID_ARG, "masks of %lld words do not hold %lld tokens", words, cu_seqlens_q ? T : p.Sq);
     if (positions) {
         if ((st = check_tokens(positions, "positions", (int)B, p.Sq, (int)T, cu_seqlens_q, false, p.o_s)) || (st = check_written(positions, "positions")))
             return st;
@@ -217,7 +218,7 @@ extern "C" fa8_status fa8_tree_masks(const fa8_tensor *parents, fa8_tensor *mask
         if ((st = check_int_vec(cu_seqlens_k, "cu_seqlens_k", B + 1))) return st;
         p.cu_k = static_cast<const int *>(cu_seqlens_k->data);
     }
-    if (T == 0 || words == 0) return FA8_SUCCESS;
+    if (T == 0) return FA8_SUCCESS;
     if (!parents->data || !masks->data || (positions && !positions->data)) return fail(FA8_ERR_INVALID_ARG, "parents, masks and positions need data");
     DeviceState *ds = nullptr;
     if ((st = device_state(&ds))) return st;

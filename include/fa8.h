@@ -376,7 +376,7 @@ FA8_API fa8_status fa8_fwd_tree(const fa8_tensor *q, const fa8_tensor *k, const 
  *   parents: int32 (B, Sq) or (total_q) with cu_seqlens_q: index among the request's drafted tokens, below the
  *     token's own; negative: it follows the text before the tree.  (Others raise FA8_ERR_DEVICE_BOUNDS and count
  *     as negative.)
- *   masks: int32 (B, Sq, words) or (total_q, words), last dim contiguous, at most 128 words.  A packed request
+ *   masks: int32 (B, Sq, words) or (total_q, words), last dim contiguous, 1 to 128 words.  A packed request
  *     of more than 32 * words tokens raises FA8_ERR_DEVICE_BOUNDS; its tokens behind those get empty masks.
  *   positions: int32, the parents' shape: Lk - Lq + depth, the number of ancestors (0 where that is below
  *     0), as fa8_rope_append takes them; without cu_seqlens_k the depth alone.  NULL = not wanted.
