@@ -462,15 +462,20 @@ def _scored(name, stream, tensors, out, lse, placed, args, workspace, out_dtype,
 
             both = (ctypes.cast(getattr(lib(), x), ctypes.c_void_p).value for x in (name, "fa8_fwd_scored_workspace_size"))
             fn = _entries[name] = functools.partial(getattr(module, name), *both)
-        if stream is None and _current_device() == index:
-            status, out, lse = fn(*tensors, out, lse, *placed, *args, workspace, _DTYPES[out_dtype], return_lse, _raw_stream(index))
-        else:
-            handle = _raw_stream(index) if stream is None else stream.cuda_stream
-            with torch.cuda.stream(stream), torch.cuda.device(index):
-                status, out, lse = fn(*tensors, out, lse, *placed, *args, workspace, _DTYPES[out_dtype], return_lse, handle)
-        if status:
-            _raise(status)
-        return out, lse
+        got = None
+        try:
+            if stream is None and _current_device() == index:
+                got = fn(*tensors, out, lse, *placed, *args, workspace, _DTYPES[out_dtype], return_lse, _raw_stream(index))
+            else:
+                handle = _raw_stream(index) if stream is None else stream.cuda_stream
+                with torch.cuda.stream(stream), torch.cuda.device(index):
+                    got = fn(*tensors, out, lse, *placed, *args, workspace, _DTYPES[out_dtype], return_lse, handle)
+        except RuntimeError:
+            pass  # torch raises its own error below, e.g. OutOfMemoryError
+        if got is not None:
+            if got[0]:
+                _raise(got[0])
+            return got[1:]
     if out is None:
         out = _beside(stream, _empty, q, out_dtype, 1, v.shape[-1])
     if lse is None and return_lse:
@@ -528,10 +533,15 @@ def tree_masks(parents, *, cu_seqlens_k=None, cu_seqlens_q=None, max_tokens=None
     index = parents.get_device()
     if stream is None and index >= 0 and _module() is not None and _current_device() == index:
         fn = _entries.get("fa8_tree_masks") or _entry("fa8_tree_masks")
-        status, masks, positions = fn(parents, masks, positions, cu_seqlens_q, cu_seqlens_k, words, _raw_stream(index))
-        if status:
-            _raise(status)
-        return masks, positions
+        got = None
+        try:
+            got = fn(parents, masks, positions, cu_seqlens_q, cu_seqlens_k, words, _raw_stream(index))
+        except RuntimeError:
+            pass  # torch raises its own error below, e.g. OutOfMemoryError
+        if got is not None:
+            if got[0]:
+                _raise(got[0])
+            return got[1:]
     if masks is None:
         masks = _beside(stream, _empty, parents, torch.int32, 0, words)
     if positions is None:

@@ -214,3 +214,14 @@ def test_a_length_near_2_31_is_reported():
     fa8.fwd_scored(p.q.cuda(), p.k.cuda(), p.v.cuda(), out=out, **kw)
     assert fa8.check() == fa8.FA8_ERR_DEVICE_BOUNDS
     assert bool((out == 7.0).all())
+
+
+# ------------------------------------------------------------------ outputs that do not fit
+def test_outputs_that_do_not_fit_raise_torchs_error():
+    """Outputs of petabytes (of an expanded q): torch's OutOfMemoryError, which callers catch to free memory."""
+    q = torch.zeros((1, 1, 1, 64), dtype=torch.uint8, device="cuda").view(R.E4M3).expand(1 << 20, 1 << 20, 128, 64)
+    k = torch.zeros((1, 64, 1, 64), dtype=torch.uint8, device="cuda").view(R.E4M3)
+    parents = torch.zeros((1, 1), dtype=torch.int32, device="cuda").expand(1 << 24, 1 << 14)
+    for f in (lambda: fa8.fwd_scored(q, k, k), lambda: fa8.fwd_tree(q, k, k, parents), lambda: fa8.tree_masks(parents)):
+        with pytest.raises(torch.OutOfMemoryError):
+            f()
