@@ -225,3 +225,39 @@ def test_outputs_that_do_not_fit_raise_torchs_error():
     for f in (lambda: fa8.fwd_scored(q, k, k), lambda: fa8.fwd_tree(q, k, k, parents), lambda: fa8.tree_masks(parents)):
         with pytest.raises(torch.OutOfMemoryError):
             f()
+
+
+# ------------------------------------------------------------------ far keys
+@pytest.mark.parametrize("m", [1, 4, 60])
+@pytest.mark.parametrize("packed", [False, True])
+def test_ranges_a_million_keys_before_the_token(m, packed):
+    """Only the distances of a range's keys from one another weigh: O is that of the same keys near the token, the LSE less by the
+    slope times the positions between."""
+    n, small, ps = 1_000_000, 300, 64
+    p = R.Problem([small], [m], Hq=4, Hkv=1, D=64, DV=64, ps=ps, packed=packed, seed=5)
+    slopes, r = torch.tensor([1.0, 8.0, 0.3, 0.0]), torch.tensor([[100, 230]] * m, dtype=torch.int32)
+    r = r if packed else r[None]
+    o, lse, mag, err = want = R.attend(p, slopes=slopes, ranges=r)
+    kw = p.kw()
+    used = -(-small // ps)
+    table = torch.full((1, -(-n // ps)), int(p.bt[0, 0]), dtype=torch.int32)  # the pages behind the range are one and the same
+    table[0, :used] = p.bt[0, :used]
+    kw.update(block_table=table.cuda(), cu_seqlens_k=torch.tensor([0, n], dtype=torch.int32, device="cuda"))
+    got = fa8.fwd_scored(p.q.cuda(), p.k.cuda(), p.v.cuda(), slopes=slopes.cuda(), ranges=r.cuda(), **kw)
+    R.check(p, (got[0], lse), want, B16)
+    away = (slopes.double() * (n - small)).view(*([-1, 1] if packed else [1, -1, 1]))
+    # a product and a sum of fp32, and the LSE's own rounding
+    assert ((got[1].double().cpu() - (lse - away)).abs() <= err + 2.0 ** -20 + away * 2.0 ** -22).all()
+
+
+@pytest.mark.parametrize("D,DV", [(64, 64), (128, 128), (256, 256)])
+@pytest.mark.parametrize("new,keys", [([1, 1, 1], [9000, 130, 4097]), ([1, 5, 200, 0, 16], [5000, 8200, 700, 40, 3001])])
+def test_packed_requests_over_longer_keys(D, DV, new, keys):
+    """Decode steps, chunks and trees of unequal size in one batch."""
+    p = R.Problem(keys, new, Hq=8, Hkv=2, D=D, DV=DV, packed=True, tail=2, seed=D)
+    for cap, slopes, kw in ((4.0, None, dict(causal=True)), (0.0, slopes_of(8), dict(causal=True, window=3000))):
+        want = R.attend(p, cap=cap, slopes=slopes, **kw)
+        R.check(p, call(p, softcap=cap, slopes=slopes, causal=True, window_left=kw.get("window", -1)), want, B16)
+    rows = [R.tree_rows(R.tree(m, m))[0] for m in new]
+    masks = torch.cat([R.pack(r, 7) for r in rows] + [torch.full((2, 7), -1, dtype=torch.int32)])
+    R.check(p, fa8.fwd_tree(p.q.cuda(), p.k.cuda(), p.v.cuda(), masks.cuda(), **p.kw()), R.attend(p, rows=rows), B16)
