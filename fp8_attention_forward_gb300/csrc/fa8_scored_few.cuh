@@ -9,9 +9,9 @@
 // are the request's tokens x the q-heads of one kv-head, so a chunk can be visible to some of them
 // alone: chunks inside every row's range take no mask.
 //
-// Measured (us; capped, d = 128, 16-key pages): 64 requests of 1024 .. 32768 keys, 64 q-heads on 8 361 (2.2 GB, 6.1 TB/s
-// of 6.8 that a copy gets), 32 of 4096 keys 56, one of 4096 10 (a chain of dependent loads: lengths, table, keys, then
-// the merge), of 131072 51.  From 9 rows on each K and V fragment feeds two MMAs, and from 2 x 8 rows the MMAs and
+// Measured (us; capped, d = 128, 16-key pages): 64 requests of 1024 .. 32768 keys, 64 q-heads on 8 362 to 375, as the box is
+// (2.2 GB, 5.9 to 6.1 TB/s of 6.8 that a copy gets), 32 of 4096 keys 58, one of 4096 11 (a chain of dependent loads: lengths,
+// table, keys, then the merge), of 131072 52.  From 9 rows on each K and V fragment feeds two MMAs, and from 2 x 8 rows the MMAs and
 // conversions, not the memory, bound it.
 #pragma once
 
@@ -27,7 +27,10 @@
 namespace fa8 {
 
 constexpr int kFewMaxCluster = 16;
-constexpr float kFewBias = 7.f, kFewSlack = 8.f;  // as kScBias and kScSlack
+// P is taken against 2^kFewBias below the row's maximum, which moves only for scores 2^kFewSlack above it: p <= 2^15 stays in
+// f16's range, and a weight down to 2^-32 of the largest still counts in P V (of the kernel for many rows, whose slack is
+// wider since it pays more for a move, 2^-28), every one in the sum.
+constexpr float kFewBias = 7.f, kFewSlack = 8.f;
 
 template <int D, int DV, int NT, int PW>
 struct FewCfg {

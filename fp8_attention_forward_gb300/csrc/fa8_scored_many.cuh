@@ -17,8 +17,8 @@
 // 372 us, of 16 302).
 //
 // Measured (us; two causal prompts of 4096, 32 q-heads on 8, d = 128, 275 GFLOP): no change of scores 207 (1330 TFLOP/s;
-// fa8_fwd 296), capped 289, sloped 220, both 278; d = 64 181, sloped 193; 16 on 4, d = 192 / 128 127, 256 189.  At 207 the
-// tensor pipe is busy 41 % of the time, the issue slots 63 %, the exponentials' unit 28 %; capped, that unit 45 %.
+// fa8_fwd 298), capped 293, sloped 225, both 284; d = 64 185, sloped 193; 16 on 4, d = 192 / 128 127, 256 194.  At 207 the
+// tensor pipe is busy 41 % of the time, the issue slots 64 %, the exponentials' unit 28 %; capped, that unit 45 %.
 //
 // Warpgroups (896 threads):
 //   0-3   softmax, thread = row: tiles 0, 1, 2, 3 (mod 4)
@@ -45,7 +45,8 @@ constexpr int kScUnits = 3;  // units between the warp that works them out and t
 
 constexpr int kScGroups = 4;             // warpgroups of softmax
 constexpr int kScOut = 4 * kScGroups, kScConv = kScOut + 4, kScCtl = kScConv + 4, kScThreads = 32 * (kScCtl + 4);  // first warps
-// registers per thread: at launch, then of the softmax, output, widening and control warpgroups (none spills)
+// registers per thread: at launch, then of the softmax, output, widening and control warpgroups (d = 256
+// spills 8 to 12 bytes, 192 with slopes 8, the others nothing)
 constexpr int kScRegs = 72, kScRegsS = 72, kScRegsO = 96, kScRegsV = 56, kScRegsC = 64;
 static_assert(kScGroups * kScRegsS + kScRegsO + kScRegsV + kScRegsC <= (kScGroups + 3) * kScRegs && kScThreads * kScRegs <= 65536, "registers");
 static_assert(kScRegsS == kScRegs && kScRegsO >= kScRegs && kScRegsV <= kScRegs && kScRegsC <= kScRegs, "taken or given");
@@ -409,8 +410,8 @@ __device__ __forceinline__ void sc_p16(const uint32_t (&u)[16], uint64_t c2, uin
         w[e / 2 + 1] = cvt_f16x2_sat(e3, e2);
     }
 }
-// The tile's P over its scores, 16 columns at a time with the next in flight: a rolled loop, whose code stays
-// small (instruction fetch is what a longer one waits for).  d: the first key less the one whose bias is zero.
+// The tile's P over its scores, 16 columns at a time, each loaded when the ones before are done with: a rolled loop, whose code
+// stays small (instruction fetch is what a longer one waits for).  d: the first key less the one whose bias is zero.
 template <int HOW>
 __device__ __forceinline__ void sc_p64(uint32_t scol, float c, float ref, float k2, float cap, float slope, int d, uint64_t &l2) {
     constexpr bool kCap = HOW == kScCap || HOW == kScCapBiased, kBias = HOW >= kScBiased;

@@ -321,6 +321,9 @@ FA8_API fa8_status fa8_fwd_pages(const fa8_tensor *q, const fa8_tensor *k, const
  * page_size are fa8_fwd's, with its head dims and bounds checks, and the shared conventions above hold but
  * that a call may need a workspace and a second kernel.  Weights go into the product with V as f16, at 2^-11
  * of themselves, or 2^-28 of the row's largest where that is more; the sum that divides them is of fp32.  What K and V hold where a token sees no key of theirs does not matter, NaNs included.
+ * Packed queries (cu_seqlens_q) always go in units of 128 rows of a request, each walked through its keys by one CTA: few packed
+ * tokens on long keys take several times what the same tokens take batched, padded if need be (one token on 131072 keys:
+ * 1072 us, batched 53).
  * ------------------------------------------------------------------------------------ */
 
 /*
