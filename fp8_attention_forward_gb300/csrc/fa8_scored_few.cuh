@@ -9,7 +9,7 @@
 // are the request's tokens x the q-heads of one kv-head, so a chunk can be visible to some of them
 // alone: chunks inside every row's range take no mask.
 //
-// Measured (us; capped, d = 128, 16-key pages): 64 requests of 1024 .. 32768 keys, 64 q-heads on 8 362 to 375, as the box is
+// Measured (us; capped, d = 128, 16-key pages): 64 requests of 1024 .. 32768 keys, 64 q-heads on 8 362 to 375, from run to run
 // (2.2 GB, 5.9 to 6.1 TB/s of 6.8 that a copy gets), 32 of 4096 keys 58, one of 4096 11 (a chain of dependent loads: lengths,
 // table, keys, then the merge), of 131072 52.  From 9 rows on each K and V fragment feeds two MMAs, and from 2 x 8 rows the MMAs and
 // conversions, not the memory, bound it.
