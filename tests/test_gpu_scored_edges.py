@@ -117,6 +117,34 @@ def test_caps_far_above_the_scores(cap, m, scale, bias):
     R.check(p, call(p, softcap=cap, slopes=slopes, softmax_scale=scale, causal=True), (o, lse, mag, err), B16)
 
 
+@pytest.mark.parametrize("D,DV", [(64, 64), (96, 96), (128, 128), (192, 128), (192, 192), (256, 256)])
+@pytest.mark.parametrize("m,Hq", [(1, 6), (70, 6), (70, 8)])
+@pytest.mark.parametrize("bias", [False, True])
+def test_large_caps_at_every_head_dim(D, DV, m, Hq, bias):
+    """With ranges, NaN values, negative descales and trees; the error of a score as above, which stays far under 2^-20 of the cap."""
+    p = R.Problem([300, 700], [m] * 2, Hq=Hq, Hkv=2, D=D, DV=DV, seed=D + m, scale=2.0, fill=0x7F)
+    p.vl[1].view(torch.uint8)[650, 1, 7] = 0x7F
+    p.dq[0, 0] = -2.0
+    p.lay_out()
+    slopes = slopes_of(Hq) if bias else None
+    ranges = torch.tensor([[[3 * i, n - 40 + i] if i % 7 else [n, n] for i in range(m)] for n in p.keys], dtype=torch.int32)
+    for kw in (dict(causal=True), dict(ranges=ranges), dict(causal=True, window=90)):
+        o, lse, mag, _ = R.attend(p, cap=1000.0, slopes=slopes, **kw)
+        err = R.attend(p, slopes=slopes, **kw)[3]
+        for b in range(2):
+            k = p.kl[b].double().repeat_interleave(p.G, 1)
+            f = (p.dq[b] * p.dk[b]).double().repeat_interleave(p.G)[:, None] / math.sqrt(D)
+            err[b] += 2.0 ** -20 * torch.einsum("ihd,jhd->hij", p.q[b].double(), k).abs().amax(-1) * f.abs()
+        kw["window_left"] = kw.pop("window", -1)
+        R.check(p, call(p, softcap=1000.0, slopes=slopes, **kw), (o, lse, mag, err), B16)
+    if not bias:
+        rows = [R.tree_rows(R.tree(m, b))[0] for b in range(2)]
+        masks = torch.stack([R.pack(r, -(-m // 32)) for r in rows])
+        got = fa8.fwd_tree(p.q.cuda(), p.k.cuda(), p.v.cuda(), masks.cuda(), softcap=1e6, **p.kw())
+        o, lse, mag, _ = R.attend(p, cap=1e6, rows=rows)
+        R.check(p, got, (o, lse, mag, err), B16)
+
+
 # ------------------------------------------------------------------ tiny caps
 @pytest.mark.parametrize("m", [1, 40])
 def test_a_tiny_cap_under_a_huge_scale(m):
